@@ -33,6 +33,11 @@
  *  - Device work is issued on the context stream (moe_config.stream; NULL is
  *    the device's null stream) in call order.
  *
+ *  - The operators beside the experts (moe_add_rmsnorm, moe_q4_*,
+ *    moe_router_balance*) have no context: they take the device and the
+ *    stream, keep nothing between calls, and leave the message of a failing
+ *    call in moe_last_error(NULL) of the calling thread.
+ *
  * Weight format (MOE_Q4_32_F16): each matrix row is a run of 18-byte blocks
  * along the reduction axis; a block is a little-endian IEEE fp16 scale d
  * followed by 16 bytes qs; element j (0..15) of the block is qs[j] & 0xF and
@@ -67,7 +72,16 @@ extern "C" {
 
 #define MOE_Q4_32_F16     1   /* the only weight format */
 
-#define MOE_ACCUMULATE    1u  /* moe_forward / moe_prefill: y += result      */
+#define MOE_ACCUMULATE    1u  /* moe_forward / moe_prefill / moe_q4_matmul:
+                                 y += result; also of moe_router_balance's
+                                 counts and moe_router_balance_grad's dlogits */
+
+/* Value types of the tensors of the operators beside the experts. */
+#define MOE_F32           0
+#define MOE_F16           1
+#define MOE_BF16          2
+#define MOE_Q8_32         3   /* int8 codes and an fp32 scale for each run of 32
+                                 values along the row: value = scale * code  */
 
 #define MOE_MAX_SWAP_LEAD 8   /* largest moe_config.swap_lead                 */
 
@@ -444,7 +458,106 @@ MOE_API int moe_get_miss_log(moe_ctx* ctx, uint64_t* out, int64_t cap, int64_t* 
 /* uint32 [L][E]: picks per expert since the last seed (moe_forward only). */
 MOE_API int moe_get_counts(moe_ctx* ctx, uint32_t* out);
 
-MOE_API const char* moe_last_error(moe_ctx* ctx);  /* ctx NULL: the last failed moe_create of this thread */
+/* ctx NULL: this thread's last failed moe_create or call without a context */
+MOE_API const char* moe_last_error(moe_ctx* ctx);
+
+/* ---------------------------------------------------------------------------
+ * Operators beside the experts: what a layer computes around moe_forward.
+ * They need no context. Common to all:
+ *  - `device` is the HIP device of every pointer and of `stream` (a
+ *    hipStream_t, NULL the null stream); it need not be the current one.
+ *  - Work is issued on `stream` and not waited for; nothing is allocated; each
+ *    call may be captured into a HIP graph. Results depend on the inputs only
+ *    (no atomics on values): equal calls give equal bits.
+ *  - Rows may be strided: *_stride is the distance of two rows in values, at
+ *    least the row length. Values of a row are contiguous and aligned to their
+ *    size. What lies between and behind the rows is neither read nor written.
+ *  - Outputs may not overlap inputs or each other unless said so.
+ *  - n_tokens is 0..2^24 (0: nothing is written but what a call says).
+ *  - MOE_E_INVAL on a bad size, type, stride, null pointer, alignment or too
+ *    small a workspace, before any work is issued; MOE_E_HIP if a launch fails.
+ */
+
+/* Residual add and RMS norm, the input of the experts and dense products:
+ *   s = x + residual                          (fp32; s = x without a residual)
+ *   residual_out = s                          (rounded to res_type)
+ *   v = s * weight / sqrt(mean(s^2) + eps)    (from the unrounded s; weight
+ *                                             fp32 [hidden], NULL: all ones)
+ *   out = v rounded to out_type, or with MOE_Q8_32, for each 32 values:
+ *         a = max |v|, scale = a / 127, code = v * (127 / a) to nearest even;
+ *         a below 2^-100: scale 0 and codes 0; a not finite: scale NaN, codes 0.
+ * hidden is 1..2^24, with MOE_Q8_32 a multiple of 32. x_type and res_type are
+ * MOE_F32, MOE_F16 or MOE_BF16. residual and residual_out may be the same
+ * (update in place) and NULL together; out may be x when type and stride are
+ * the same. scales (fp32 [n_tokens][hidden/32]) belongs to MOE_Q8_32 and is
+ * NULL otherwise. eps >= 0. */
+MOE_API int moe_add_rmsnorm(int32_t device, void* stream, int32_t n_tokens, int32_t hidden,
+                            int32_t x_type, const void* x, int64_t x_stride,
+                            int32_t res_type, const void* residual, int64_t res_stride,
+                            void* residual_out, int64_t res_out_stride, const float* weight, float eps,
+                            int32_t out_type, void* out, int64_t out_stride, float* scales, int64_t scales_stride);
+
+/* Split canonical MOE_Q4_32_F16 blocks (host, [rows][k/32] of 18 bytes) into
+ * the two planes moe_q4_matmul reads, as the pool keeps an expert's matrix:
+ * nibbles uint8 [rows][k/32][16] and scales fp16 [rows][k/32] (host). */
+MOE_API int moe_q4_split(int32_t rows, int32_t k, const void* blocks, void* nibbles, void* scales);
+
+/* Dense product with 4-bit weights (attention projections, shared experts,
+ * output head) for any number of tokens:
+ *   y[t][n] (=|+=) sum_b d[n][b] * sum_{j<32} (q[n][b][j] - 8) * x[t][32 b + j]
+ * nibbles and w_scales are the planes of moe_q4_split in device memory,
+ * contiguous, 16-byte aligned. x_type MOE_F32, MOE_F16, MOE_BF16, or MOE_Q8_32
+ * with x_scales fp32 [n_tokens][k/32] (x = scale * code); y_type MOE_F32,
+ * MOE_F16 or MOE_BF16. n_out >= 1, k a multiple of 32, 32..2^20.
+ * Weights and activations enter the products unrounded (MOE_Q8_32: scale *
+ * code rounded to fp32) and sums are fp32; y is rounded once. |x| up to 2^115;
+ * a token with a value that is not finite gives NaN.
+ * workspace: moe_q4_workspace_bytes bytes of device memory, 256-byte aligned,
+ * with any content, NULL if 0; calls that may run at once (other streams,
+ * graphs replayed side by side) need one each. flags: MOE_ACCUMULATE or 0. */
+MOE_API int moe_q4_matmul(int32_t device, void* stream, int32_t n_tokens, int32_t n_out, int32_t k,
+                          int32_t x_type, const void* x, int64_t x_stride, const float* x_scales,
+                          int64_t x_scales_stride, const void* nibbles, const void* w_scales,
+                          int32_t y_type, void* y, int64_t y_stride, void* workspace, int64_t workspace_bytes,
+                          uint32_t flags);
+/* Bytes of its workspace, -1 on a bad size or type. */
+MOE_API int64_t moe_q4_workspace_bytes(int32_t n_tokens, int32_t n_out, int32_t k, int32_t x_type);
+
+/* The router's load over a batch of tokens, and its losses. For logits
+ * [n_tokens][n_experts] (MOE_F32, MOE_F16 or MOE_BF16):
+ *   p[t] = softmax(logits[t]), lse[t] = log sum exp(logits[t])
+ *   S[t] = the top_k largest, ties to the lower id (moe_forward's picks)
+ *   counts[e] (=|+=) tokens with e in S[t]; a row of them is a row of moe_seed's
+ *              freq (uint32 there, int32 here: the same bits)
+ *   load[e]  = n_experts * c[e] / (top_k * n), c the counts of this call and n
+ *              its tokens: 1 for every expert if balanced
+ *   stats    = {balance + z term, balance term, z term, n} with
+ *              balance term = balance_coef * sum_e load[e] * mean_t p[t][e]
+ *              z term       = z_coef * mean_t lse[t]^2
+ * Tokens with valid[t] == 0 (uint8; NULL: none) and tokens whose logits are all
+ * -inf are left out of every sum: their lse is -inf. With n = 0 the loads and
+ * losses are 0. A NaN or +inf logit makes the losses NaN.
+ * n_experts 1..4096, top_k 1..min(n_experts, 32). counts
+ * int32 [E], load fp32 [E], stats fp32 [4], lse fp32 [n_tokens] are outputs.
+ * workspace: moe_router_balance_workspace_bytes bytes of device memory,
+ * 256-byte aligned, as moe_q4_matmul's. flags: MOE_ACCUMULATE (counts only) or 0. */
+MOE_API int moe_router_balance(int32_t device, void* stream, int32_t n_tokens, int32_t n_experts, int32_t top_k,
+                               int32_t z_type, const void* logits, int64_t z_stride, const uint8_t* valid,
+                               float balance_coef, float z_coef, int32_t* counts, float* load, float* stats,
+                               float* lse, void* workspace, int64_t workspace_bytes, uint32_t flags);
+MOE_API int64_t moe_router_balance_workspace_bytes(int32_t n_tokens, int32_t n_experts);
+
+/* Gradient of stats[0] to the logits (the picks, so load, taken as fixed):
+ *   dlogits[t][e] (=|+=) g / n * p[t][e] * (balance_coef * (load[e] -
+ *                        sum_j load[j] p[t][j]) + 2 * z_coef * lse[t])
+ * and 0 for a token left out (with MOE_ACCUMULATE: unchanged). g = *dloss
+ * (device fp32, NULL: 1). logits, load, stats and lse are those of the
+ * moe_router_balance call; d_type is MOE_F32, MOE_F16 or MOE_BF16; dlogits may
+ * be logits when type and stride are the same (not with MOE_ACCUMULATE). */
+MOE_API int moe_router_balance_grad(int32_t device, void* stream, int32_t n_tokens, int32_t n_experts,
+                                    int32_t z_type, const void* logits, int64_t z_stride, const float* load,
+                                    const float* stats, const float* lse, const float* dloss, float balance_coef,
+                                    float z_coef, int32_t d_type, void* dlogits, int64_t d_stride, uint32_t flags);
 
 /* Measurement aid, outside the MoE path: the read bandwidth a plain
  * streaming kernel (128-bit loads, grid-stride, 8 work-groups per CU)

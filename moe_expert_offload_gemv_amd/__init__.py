@@ -26,6 +26,10 @@ MOE_E_CAPTURING = -5
 MOE_E_RANGE = -6
 MOE_Q4_32_F16 = 1
 MOE_ACCUMULATE = 1
+MOE_F32 = 0
+MOE_F16 = 1
+MOE_BF16 = 2
+MOE_Q8_32 = 3
 MOE_MAX_SWAP_LEAD = 8
 MOE_STATIC_SCRATCH_BYTES = 16777216
 MOE_COLD_GPU = 0
@@ -40,6 +44,8 @@ EXPORTED = [
     "moe_forward", "moe_prefill", "moe_cache_step", "moe_get_info", "moe_get_slot_table", "moe_get_stamps",
     "moe_get_miss_log", "moe_get_counts", "moe_last_error", "moe_profile", "moe_preheat", "moe_measure_read_bandwidth",
     "moe_forward_static_scratch",
+    "moe_add_rmsnorm", "moe_q4_split", "moe_q4_matmul", "moe_q4_workspace_bytes", "moe_router_balance",
+    "moe_router_balance_workspace_bytes", "moe_router_balance_grad",
 ]
 
 
@@ -102,7 +108,7 @@ def lib():
         if not os.path.exists(LIB_PATH):
             raise RuntimeError(f"{LIB_PATH} is missing: build it with python -m moe_expert_offload_gemv_amd.build")
         L = C.CDLL(LIB_PATH)
-        vp, i32, i64, u32 = C.c_void_p, C.c_int32, C.c_int64, C.c_uint32
+        vp, i32, i64, u32, f32 = C.c_void_p, C.c_int32, C.c_int64, C.c_uint32, C.c_float
         sig = {
             "moe_expert_bytes": (i64, [i32, i32]),
             "moe_create": (C.c_int, [C.POINTER(moe_config), C.POINTER(vp)]),
@@ -123,6 +129,17 @@ def lib():
             "moe_profile": (C.c_int, [vp, i32, C.POINTER(moe_profile_stats)]),
             "moe_preheat": (C.c_int, [vp, i32, i32, C.POINTER(i32)]),
             "moe_measure_read_bandwidth": (C.c_int, [vp, i64, i32, i32, vp, C.POINTER(C.c_double)]),
+            "moe_add_rmsnorm": (C.c_int, [i32, vp, i32, i32, i32, vp, i64, i32, vp, i64, vp, i64, vp, f32, i32, vp, i64,
+                                          vp, i64]),
+            "moe_q4_split": (C.c_int, [i32, i32, vp, vp, vp]),
+            "moe_q4_matmul": (C.c_int, [i32, vp, i32, i32, i32, i32, vp, i64, vp, i64, vp, vp, i32, vp, i64, vp, i64,
+                                        u32]),
+            "moe_q4_workspace_bytes": (i64, [i32, i32, i32, i32]),
+            "moe_router_balance": (C.c_int, [i32, vp, i32, i32, i32, i32, vp, i64, vp, f32, f32, vp, vp, vp, vp, vp, i64,
+                                             u32]),
+            "moe_router_balance_workspace_bytes": (i64, [i32, i32]),
+            "moe_router_balance_grad": (C.c_int, [i32, vp, i32, i32, i32, vp, i64, vp, vp, vp, vp, f32, f32, i32, vp,
+                                                  i64, u32]),
         }
         for name, (res, args) in sig.items():
             f = getattr(L, name)
@@ -307,3 +324,209 @@ def moe_measure_read_bandwidth(buf=None, nbytes: int = 0, reps: int = 3, host_co
 
 def moe_last_error(ctx) -> str:
     return (lib().moe_last_error(ctx) or b"").decode(errors="replace")
+
+
+# ---------------------------------------------------------------------------
+# Operators beside the experts: torch tensors of any strided rows on one
+# device, issued on that device's current torch stream (or `stream`: a
+# torch.cuda.Stream or a raw hipStream_t int).
+
+_types = None
+
+
+def _type_codes() -> dict:
+    global _types
+    if _types is None:
+        import torch
+
+        _types = {torch.float32: MOE_F32, torch.float16: MOE_F16, torch.bfloat16: MOE_BF16, torch.int8: MOE_Q8_32}
+    return _types
+
+
+def _rows(name, t, dev, shape=None, dtype=None):
+    """(type code, address, row stride) of a 2-d tensor whose rows are contiguous runs of values."""
+    if t.dim() != 2 or (shape is not None and tuple(t.shape) != shape):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, not {shape or 'two-dimensional'}")
+    n, width = t.shape
+    stride, step = t.stride()
+    code = _type_codes().get(t.dtype)
+    if code is None or (dtype is not None and t.dtype != dtype):
+        raise ValueError(f"{name}: type {t.dtype}")
+    if t.get_device() != dev or dev < 0:
+        raise ValueError(f"{name}: not on cuda device {dev}")
+    if (step != 1 and width > 1) or (stride < width and n > 1):
+        raise ValueError(f"{name}: rows must be contiguous and must not overlap, strides {t.stride()}")
+    return code, t.data_ptr(), stride if stride > width else width
+
+
+def _flat(name, t, dev, shape, dtype):
+    """Address of a contiguous tensor (None -> NULL)."""
+    if t is None:
+        return None
+    if tuple(t.shape) != shape or t.dtype != dtype or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{name}: a contiguous {dtype} tensor of shape {shape} on cuda device {dev} is needed, "
+                         f"got {t.dtype} {tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
+
+
+def _bytes(name, t, dev):
+    """(address, bytes) of a workspace tensor."""
+    if t is None:
+        return None, 0
+    if t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{name}: a contiguous tensor on cuda device {dev} is needed")
+    return t.data_ptr(), t.numel() * t.element_size()
+
+
+def _stream_of(stream, dev):
+    if stream is None:
+        import torch
+
+        return torch.cuda.current_stream(dev).cuda_stream
+    return stream if isinstance(stream, int) else stream.cuda_stream
+
+
+def moe_add_rmsnorm(x, weight, out, residual=None, residual_out=None, scales=None, eps=1e-6, stream=None) -> None:
+    """out = RMS norm of x + residual (x without one) times weight; residual_out = x + residual.
+
+    x [T][H] fp32, fp16 or bf16; weight fp32 [H] or None; out [T][H] of those types, or int8 with
+    scales fp32 [T][H/32] (MOE_Q8_32). residual [T][H] is updated in place unless residual_out is given.
+    """
+    import torch
+
+    dev, shape = x.get_device(), tuple(x.shape)
+    xt, xp, xs = _rows("x", x, dev)
+    ot, op, os_ = _rows("out", out, dev, shape)
+    rt, rp, rs, rop, ros = xt, None, 0, None, 0
+    if residual is not None:
+        rt, rp, rs = _rows("residual", residual, dev, shape)
+        if residual_out is None:
+            rop, ros = rp, rs
+        else:
+            _, rop, ros = _rows("residual_out", residual_out, dev, shape, residual.dtype)
+    elif residual_out is not None:
+        raise ValueError("residual_out without a residual")
+    sp, ss = None, 0
+    if scales is not None:
+        _, sp, ss = _rows("scales", scales, dev, (shape[0], shape[1] // 32), torch.float32)
+    wp = _flat("weight", weight, dev, (shape[1],), torch.float32)
+    rc = lib().moe_add_rmsnorm(dev, _stream_of(stream, dev), shape[0], shape[1], xt, xp, xs, rt, rp, rs, rop, ros, wp,
+                               eps, ot, op, os_, sp, ss)
+    if rc:
+        _check(None, rc)
+
+
+def moe_q4_split(blocks):
+    """(nibbles uint8 [rows][k/32][16], scales fp16 [rows][k/32]) of canonical blocks uint8 [rows][k/32][18]."""
+    b = np.ascontiguousarray(blocks, np.uint8)
+    if b.ndim != 3 or b.shape[2] != 18:
+        raise ValueError(f"blocks of shape [rows][k/32][18] are needed, got {b.shape}")
+    nib, scl = np.empty(b.shape[:2] + (16,), np.uint8), np.empty(b.shape[:2], np.float16)
+    _check(None, lib().moe_q4_split(b.shape[0], 32 * b.shape[1], b.ctypes.data, nib.ctypes.data, scl.ctypes.data))
+    return nib, scl
+
+
+def moe_q4_workspace_bytes(n_tokens: int, n_out: int, k: int, x_type: int) -> int:
+    return int(lib().moe_q4_workspace_bytes(n_tokens, n_out, k, x_type))
+
+
+def moe_q4_workspace(x, nibbles):
+    """A workspace tensor for moe_q4_matmul of x with these weights (None if it needs none)."""
+    import torch
+
+    n = moe_q4_workspace_bytes(x.shape[0], nibbles.shape[0], x.shape[1], _type_codes()[x.dtype])
+    if n < 0:
+        raise ValueError(f"no product of x {tuple(x.shape)} with weights {tuple(nibbles.shape)}")
+    return torch.empty(n, dtype=torch.uint8, device=x.device) if n else None
+
+
+def moe_q4_matmul(x, nibbles, w_scales, y, scales=None, workspace=None, flags: int = 0, stream=None) -> None:
+    """y [T][N] = x [T][K] times the 4-bit weights [N][K] (nibbles, w_scales: the planes of moe_q4_split).
+
+    x fp32, fp16, bf16, or int8 with scales fp32 [T][K/32]; y fp32, fp16 or bf16. Without a workspace
+    a call that needs one allocates it from torch.
+    """
+    import torch
+
+    dev = x.get_device()
+    T, K = x.shape
+    xt, xp, xs = _rows("x", x, dev)
+    N = nibbles.shape[0]
+    np_ = _flat("nibbles", nibbles, dev, (N, K // 32, 16), torch.uint8)
+    wp = _flat("w_scales", w_scales, dev, (N, K // 32), torch.float16)
+    yt, yp, ys = _rows("y", y, dev, (T, N))
+    sp, ss = None, 0
+    if scales is not None:
+        _, sp, ss = _rows("scales", scales, dev, (T, K // 32), torch.float32)
+    s = _stream_of(stream, dev)
+    if workspace is None:
+        workspace = moe_q4_workspace(x, nibbles)
+        if workspace is not None and stream is not None:
+            raise ValueError("a call on a stream of its own needs its workspace")
+    kp, kn = _bytes("workspace", workspace, dev)
+    rc = lib().moe_q4_matmul(dev, s, T, N, K, xt, xp, xs, sp, ss, np_, wp, yt, yp, ys, kp, kn, flags)
+    if rc:
+        _check(None, rc)
+
+
+def moe_router_balance_workspace_bytes(n_tokens: int, n_experts: int) -> int:
+    return int(lib().moe_router_balance_workspace_bytes(n_tokens, n_experts))
+
+
+def moe_router_balance_workspace(logits):
+    """A workspace tensor for moe_router_balance of these logits."""
+    import torch
+
+    n = moe_router_balance_workspace_bytes(*logits.shape)
+    if n < 0:
+        raise ValueError(f"no balance of logits {tuple(logits.shape)}")
+    return torch.empty(n, dtype=torch.uint8, device=logits.device)
+
+
+def moe_router_balance(logits, top_k: int, counts, load, stats, lse, valid=None, balance=0.0, z=0.0, workspace=None,
+                       flags: int = 0, stream=None) -> None:
+    """Per-expert counts, loads and the balance and z losses of logits [T][E] (see moe_offload.h).
+
+    counts int32 [E], load fp32 [E], stats fp32 [4] and lse fp32 [T] are outputs; valid uint8 or bool [T] leaves
+    out tokens. Without a workspace the call allocates it from torch.
+    """
+    import torch
+
+    dev = logits.get_device()
+    zt, zp, zs = _rows("logits", logits, dev)
+    T, E = logits.shape
+    if valid is not None and valid.dtype == torch.bool:
+        valid = valid.view(torch.uint8)
+    vp = _flat("valid", valid, dev, (T,), torch.uint8)
+    cp = _flat("counts", counts, dev, (E,), torch.int32)
+    lp = _flat("load", load, dev, (E,), torch.float32)
+    tp = _flat("stats", stats, dev, (4,), torch.float32)
+    ep = _flat("lse", lse, dev, (T,), torch.float32)
+    s = _stream_of(stream, dev)
+    if workspace is None:
+        if stream is not None:
+            raise ValueError("a call on a stream of its own needs its workspace")
+        workspace = moe_router_balance_workspace(logits)
+    kp, kn = _bytes("workspace", workspace, dev)
+    rc = lib().moe_router_balance(dev, s, T, E, top_k, zt, zp, zs, vp, balance, z, cp, lp, tp, ep, kp, kn, flags)
+    if rc:
+        _check(None, rc)
+
+
+def moe_router_balance_grad(logits, load, stats, lse, dlogits, dloss=None, balance=0.0, z=0.0, flags: int = 0,
+                            stream=None) -> None:
+    """dlogits [T][E] = gradient of stats[0] to the logits, times dloss (fp32 [1], None: 1)."""
+    import torch
+
+    dev = logits.get_device()
+    zt, zp, zs = _rows("logits", logits, dev)
+    T, E = logits.shape
+    lp = _flat("load", load, dev, (E,), torch.float32)
+    tp = _flat("stats", stats, dev, (4,), torch.float32)
+    ep = _flat("lse", lse, dev, (T,), torch.float32)
+    gp = _flat("dloss", dloss, dev, (1,), torch.float32)
+    dt, dp, ds = _rows("dlogits", dlogits, dev, (T, E))
+    rc = lib().moe_router_balance_grad(dev, _stream_of(stream, dev), T, E, zt, zp, zs, lp, tp, ep, gp, balance, z, dt, dp,
+                                       ds, flags)
+    if rc:
+        _check(None, rc)

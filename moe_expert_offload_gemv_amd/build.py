@@ -18,7 +18,8 @@ OBJDIR = os.path.join(ROOT, "_build", "moe_offload")
 ARCH = os.environ.get("MOE_OFFLOAD_ARCH", "gfx950")
 
 SOURCES = ["route.hip", "decode.hip", "decode_layer.hip", "prefill_kernels.hip", "measure.hip", "step_copy.hip", "scratch.hip", "grouped_mfma.hip",
-           "runtime.cpp", "prefill.cpp", "host_experts.cpp"]
+           "norm.hip", "dense_q4.hip", "balance.hip",
+           "runtime.cpp", "prefill.cpp", "dense_ops.cpp", "host_experts.cpp"]
 # plain C++ with no HIP in it (x86 vector code chosen at run time), built by the host compiler
 HOST_ONLY = {"host_experts.cpp"}
 CXX = os.environ.get("CXX_HOST", "g++")

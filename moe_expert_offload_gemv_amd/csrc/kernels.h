@@ -277,6 +277,66 @@ struct CopyList {
 };
 hipError_t launch_copy_list(const CopyList& l, hipStream_t s);
 
+// ---------------------------------------------------------------------------
+// operators beside the experts (types: MOE_F32 ... of the public header;
+// strides in values; every size checked by the callers in dense_ops.cpp)
+
+// norm.hip
+struct NormArgs {
+  const void* x;
+  const void* res;     // nullptr: no residual
+  void* res_out;
+  const float* weight; // nullptr: ones
+  void* out;
+  float* scales;       // 8-bit out
+  int64_t x_stride, res_stride, res_out_stride, out_stride, scales_stride;
+  int64_t T, H;
+  int32_t x_type, res_type, out_type;
+  float eps;
+};
+hipError_t launch_add_rmsnorm(const NormArgs& a, hipStream_t s);
+
+// dense_q4.hip
+struct Q4Args {
+  const void* x;
+  const float* x_scales;      // 8-bit x
+  const void* nibbles;        // [N][K/32][16]
+  const uint16_t* w_scales;   // [N][K/32] fp16
+  void* y;
+  uint8_t* ws;
+  int64_t x_stride, x_scales_stride, y_stride;
+  int64_t T, N, K;
+  int32_t x_type, y_type, accumulate;
+};
+int64_t q4_workspace_bytes(int64_t T, int64_t N, int64_t K, int32_t x_type);
+hipError_t launch_q4_matmul(const Q4Args& a, hipStream_t s);
+
+// balance.hip
+struct BalanceArgs {
+  const void* logits;
+  const uint8_t* valid;  // nullptr: every token
+  int32_t* counts;
+  float* load;
+  float* stats;          // [4]
+  float* lse;
+  uint8_t* ws;
+  int64_t z_stride, T;
+  int32_t E, k, z_type, accumulate;
+  float balance, z;
+};
+int64_t balance_workspace_bytes(int64_t T, int32_t E);
+hipError_t launch_balance(const BalanceArgs& a, hipStream_t s);
+struct BalanceGradArgs {
+  const void* logits;
+  const float *load, *stats, *lse;
+  const float* dloss;    // nullptr: 1
+  void* dlogits;
+  int64_t z_stride, d_stride, T;
+  int32_t E, z_type, d_type, accumulate;
+  float balance, z;
+};
+hipError_t launch_balance_grad(const BalanceGradArgs& a, hipStream_t s);
+
 // Per-call scratch of a decode forward: device memory beyond its inputs and
 // outputs, carved from one block at 256-byte boundaries for P picks.
 struct ForwardScratch {

@@ -47,6 +47,19 @@ int moe_ctx_fail(moe_ctx* c, int code, const char* fmt, ...) {
   return code;
 }
 
+int moe_thread_fail(int code, const char* fmt, ...) {
+  char buf[512];
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(buf, sizeof(buf), fmt, ap);
+  va_end(ap);
+  try {
+    g_create_error = buf;
+  } catch (...) {  // out of host memory: the code still tells
+  }
+  return code;
+}
+
 #define HIP_TRY(ctx, expr)                                                                             \
   do {                                                                                                 \
     hipError_t e_ = (expr);                                                                            \
@@ -54,18 +67,6 @@ int moe_ctx_fail(moe_ctx* c, int code, const char* fmt, ...) {
   } while (0)
 
 namespace {
-
-struct DeviceGuard {
-  int prev = -1;
-  explicit DeviceGuard(int dev) {
-    if (hipGetDevice(&prev) != hipSuccess) prev = -1;
-    if (prev != dev) (void)hipSetDevice(dev);
-  }
-  ~DeviceGuard() {
-    int cur = -1;
-    if (prev >= 0 && hipGetDevice(&cur) == hipSuccess && cur != prev) (void)hipSetDevice(prev);
-  }
-};
 
 bool stream_capturing(hipStream_t s) {
   hipStreamCaptureStatus st = hipStreamCaptureStatusNone;

@@ -122,6 +122,22 @@ struct moe_ctx {
 };
 
 int moe_ctx_fail(moe_ctx* c, int code, const char* fmt, ...);
+// the same for calls without a context: the calling thread's message
+// (moe_last_error(NULL))
+int moe_thread_fail(int code, const char* fmt, ...);
+
+// makes `dev` the current device for its scope
+struct DeviceGuard {
+  int prev = -1;
+  explicit DeviceGuard(int dev) {
+    if (hipGetDevice(&prev) != hipSuccess) prev = -1;
+    if (prev != dev) (void)hipSetDevice(dev);
+  }
+  ~DeviceGuard() {
+    int cur = -1;
+    if (prev >= 0 && hipGetDevice(&cur) == hipSuccess && cur != prev) (void)hipSetDevice(prev);
+  }
+};
 int moe_ctx_dev_alloc(moe_ctx* c, void** p, size_t bytes, const char* what);
 int moe_ctx_host_alloc(moe_ctx* c, void** p, size_t bytes, unsigned flags, const char* what);
 
