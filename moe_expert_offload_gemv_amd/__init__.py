@@ -329,61 +329,73 @@ def moe_last_error(ctx) -> str:
 # ---------------------------------------------------------------------------
 # Operators beside the experts: torch tensors of any strided rows on one
 # device, issued on that device's current torch stream (or `stream`: a
-# torch.cuda.Stream or a raw hipStream_t int).
+# torch.cuda.Stream or a raw hipStream_t int). A call of theirs takes a few
+# microseconds on the GPU, so the checks here are kept to a few of the host.
 
-_types = None
+_types = {}  # torch dtype -> type code, filled with torch's first use
+_raw_stream = None
 
 
-def _type_codes() -> dict:
-    global _types
-    if _types is None:
+def _dense():
+    """The library's handle, with the torch side set up."""
+    global _raw_stream
+    if _raw_stream is None:
         import torch
 
-        _types = {torch.float32: MOE_F32, torch.float16: MOE_F16, torch.bfloat16: MOE_BF16, torch.int8: MOE_Q8_32}
-    return _types
-
-
-def _rows(name, t, dev, shape=None, dtype=None):
-    """(type code, address, row stride) of a 2-d tensor whose rows are contiguous runs of values."""
-    if t.dim() != 2 or (shape is not None and tuple(t.shape) != shape):
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, not {shape or 'two-dimensional'}")
-    n, width = t.shape
-    stride, step = t.stride()
-    code = _type_codes().get(t.dtype)
-    if code is None or (dtype is not None and t.dtype != dtype):
-        raise ValueError(f"{name}: type {t.dtype}")
-    if t.get_device() != dev or dev < 0:
-        raise ValueError(f"{name}: not on cuda device {dev}")
-    if (step != 1 and width > 1) or (stride < width and n > 1):
-        raise ValueError(f"{name}: rows must be contiguous and must not overlap, strides {t.stride()}")
-    return code, t.data_ptr(), stride if stride > width else width
-
-
-def _flat(name, t, dev, shape, dtype):
-    """Address of a contiguous tensor (None -> NULL)."""
-    if t is None:
-        return None
-    if tuple(t.shape) != shape or t.dtype != dtype or t.get_device() != dev or not t.is_contiguous():
-        raise ValueError(f"{name}: a contiguous {dtype} tensor of shape {shape} on cuda device {dev} is needed, "
-                         f"got {t.dtype} {tuple(t.shape)} on {t.device}")
-    return t.data_ptr()
-
-
-def _bytes(name, t, dev):
-    """(address, bytes) of a workspace tensor."""
-    if t is None:
-        return None, 0
-    if t.get_device() != dev or not t.is_contiguous():
-        raise ValueError(f"{name}: a contiguous tensor on cuda device {dev} is needed")
-    return t.data_ptr(), t.numel() * t.element_size()
+        _types.update({torch.float32: MOE_F32, torch.float16: MOE_F16, torch.bfloat16: MOE_BF16, torch.int8: MOE_Q8_32})
+        # the stream's handle without a Stream object around it, where this torch has that
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+    return _lib or lib()
 
 
 def _stream_of(stream, dev):
     if stream is None:
-        import torch
-
-        return torch.cuda.current_stream(dev).cuda_stream
+        return _raw_stream(dev)
     return stream if isinstance(stream, int) else stream.cuda_stream
+
+
+def _rows(name, t, dev, shape):
+    """(type code, address, row stride) of a 2-d tensor whose rows are contiguous runs of values."""
+    if t.shape != shape or t.get_device() != dev or dev < 0 or t.dtype not in _types:
+        raise ValueError(f"{name}: {t.dtype} {tuple(t.shape)} on {t.device}; fp32, fp16, bf16 or int8 of shape "
+                         f"{tuple(shape)} on cuda device {max(dev, 0)} is needed")
+    stride, step = t.stride()
+    width = shape[1]
+    if stride < width or step != 1:
+        if (step != 1 and width > 1) or (stride < width and shape[0] > 1):
+            raise ValueError(f"{name}: rows must be contiguous and must not overlap, strides {t.stride()}")
+        stride = max(stride, width)
+    return _types[t.dtype], t.data_ptr(), stride
+
+
+def _flat(name, t, dev, shape, dtype):
+    """Address of a contiguous tensor (None -> NULL); dtype: its name in torch."""
+    if t is None:
+        return None
+    if t.shape != shape or t.get_device() != dev or dev < 0 or str(t.dtype) != dtype or not t.is_contiguous():
+        raise ValueError(f"{name}: {t.dtype} {tuple(t.shape)} on {t.device}; a contiguous {dtype} tensor of shape "
+                         f"{tuple(shape)} on cuda device {max(dev, 0)} is needed")
+    return t.data_ptr()
+
+
+def _two_dims(name, t):
+    if t.dim() != 2:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, two dimensions are needed")
+    return t.shape
+
+
+def _workspace(t, dev, stream, make):
+    """(tensor, address, bytes) of the workspace tensor given, or of a new one from torch."""
+    if t is None:
+        t = make()
+        if t is None:
+            return None, None, 0
+        if stream is not None:  # torch's allocator would hand its memory on by the current stream's order
+            raise ValueError("workspace: a call on a stream of its own needs one")
+    if t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"workspace: a contiguous tensor on cuda device {dev} is needed")
+    return t, t.data_ptr(), t.numel() * t.element_size()
 
 
 def moe_add_rmsnorm(x, weight, out, residual=None, residual_out=None, scales=None, eps=1e-6, stream=None) -> None:
@@ -392,26 +404,29 @@ def moe_add_rmsnorm(x, weight, out, residual=None, residual_out=None, scales=Non
     x [T][H] fp32, fp16 or bf16; weight fp32 [H] or None; out [T][H] of those types, or int8 with
     scales fp32 [T][H/32] (MOE_Q8_32). residual [T][H] is updated in place unless residual_out is given.
     """
-    import torch
-
-    dev, shape = x.get_device(), tuple(x.shape)
-    xt, xp, xs = _rows("x", x, dev)
+    L = _dense()
+    shape, dev = _two_dims("x", x), x.get_device()
+    T, H = shape
+    xt, xp, xs = _rows("x", x, dev, shape)
     ot, op, os_ = _rows("out", out, dev, shape)
     rt, rp, rs, rop, ros = xt, None, 0, None, 0
     if residual is not None:
         rt, rp, rs = _rows("residual", residual, dev, shape)
-        if residual_out is None:
-            rop, ros = rp, rs
-        else:
-            _, rop, ros = _rows("residual_out", residual_out, dev, shape, residual.dtype)
+        rop, ros = rp, rs
+        if residual_out is not None:
+            rot, rop, ros = _rows("residual_out", residual_out, dev, shape)
+            if rot != rt:
+                raise ValueError(f"residual_out: {residual_out.dtype}, but the residual is {residual.dtype}")
     elif residual_out is not None:
-        raise ValueError("residual_out without a residual")
+        raise ValueError("residual_out: there is no residual")
     sp, ss = None, 0
     if scales is not None:
-        _, sp, ss = _rows("scales", scales, dev, (shape[0], shape[1] // 32), torch.float32)
-    wp = _flat("weight", weight, dev, (shape[1],), torch.float32)
-    rc = lib().moe_add_rmsnorm(dev, _stream_of(stream, dev), shape[0], shape[1], xt, xp, xs, rt, rp, rs, rop, ros, wp,
-                               eps, ot, op, os_, sp, ss)
+        st, sp, ss = _rows("scales", scales, dev, (T, H // 32))
+        if st != MOE_F32:
+            raise ValueError(f"scales: {scales.dtype}")
+    wp = _flat("weight", weight, dev, (H,), "torch.float32")
+    rc = L.moe_add_rmsnorm(dev, _stream_of(stream, dev), T, H, xt, xp, xs, rt, rp, rs, rop, ros, wp, eps, ot, op, os_, sp,
+                           ss)
     if rc:
         _check(None, rc)
 
@@ -434,9 +449,10 @@ def moe_q4_workspace(x, nibbles):
     """A workspace tensor for moe_q4_matmul of x with these weights (None if it needs none)."""
     import torch
 
-    n = moe_q4_workspace_bytes(x.shape[0], nibbles.shape[0], x.shape[1], _type_codes()[x.dtype])
+    _dense()
+    n = moe_q4_workspace_bytes(x.shape[0], nibbles.shape[0], x.shape[1], _types.get(x.dtype, -1))
     if n < 0:
-        raise ValueError(f"no product of x {tuple(x.shape)} with weights {tuple(nibbles.shape)}")
+        raise ValueError(f"no product of x {x.dtype} {tuple(x.shape)} with weights {tuple(nibbles.shape)}")
     return torch.empty(n, dtype=torch.uint8, device=x.device) if n else None
 
 
@@ -446,25 +462,21 @@ def moe_q4_matmul(x, nibbles, w_scales, y, scales=None, workspace=None, flags: i
     x fp32, fp16, bf16, or int8 with scales fp32 [T][K/32]; y fp32, fp16 or bf16. Without a workspace
     a call that needs one allocates it from torch.
     """
-    import torch
-
-    dev = x.get_device()
-    T, K = x.shape
-    xt, xp, xs = _rows("x", x, dev)
+    L = _dense()
+    shape, dev = _two_dims("x", x), x.get_device()
+    T, K = shape
     N = nibbles.shape[0]
-    np_ = _flat("nibbles", nibbles, dev, (N, K // 32, 16), torch.uint8)
-    wp = _flat("w_scales", w_scales, dev, (N, K // 32), torch.float16)
+    xt, xp, xs = _rows("x", x, dev, shape)
+    np_ = _flat("nibbles", nibbles, dev, (N, K // 32, 16), "torch.uint8")
+    wp = _flat("w_scales", w_scales, dev, (N, K // 32), "torch.float16")
     yt, yp, ys = _rows("y", y, dev, (T, N))
     sp, ss = None, 0
     if scales is not None:
-        _, sp, ss = _rows("scales", scales, dev, (T, K // 32), torch.float32)
-    s = _stream_of(stream, dev)
-    if workspace is None:
-        workspace = moe_q4_workspace(x, nibbles)
-        if workspace is not None and stream is not None:
-            raise ValueError("a call on a stream of its own needs its workspace")
-    kp, kn = _bytes("workspace", workspace, dev)
-    rc = lib().moe_q4_matmul(dev, s, T, N, K, xt, xp, xs, sp, ss, np_, wp, yt, yp, ys, kp, kn, flags)
+        st, sp, ss = _rows("scales", scales, dev, (T, K // 32))
+        if st != MOE_F32:
+            raise ValueError(f"scales: {scales.dtype}")
+    workspace, kp, kn = _workspace(workspace, dev, stream, lambda: moe_q4_workspace(x, nibbles))
+    rc = L.moe_q4_matmul(dev, _stream_of(stream, dev), T, N, K, xt, xp, xs, sp, ss, np_, wp, yt, yp, ys, kp, kn, flags)
     if rc:
         _check(None, rc)
 
@@ -490,25 +502,20 @@ def moe_router_balance(logits, top_k: int, counts, load, stats, lse, valid=None,
     counts int32 [E], load fp32 [E], stats fp32 [4] and lse fp32 [T] are outputs; valid uint8 or bool [T] leaves
     out tokens. Without a workspace the call allocates it from torch.
     """
-    import torch
-
-    dev = logits.get_device()
-    zt, zp, zs = _rows("logits", logits, dev)
-    T, E = logits.shape
-    if valid is not None and valid.dtype == torch.bool:
-        valid = valid.view(torch.uint8)
-    vp = _flat("valid", valid, dev, (T,), torch.uint8)
-    cp = _flat("counts", counts, dev, (E,), torch.int32)
-    lp = _flat("load", load, dev, (E,), torch.float32)
-    tp = _flat("stats", stats, dev, (4,), torch.float32)
-    ep = _flat("lse", lse, dev, (T,), torch.float32)
-    s = _stream_of(stream, dev)
-    if workspace is None:
-        if stream is not None:
-            raise ValueError("a call on a stream of its own needs its workspace")
-        workspace = moe_router_balance_workspace(logits)
-    kp, kn = _bytes("workspace", workspace, dev)
-    rc = lib().moe_router_balance(dev, s, T, E, top_k, zt, zp, zs, vp, balance, z, cp, lp, tp, ep, kp, kn, flags)
+    L = _dense()
+    shape, dev = _two_dims("logits", logits), logits.get_device()
+    T, E = shape
+    zt, zp, zs = _rows("logits", logits, dev, shape)
+    vp = None
+    if valid is not None:
+        vp = _flat("valid", valid, dev, (T,), "torch.bool" if str(valid.dtype) == "torch.bool" else "torch.uint8")
+    cp = _flat("counts", counts, dev, (E,), "torch.int32")
+    lp = _flat("load", load, dev, (E,), "torch.float32")
+    tp = _flat("stats", stats, dev, (4,), "torch.float32")
+    ep = _flat("lse", lse, dev, (T,), "torch.float32")
+    workspace, kp, kn = _workspace(workspace, dev, stream, lambda: moe_router_balance_workspace(logits))
+    rc = L.moe_router_balance(dev, _stream_of(stream, dev), T, E, top_k, zt, zp, zs, vp, balance, z, cp, lp, tp, ep, kp,
+                              kn, flags)
     if rc:
         _check(None, rc)
 
@@ -516,17 +523,16 @@ def moe_router_balance(logits, top_k: int, counts, load, stats, lse, valid=None,
 def moe_router_balance_grad(logits, load, stats, lse, dlogits, dloss=None, balance=0.0, z=0.0, flags: int = 0,
                             stream=None) -> None:
     """dlogits [T][E] = gradient of stats[0] to the logits, times dloss (fp32 [1], None: 1)."""
-    import torch
-
-    dev = logits.get_device()
-    zt, zp, zs = _rows("logits", logits, dev)
-    T, E = logits.shape
-    lp = _flat("load", load, dev, (E,), torch.float32)
-    tp = _flat("stats", stats, dev, (4,), torch.float32)
-    ep = _flat("lse", lse, dev, (T,), torch.float32)
-    gp = _flat("dloss", dloss, dev, (1,), torch.float32)
-    dt, dp, ds = _rows("dlogits", dlogits, dev, (T, E))
-    rc = lib().moe_router_balance_grad(dev, _stream_of(stream, dev), T, E, zt, zp, zs, lp, tp, ep, gp, balance, z, dt, dp,
-                                       ds, flags)
+    L = _dense()
+    shape, dev = _two_dims("logits", logits), logits.get_device()
+    T, E = shape
+    zt, zp, zs = _rows("logits", logits, dev, shape)
+    lp = _flat("load", load, dev, (E,), "torch.float32")
+    tp = _flat("stats", stats, dev, (4,), "torch.float32")
+    ep = _flat("lse", lse, dev, (T,), "torch.float32")
+    gp = _flat("dloss", dloss, dev, (1,), "torch.float32")
+    dt, dp, ds = _rows("dlogits", dlogits, dev, shape)
+    rc = L.moe_router_balance_grad(dev, _stream_of(stream, dev), T, E, zt, zp, zs, lp, tp, ep, gp, balance, z, dt, dp, ds,
+                                   flags)
     if rc:
         _check(None, rc)

@@ -36,10 +36,10 @@ FLAGS = [
 ]
 
 
-# per-file code generation options: the grouped MFMA kernels scale each MFMA
+# per-file code generation options: the grouped and dense MFMA kernels scale each MFMA
 # result in VALU right away, so their results go to VGPRs (the AGPR form
 # would add a v_accvgpr_read per result element)
-EXTRA_FLAGS = {"grouped_mfma.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
+EXTRA_FLAGS = {f: ["-mllvm", "-amdgpu-mfma-vgpr-form"] for f in ("grouped_mfma.hip", "dense_q4.hip")}
 
 
 def _compile(src: str) -> str:

@@ -3,6 +3,7 @@
 // on the caller's stream. Nothing is kept between calls.
 #include <hip/hip_runtime.h>
 
+#include <atomic>
 #include <cstring>
 
 #include "../../include/moe_offload.h"
@@ -12,7 +13,7 @@
 namespace {
 
 constexpr int32_t kMaxTokens = 1 << 24;  // token counts stay exact in fp32, grids and offsets in range
-constexpr int32_t kMaxOut = 1 << 24;
+constexpr int32_t kMaxOut = 1 << 22;
 
 bool value_type(int32_t t) { return t == MOE_F32 || t == MOE_F16 || t == MOE_BF16; }
 int64_t value_size(int32_t t) { return t == MOE_F32 ? 4 : t == MOE_Q8_32 ? 1 : 2; }
@@ -25,11 +26,17 @@ bool rows_ok(const void* p, int32_t type, int64_t n, int64_t stride) {
 bool aligned(const void* p, uintptr_t to) { return (uintptr_t)p % to == 0; }
 
 int device_ok(int32_t device, const char* what) {
-  int n = 0;
-  if (hipGetDeviceCount(&n) != hipSuccess || device < 0 || device >= n) {
-    (void)hipGetLastError();
-    return moe_thread_fail(MOE_E_INVAL, "%s: no HIP device %d", what, device);
+  static std::atomic<int> count{-1};  // devices of the process, asked for once
+  int n = count.load(std::memory_order_relaxed);
+  if (n < 0) {
+    if (hipGetDeviceCount(&n) != hipSuccess) {
+      (void)hipGetLastError();
+      n = 0;
+    } else {
+      count.store(n, std::memory_order_relaxed);
+    }
   }
+  if (device < 0 || device >= n) return moe_thread_fail(MOE_E_INVAL, "%s: no HIP device %d", what, device);
   return MOE_OK;
 }
 

@@ -131,11 +131,13 @@ struct DeviceGuard {
   int prev = -1;
   explicit DeviceGuard(int dev) {
     if (hipGetDevice(&prev) != hipSuccess) prev = -1;
-    if (prev != dev) (void)hipSetDevice(dev);
+    if (prev == dev)
+      prev = -1;  // nothing to restore
+    else
+      (void)hipSetDevice(dev);
   }
   ~DeviceGuard() {
-    int cur = -1;
-    if (prev >= 0 && hipGetDevice(&cur) == hipSuccess && cur != prev) (void)hipSetDevice(prev);
+    if (prev >= 0) (void)hipSetDevice(prev);
   }
 };
 int moe_ctx_dev_alloc(moe_ctx* c, void** p, size_t bytes, const char* what);
