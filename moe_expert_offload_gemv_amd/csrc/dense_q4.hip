@@ -27,6 +27,7 @@
 #include <algorithm>
 
 #include "kernels.h"
+#include "route_dev.h"
 #include "value_dev.h"
 
 namespace moe {
@@ -35,17 +36,24 @@ namespace {
 using namespace value_dev;
 
 typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 
-// bf16 terms an activation is split into
+// wide tiles: bf16 terms an activation is split into, and the operands' type
+template <int XT>
+constexpr int op_of() {
+  return XT == MOE_F16 ? MOE_F16 : MOE_BF16;
+}
 template <int XT>
 constexpr int terms_of() {
   return XT == MOE_F32 || XT == MOE_Q8_32 ? 3 : 1;
 }
 
-template <int XT>
+// OP: the 16-bit type of the products' operands, MOE_F16 or MOE_BF16
+template <int OP>
 __device__ __forceinline__ f32x4_t mfma(u32x4_t a, u32x4_t b, f32x4_t c) {
-  if constexpr (XT == MOE_F16) {
+  if constexpr (OP == MOE_F16) {
     f16x8_t x, y;
     __builtin_memcpy(&x, &a, 16);
     __builtin_memcpy(&y, &b, 16);
@@ -65,9 +73,9 @@ __device__ __forceinline__ uint32_t and_or(uint32_t x, uint32_t m, uint32_t c) {
 
 // the 8 weights 16 + q of a chunk from its dword: the nibble becomes the top
 // four mantissa bits of 16.0 (bf16: bits 3..6, fp16: bits 6..9)
-template <int XT>
+template <int OP>
 __device__ __forceinline__ uint32_t weights_part(uint32_t w, int i) {
-  if constexpr (XT == MOE_F16) {
+  if constexpr (OP == MOE_F16) {
     constexpr uint32_t M = 0x03C003C0u, C = 0x4C004C00u;
     return and_or(i == 0 ? w << 6 : i == 1 ? w >> 2 : i == 2 ? w << 2 : w >> 6, M, C);
   } else {
@@ -75,13 +83,13 @@ __device__ __forceinline__ uint32_t weights_part(uint32_t w, int i) {
     return and_or(i == 0 ? w << 3 : i == 1 ? w >> 5 : i == 2 ? w >> 1 : w >> 9, M, C);
   }
 }
-template <int XT>
+template <int OP>
 __device__ __forceinline__ u32x4_t weights_of(uint32_t w) {
-  return u32x4_t{weights_part<XT>(w, 0), weights_part<XT>(w, 1), weights_part<XT>(w, 2), weights_part<XT>(w, 3)};
+  return u32x4_t{weights_part<OP>(w, 0), weights_part<OP>(w, 1), weights_part<OP>(w, 2), weights_part<OP>(w, 3)};
 }
-template <int XT>
+template <int OP>
 __device__ __forceinline__ u32x4_t minus24() {
-  const uint32_t v = XT == MOE_F16 ? 0xCE00CE00u : 0xC1C0C1C0u;
+  const uint32_t v = OP == MOE_F16 ? 0xCE00CE00u : 0xC1C0C1C0u;
   return u32x4_t{v, v, v, v};
 }
 
@@ -102,6 +110,28 @@ __device__ __forceinline__ void broadcast4(uint32_t x, uint32_t (&out)[4]) {
   out[0] = lo[0], out[1] = lo[1], out[2] = hi[0], out[3] = hi[1];
 }
 
+// 4 x 4 transpose within every quad of lanes: register i of lane j and
+// register j of lane i change places
+template <int CTRL>
+__device__ __forceinline__ uint32_t from_quad(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, true);
+}
+__device__ __forceinline__ void transpose_quad(uint32_t (&v)[4]) {
+  const bool odd = threadIdx.x & 1, high = threadIdx.x & 2;
+  constexpr int kXor1 = 0xB1, kXor2 = 0x4E;  // quad_perm [1,0,3,2], [2,3,0,1]
+  // the moves stand before the selects: an arm of a conditional would run them
+  // with half the lanes off, and they read the other half
+  const uint32_t x0 = from_quad<kXor1>(v[0]), x1 = from_quad<kXor1>(v[1]);
+  const uint32_t x2 = from_quad<kXor1>(v[2]), x3 = from_quad<kXor1>(v[3]);
+  const uint32_t a0 = odd ? x1 : v[0], a1 = odd ? v[1] : x0, a2 = odd ? x3 : v[2], a3 = odd ? v[3] : x2;
+  const uint32_t y0 = from_quad<kXor2>(a0), y1 = from_quad<kXor2>(a1);
+  const uint32_t y2 = from_quad<kXor2>(a2), y3 = from_quad<kXor2>(a3);
+  v[0] = high ? y2 : a0;
+  v[1] = high ? y3 : a1;
+  v[2] = high ? a2 : y0;
+  v[3] = high ? a3 : y1;
+}
+
 // the upper halves of two words: low half from a, high half from b
 __device__ __forceinline__ uint32_t upper_halves(uint32_t a, uint32_t b) {
   return __builtin_amdgcn_perm(b, a, 0x07060302u);
@@ -110,41 +140,64 @@ __device__ __forceinline__ uint32_t lower_halves(uint32_t a, uint32_t b) {
   return __builtin_amdgcn_perm(b, a, 0x05040100u);
 }
 
-// The operand of chunk c of a block of a row, from the row's values: elements
-// 4c .. 4c + 3 and 16 + 4c .. 16 + 4c + 3, in the slots' order.
+// Four 8-bit codes as fp16, elements (0, 2) and (1, 3), exact: code + 128
+// becomes the low mantissa byte of 1024 + code + 128, from which 1152 is taken.
+__device__ __forceinline__ void codes_to_half(uint32_t codes, uint32_t& even, uint32_t& odd) {
+  const uint32_t x = codes ^ 0x80808080u;
+  const uint32_t u[2] = {__builtin_amdgcn_perm(0x64646464u, x, 0x04020400u),
+                         __builtin_amdgcn_perm(0x64646464u, x, 0x04030401u)};
+  f16x2_t h[2];
+  __builtin_memcpy(h, u, 8);
+  const f16x2_t off = {(_Float16)1152.0f, (_Float16)1152.0f};
+  h[0] -= off, h[1] -= off;
+  __builtin_memcpy(&even, &h[0], 4);
+  __builtin_memcpy(&odd, &h[1], 4);
+}
+
+// The values of chunk c of a block of a row, elements 4c .. 4c + 3 and 16 + 4c
+// .. 16 + 4c + 3, as loaded; scale: of 8-bit codes.
 template <int XT>
-__device__ __forceinline__ void chunk_of(const char* row, const float* scale, int64_t b, int c,
-                                         u32x4_t (&t)[terms_of<XT>()]) {
-  const int64_t i = 32 * b + 4 * c;
+struct RawChunk {
+  uint32_t lo[XT == MOE_F32 ? 4 : XT == MOE_Q8_32 ? 1 : 2], hi[XT == MOE_F32 ? 4 : XT == MOE_Q8_32 ? 1 : 2];
+  float scale;
+};
+template <int XT>
+__device__ __forceinline__ RawChunk<XT> load_chunk(const char* row, const float* scale, int64_t b, int c) {
+  RawChunk<XT> r;
+  const char* p = row + (32 * b + 4 * c) * value_size<XT>();
+  __builtin_memcpy(r.lo, p, 4 * value_size<XT>());
+  __builtin_memcpy(r.hi, p + 16 * value_size<XT>(), 4 * value_size<XT>());
+  if constexpr (XT == MOE_Q8_32) r.scale = scale[b];
+  return r;
+}
+
+// Its operand, in the slots' order: 16-bit values, or fp32 values (scale * code)
+// cut into bf16 terms.
+template <int XT, int TERMS>
+__device__ __forceinline__ void chunk_terms(const RawChunk<XT>& r, u32x4_t (&t)[TERMS]) {
   if constexpr (XT == MOE_F16 || XT == MOE_BF16) {
-    uint32_t lo[2], hi[2];
-    __builtin_memcpy(lo, row + 2 * i, 8);
-    __builtin_memcpy(hi, row + 2 * i + 32, 8);
-    t[0] = u32x4_t{lower_halves(lo[0], lo[1]), upper_halves(lo[0], lo[1]), lower_halves(hi[0], hi[1]),
-                   upper_halves(hi[0], hi[1])};
+    t[0] = u32x4_t{lower_halves(r.lo[0], r.lo[1]), upper_halves(r.lo[0], r.lo[1]), lower_halves(r.hi[0], r.hi[1]),
+                   upper_halves(r.hi[0], r.hi[1])};
   } else {
     float v[8];
-    if constexpr (XT == MOE_F32) {
-      __builtin_memcpy(v, row + 4 * i, 16);
-      __builtin_memcpy(v + 4, row + 4 * i + 64, 16);
-    } else {
-      uint32_t lo, hi;
-      __builtin_memcpy(&lo, row + i, 4);
-      __builtin_memcpy(&hi, row + i + 16, 4);
-      const float s = scale[b];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        v[j] = s * (float)(int8_t)(lo >> (8 * j));
-        v[4 + j] = s * (float)(int8_t)(hi >> (8 * j));
+    for (int j = 0; j < 4; ++j) {
+      if constexpr (XT == MOE_F32) {
+        v[j] = __uint_as_float(r.lo[j]);
+        v[4 + j] = __uint_as_float(r.hi[j]);
+      } else {
+        v[j] = (float)(int8_t)(r.lo[0] >> (8 * j));
+        v[4 + j] = (float)(int8_t)(r.hi[0] >> (8 * j));
+        v[j] *= r.scale, v[4 + j] *= r.scale;
       }
     }
 #pragma unroll
-    for (int k = 0; k < 3; ++k) {
+    for (int k = 0; k < TERMS; ++k) {
       uint32_t u[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         u[j] = __float_as_uint(v[j]);
-        v[j] -= __uint_as_float(u[j] & 0xFFFF0000u);  // exact: the bits below
+        if (k + 1 < TERMS) v[j] -= __uint_as_float(u[j] & 0xFFFF0000u);  // exact: the bits below
       }
       t[k] = u32x4_t{upper_halves(u[0], u[2]), upper_halves(u[1], u[3]), upper_halves(u[4], u[6]),
                      upper_halves(u[5], u[7])};
@@ -152,6 +205,21 @@ __device__ __forceinline__ void chunk_of(const char* row, const float* scale, in
   }
 }
 
+// sum of a chunk's 8 values, small terms first
+template <int XT, int TERMS>
+__device__ __forceinline__ float chunk_sum(const u32x4_t (&t)[TERMS]) {
+  float sum = 0.f;
+#pragma unroll
+  for (int k = TERMS - 1; k >= 0; --k)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (XT == MOE_F16)
+        sum += half_to_float((uint16_t)t[k][i]) + half_to_float((uint16_t)(t[k][i] >> 16));
+      else
+        sum += __uint_as_float(t[k][i] << 16) + __uint_as_float(t[k][i] & 0xFFFF0000u);
+    }
+  return sum;
+}
 // y[t][f] = v, or += v
 __device__ __forceinline__ void put(const Q4Args& a, int64_t t, int64_t f, float v) {
   const int64_t i = t * a.y_stride + f;
@@ -164,67 +232,554 @@ __device__ __forceinline__ void put(const Q4Args& a, int64_t t, int64_t f, float
 }
 
 // ---------------------------------------------------------------------------
-// Up to 16 tokens per work-group (more: further work-groups): 16 NW features
-// by 8 waves that share the reduction in steps of four blocks.
+// One token, or a few whose values fit the registers of a wave: dot products
+// on the vector unit. LPR lanes share a weight row; lane l has its blocks l,
+// l + LPR, ... (BPL of them) and keeps the activations of those blocks in
+// registers for all rows the wave takes, NR at a time, the next NR being
+// loaded meanwhile. A matrix tile would spend 140 instructions on 64 blocks,
+// most of them to bring weights and scales to its lanes, and its products wait
+// for each other; a lane's dot products take, per block of T tokens:
+//   8-bit x   12 + 11 T  (v_dot4 on bytes: integers, exact)
+//   16-bit x  32 + 18 T  (v_dot2 on 16 + q, sums starting at -24 sum x)
+//   fp32 x    44 + 34 T  (v_cvt_f32_ubyte, FMA)
+
+// the activations of one block of one token
+template <int XT>
+struct BlockX {
+  static constexpr int WORDS = XT == MOE_F32 ? 32 : XT == MOE_Q8_32 ? 8 : 16;
+  uint32_t v[WORDS];
+  float base;   // what the sum starts from: -24 (-8: fp32, 8-bit codes) times the sum of the values
+  float scale;  // 8-bit codes
+};
+
+template <int XT>
+__device__ __forceinline__ void load_block_x(const char* row, const float* scale, int b, int KB, BlockX<XT>& x) {
+  constexpr int S = value_size<XT>();
+  uint32_t raw[8 * S];
+  const bool inside = b < KB;  // past the row: zeros
+  __builtin_memcpy(raw, row + (int64_t)min(b, KB - 1) * 32 * S, 32 * S);
+#pragma unroll
+  for (int i = 0; i < 8 * S; ++i) raw[i] = inside ? raw[i] : 0u;
+  if constexpr (XT == MOE_F32) {
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) x.v[i] = raw[i], sum += __uint_as_float(raw[i]);
+    x.base = -8.0f * sum;
+  } else if constexpr (XT == MOE_Q8_32) {
+    int sum = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x.v[i] = raw[i], sum = __builtin_amdgcn_sdot4((int)raw[i], 0x01010101, sum, false);
+    x.base = __int_as_float(-8 * sum);  // an integer here
+    x.scale = inside ? scale[b] : 0.f;
+  } else {
+    // pairs in the order of weights_part: chunk c, elements (0, 2), (1, 3), (16, 18), (17, 19)
+    float sum = 0.f;
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t a = raw[8 * h + 2 * c], b2 = raw[8 * h + 2 * c + 1];
+        x.v[4 * c + 2 * h] = lower_halves(a, b2);
+        x.v[4 * c + 2 * h + 1] = upper_halves(a, b2);
+#pragma unroll
+        for (const uint32_t w : {a, b2})
+          sum += XT == MOE_F16 ? half_to_float((uint16_t)w) + half_to_float((uint16_t)(w >> 16))
+                               : __uint_as_float(w << 16) + __uint_as_float(w & 0xFFFF0000u);
+      }
+    x.base = -24.0f * sum;
+  }
+}
+
+// sum over a block of (q - 8) x, times the block's scale
+template <int XT, int T>
+__device__ __forceinline__ void block_dots(u32x4_t w, float d, const BlockX<XT> (&x)[T], float (&acc)[T]) {
+  if constexpr (XT == MOE_Q8_32) {
+    int s[T];
+#pragma unroll
+    for (int t = 0; t < T; ++t) s[t] = __float_as_int(x[t].base);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const uint32_t lo = w[c] & 0x0F0F0F0Fu, hi = (w[c] >> 4) & 0x0F0F0F0Fu;
+#pragma unroll
+      for (int t = 0; t < T; ++t) {
+        s[t] = __builtin_amdgcn_sdot4((int)lo, (int)x[t].v[c], s[t], false);
+        s[t] = __builtin_amdgcn_sdot4((int)hi, (int)x[t].v[4 + c], s[t], false);
+      }
+    }
+#pragma unroll
+    for (int t = 0; t < T; ++t) acc[t] = fmaf(d * x[t].scale, (float)s[t], acc[t]);
+  } else if constexpr (XT == MOE_F32) {
+    float s0[T], s1[T];
+#pragma unroll
+    for (int t = 0; t < T; ++t) s0[t] = x[t].base, s1[t] = 0.f;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      // through v_bitop3 (S0 & S1): a plain AND is folded into an extract per element
+      const uint32_t lo = __builtin_amdgcn_bitop3_b32(w[c], 0x0F0F0F0Fu, 0u, 0xC0);
+      const uint32_t hi = __builtin_amdgcn_bitop3_b32(w[c] >> 4, 0x0F0F0F0Fu, 0u, 0xC0);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float a = (float)((lo >> (8 * j)) & 0xFFu), b = (float)((hi >> (8 * j)) & 0xFFu);
+#pragma unroll
+        for (int t = 0; t < T; ++t) {
+          s0[t] = fmaf(a, __uint_as_float(x[t].v[4 * c + j]), s0[t]);
+          s1[t] = fmaf(b, __uint_as_float(x[t].v[16 + 4 * c + j]), s1[t]);
+        }
+      }
+    }
+#pragma unroll
+    for (int t = 0; t < T; ++t) acc[t] = fmaf(d, s0[t] + s1[t], acc[t]);
+  } else {
+    float s[T];
+#pragma unroll
+    for (int t = 0; t < T; ++t) s[t] = x[t].base;
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t p = weights_part<XT>(w[c], i);
+#pragma unroll
+        for (int t = 0; t < T; ++t) {
+          if constexpr (XT == MOE_F16) {
+            f16x2_t a, b;
+            __builtin_memcpy(&a, &p, 4);
+            __builtin_memcpy(&b, &x[t].v[4 * c + i], 4);
+            s[t] = __builtin_amdgcn_fdot2(a, b, s[t], false);
+          } else {
+            bf16x2_t a, b;
+            __builtin_memcpy(&a, &p, 4);
+            __builtin_memcpy(&b, &x[t].v[4 * c + i], 4);
+            s[t] = __builtin_amdgcn_fdot2_f32_bf16(a, b, s[t], false);
+          }
+        }
+      }
+#pragma unroll
+    for (int t = 0; t < T; ++t) acc[t] = fmaf(d, s[t], acc[t]);
+  }
+}
+
+// sum over the lanes at the same place of the wave's four 16-lane rows
+__device__ __forceinline__ float across_rows(float v) {
+  const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = __uint_as_float(a[0]) + __uint_as_float(a[1]);
+  const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(b[0]) + __uint_as_float(b[1]);
+}
+// sum over the LPR lanes of a row, in every one of them
+template <int LPR>
+__device__ __forceinline__ float row_sum(float v) {
+  v += __uint_as_float(route_dev::dpp32<route_dev::kDppQuadXor1>(__float_as_uint(v)));
+  v += __uint_as_float(route_dev::dpp32<route_dev::kDppQuadXor2>(__float_as_uint(v)));
+  v += __uint_as_float(route_dev::dpp32<route_dev::kDppRowHalfMirror>(__float_as_uint(v)));
+  v += __uint_as_float(route_dev::dpp32<route_dev::kDppRowMirror>(__float_as_uint(v)));
+  return LPR == 64 ? across_rows(v) : v;
+}
+
+// Sums of V values over the LPR lanes of a row: lane i (mod 4; 4 and above the
+// second four) ends with value i. Two rounds in which a lane hands half of its
+// values to its neighbour and keeps the other half, then plain sums over the
+// lanes that keep the same one: 17 instructions for four values, 14 for one.
+template <int LPR, int V>
+__device__ __forceinline__ float row_sums(const float (&v)[V]) {
+  static_assert(V <= 8, "two sets of four");
+  if constexpr (V == 1) {
+    return row_sum<LPR>(v[0]);
+  } else {
+    const int lane = threadIdx.x & 63;
+    const bool odd = lane & 1, high = lane & 2;
+    float out[V > 4 ? 2 : 1];
+#pragma unroll
+    for (int s = 0; s < (V > 4 ? 2 : 1); ++s) {
+      float q[4], h[2];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) q[i] = 4 * s + i < V ? v[4 * s + i < V ? 4 * s + i : 0] : 0.f;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float keep = odd ? q[2 * i + 1] : q[2 * i], send = odd ? q[2 * i] : q[2 * i + 1];
+        h[i] = keep + __uint_as_float(route_dev::dpp32<route_dev::kDppQuadXor1>(__float_as_uint(send)));
+      }
+      const float keep = high ? h[1] : h[0], send = high ? h[0] : h[1];
+      float r = keep + __uint_as_float(route_dev::dpp32<route_dev::kDppQuadXor2>(__float_as_uint(send)));
+      r += __uint_as_float(route_dev::dpp32<0x124>(__float_as_uint(r)));  // row_ror:4, row_ror:8
+      r += __uint_as_float(route_dev::dpp32<0x128>(__float_as_uint(r)));
+      out[s] = LPR == 64 ? across_rows(r) : r;
+    }
+    if constexpr (V > 4) return lane & 4 ? out[1] : out[0];
+    return out[0];
+  }
+}
+
+constexpr int kDotWaves = 4;
+
+// T: tokens held, at least those there are (the last one again, never stored)
+template <int XT, int LPR, int BPL, int T, int NR>
+__global__ __launch_bounds__(64 * kDotWaves) void q4_dot_kernel(Q4Args a) {
+  constexpr int RPW = 64 / LPR;  // rows side by side
+  const int lane = threadIdx.x & 63, lb = lane & (LPR - 1), side = lane / LPR;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int KB = (int)(a.K / 32), N = (int)a.N;
+  const u32x4_t* nib = static_cast<const u32x4_t*>(a.nibbles);
+  u32x4_t w[NR][BPL];
+  uint16_t d[NR][BPL];
+  auto issue = [&](int g) __attribute__((always_inline)) {
+#pragma unroll
+    for (int r = 0; r < NR; ++r) {
+      const int row = min((g * NR + r) * RPW + side, N - 1);  // past N: the last row, never stored
+#pragma unroll
+      for (int j = 0; j < BPL; ++j) {
+        const int64_t at = (int64_t)row * KB + min(lb + LPR * j, KB - 1);
+        w[r][j] = nib[at];
+        d[r][j] = a.w_scales[at];
+      }
+    }
+  };
+  const int groups = (N + NR * RPW - 1) / (NR * RPW), stride = gridDim.x * kDotWaves;
+  int g = blockIdx.x * kDotWaves + wave;
+  issue(g);
+  BlockX<XT> x[BPL][T];
+#pragma unroll
+  for (int t = 0; t < T; ++t) {
+    const int64_t tok = std::min<int64_t>(t, a.T - 1);
+    const char* row = static_cast<const char*>(a.x) + tok * a.x_stride * value_size<XT>();
+    const float* scale = XT == MOE_Q8_32 ? a.x_scales + tok * a.x_scales_stride : nullptr;
+#pragma unroll
+    for (int j = 0; j < BPL; ++j) load_block_x<XT>(row, scale, lb + LPR * j, KB, x[j][t]);
+  }
+#pragma unroll 1
+  for (; g < groups; g += stride) {
+    float acc[NR][T];
+#pragma unroll
+    for (int r = 0; r < NR; ++r) {
+#pragma unroll
+      for (int t = 0; t < T; ++t) acc[r][t] = 0.f;
+#pragma unroll
+      for (int j = 0; j < BPL; ++j) {
+        block_dots<XT, T>(w[r][j], half_to_float(d[r][j]), x[j], acc[r]);
+        // the row's registers are free: its loads of the next group
+        const int row = min(((g + stride) * NR + r) * RPW + side, N - 1);
+        const int64_t at = (int64_t)row * KB + min(lb + LPR * j, KB - 1);
+        w[r][j] = nib[at];
+        d[r][j] = a.w_scales[at];
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+    // lane i of a row's lanes stores value i: token i / NR of row i % NR
+    float flat[NR * T];
+#pragma unroll
+    for (int i = 0; i < NR * T; ++i) flat[i] = acc[i % NR][i / NR];
+    const float v = row_sums<LPR>(flat);
+    const int64_t row = ((int64_t)g * NR + lb % NR) * RPW + side;
+    if (lb < NR * (int)a.T && row < N) put(a, lb / NR, row, v);
+  }
+}
+
+template <int XT, int LPR, int BPL, int T, int NR>
+hipError_t launch_dot_rows(const Q4Args& a, hipStream_t s) {
+  constexpr int RPW = 64 / LPR;
+  static_assert(NR * T <= LPR && NR * T <= 8, "a lane per output of a row group");
+  // as many work-groups as a CU holds at about this many registers, every wave
+  // the same number of row groups
+  constexpr int kRegs = 32 + BPL * T * (BlockX<XT>::WORDS + 2) + 7 * NR * BPL;
+  constexpr int kWaves = 256 * kDotWaves * std::max(1, std::min(8, 512 / kRegs));
+  const int64_t groups = (a.N + NR * RPW - 1) / (NR * RPW), rounds = (groups + kWaves - 1) / kWaves;
+  const dim3 grid((unsigned)((groups + kDotWaves * rounds - 1) / (kDotWaves * rounds)));
+  return launch(q4_dot_kernel<XT, LPR, BPL, T, NR>, grid, dim3(64 * kDotWaves), Launch{s}, a);
+}
+template <int XT, int LPR, int BPL, int T>
+hipError_t launch_dot(const Q4Args& a, hipStream_t s) {
+  // rows in flight: 64 bytes per lane; up to 8192 rows one at a time, so that every CU has some
+  constexpr int kMany = std::max(1, std::min(4 / BPL, 8 / T));
+  return a.N <= 8192 ? launch_dot_rows<XT, LPR, BPL, T, 1>(a, s) : launch_dot_rows<XT, LPR, BPL, T, kMany>(a, s);
+}
+
+// tokens times blocks per lane whose values the kernel keeps in registers
+template <int XT>
+constexpr int dot_limit() {
+  return XT == MOE_F32 ? 2 : XT == MOE_Q8_32 ? 12 : 4;
+}
+template <int XT, int LPR, int BPL>
+hipError_t launch_dot_tokens(const Q4Args& a, hipStream_t s) {
+  constexpr int L = dot_limit<XT>() / BPL;
+  if (a.T <= 1) return launch_dot<XT, LPR, BPL, 1>(a, s);
+  if constexpr (L >= 2)
+    if (a.T <= 2) return launch_dot<XT, LPR, BPL, 2>(a, s);
+  if constexpr (L >= 4)
+    if (a.T <= 4) return launch_dot<XT, LPR, BPL, 4>(a, s);
+  if constexpr (L >= 6)
+    if (a.T <= 6) return launch_dot<XT, LPR, BPL, 6>(a, s);
+  return hipErrorInvalidValue;
+}
+template <int XT>
+int dot_blocks(int64_t KB) {  // per lane
+  return KB <= 16 ? 1 : KB <= 32 ? 2 : KB <= 64 ? 1 : KB <= 128 ? 2 : KB <= 256 ? 4 : 1 << 20;
+}
+template <int XT>
+bool dot_fits(const Q4Args& a) {
+  const int64_t T = a.T <= 2 ? a.T : a.T <= 4 ? 4 : a.T <= 6 ? 6 : 1 << 10;
+  return T * dot_blocks<XT>(a.K / 32) <= dot_limit<XT>();
+}
+template <int XT>
+hipError_t launch_dot_types(const Q4Args& a, hipStream_t s) {
+  const int64_t KB = a.K / 32;
+  if (KB <= 16) return launch_dot_tokens<XT, 16, 1>(a, s);
+  if (KB <= 32) return launch_dot_tokens<XT, 16, 2>(a, s);
+  if (KB <= 64) return launch_dot_tokens<XT, 64, 1>(a, s);
+  if (KB <= 128) return launch_dot_tokens<XT, 64, 2>(a, s);
+  if constexpr (dot_limit<XT>() >= 4) return launch_dot_tokens<XT, 64, 4>(a, s);
+  return hipErrorInvalidValue;
+}
+
+// The weights of one step, four blocks of 16 features, as loaded: lane l has
+// block l % 4 of row l / 4 of the tile and its scale. Sixteen neighbouring lanes so
+// read four runs of 64 bytes (and of 8); the lanes of a product's column each
+// reading its row would take a cache access per lane, 64 of them per load,
+// and those bound the kernel.
+struct StepWeights {
+  u32x4_t w;
+  uint32_t d;
+};
+// The products' column of a tile's feature and back: columns 4i + j and
+// features 4j + i.
+__device__ __forceinline__ constexpr int column_of(int f) { return 4 * (f & 3) + (f >> 2); }
+
+// blocks 4s .. of the row whose first block is `row`; past the row: its last
+// block, whose scale counts as 0 in step_ready. Nothing is done to the results
+// here, which would wait for them.
+__device__ __forceinline__ void load_step(const u32x4_t* nib, const uint16_t* scl, uint32_t row, int s, int lane, int KB,
+                                          StepWeights& st) {
+  const uint32_t at = row + (uint32_t)min(4 * s + (lane & 3), KB - 1);
+  st.w = nib[at];
+  st.d = scl[at];
+}
+// After the loads: w[i] of lane (column, c) holds chunk c of block 4s + i of
+// the column's feature, d[i] that block's scale. With lane = 16 c + 4 h + l, the
+// loaded word (c, h, l; dword) is wanted at (dword, h, c; register l): the swap
+// rounds exchange c and dword, the quads l and the register. The scales take
+// the same way from lane groups to registers by broadcasting.
+__device__ __forceinline__ void step_ready(const StepWeights& st, int s, int lane, int KB, uint32_t (&w)[4], float (&d)[4]) {
+  u32x4_t t = st.w;
+  transpose4(t);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w[i] = t[i];
+  transpose_quad(w);
+  uint32_t b[4];
+  broadcast4(4 * s + (lane & 3) < KB ? __float_as_uint(half_to_float((uint16_t)st.d)) : 0u, b);
+  transpose_quad(b);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) d[i] = __uint_as_float(b[i]);
+}
+
+// ---------------------------------------------------------------------------
+// Up to 256 tokens, one launch: a work-group of 8 waves takes 16 MT tokens by
+// 16 FW features; KW = 8 / FW waves share the reduction in steps of four
+// blocks. A chunk of CB blocks of the activations at a time is brought into
+// operand form in LDS by the whole work-group, read from memory in whole lines
+// and converted once for all its features; the next chunk's values and weights are
+// on their way meanwhile.
 
 constexpr int kWaves = 8;
 
-template <int XT, int NW>
-__global__ __launch_bounds__(64 * kWaves) void q4_rows16_kernel(Q4Args a) {
-  constexpr int TERMS = terms_of<XT>();
-  __shared__ f32x4_t s_red[kWaves][NW][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int col = lane & 15, c = lane >> 4;
-  const int64_t KB = a.K / 32, f0 = (int64_t)blockIdx.x * 16 * NW, t0 = (int64_t)blockIdx.y * 16;
-  const int64_t trow = std::min<int64_t>(t0 + col, a.T - 1);  // past the last token: its row, never stored
-  const char* xr = static_cast<const char*>(a.x) + trow * a.x_stride * value_size<XT>();
-  const float* xs = XT == MOE_Q8_32 ? a.x_scales + trow * a.x_scales_stride : nullptr;
-  f32x4_t acc[NW];
+// 8-bit codes stay one exact fp16 term here and their scales join the scale
+// FMAs: a third of the LDS and of the products
+template <int XT>
+constexpr int tile_terms() {
+  return XT == MOE_F32 ? 3 : 1;
+}
+template <int XT>
+constexpr int tile_op() {
+  return XT == MOE_F16 || XT == MOE_Q8_32 ? MOE_F16 : MOE_BF16;
+}
+
+template <int XT, int MT, int KW, int CB>
+__global__ __launch_bounds__(64 * kWaves, 2) void q4_tile_kernel(Q4Args a) {
+  constexpr int TERMS = tile_terms<XT>(), OP = tile_op<XT>(), FW = kWaves / KW, ROWS = 16 * MT, THREADS = 64 * kWaves;
+  constexpr bool Q8 = XT == MOE_Q8_32;
+  constexpr int UPB = 2 * value_size<XT>();               // 16-byte units of a block of x
+  constexpr int UNITS = ROWS * CB * UPB / THREADS;        // a thread's units of a chunk
+  constexpr int SCALES = (ROWS * CB + THREADS - 1) / THREADS;
+  static_assert(ROWS * CB * UPB % THREADS == 0 && CB % (4 * KW) == 0, "whole rounds");
+  // operand [term][block][token][c] of 16 bytes, c xor-ed by the token so that a
+  // fragment's reads spread over the banks; -24 sums and scales [block][token]
+  constexpr int kTerm = CB * ROWS * 64, kBase = TERMS * kTerm, kScale = kBase + CB * ROWS * 4;
+  constexpr int kLds = kScale + (Q8 ? CB * ROWS * 4 : 0), kSums = KW > 1 ? kWaves * MT * 64 * 16 : 0;
+  __shared__ __attribute__((aligned(16))) uint8_t s_x[kLds > kSums ? kLds : kSums];
+  float* s_base = reinterpret_cast<float*>(s_x + kBase);
+  float* s_scale = reinterpret_cast<float*>(s_x + kScale);
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int col = lane & 15, c = lane >> 4, kw = wave % KW, fw = wave / KW;
+  const int KB = (int)(a.K / 32), steps = (KB + 3) / 4;
+  const int64_t t0 = (int64_t)blockIdx.y * ROWS;
+  const int live = (int)std::min<int64_t>(a.T - t0, ROWS);
+  const int f0 = ((int)blockIdx.x * FW + fw) * 16, fb = min(f0, (int)a.N - 1);  // this wave's features
+  const u32x4_t* nib = static_cast<const u32x4_t*>(a.nibbles) + (int64_t)fb * KB;
+  const uint16_t* scl = a.w_scales + (int64_t)fb * KB;
+  const uint32_t wrow = (uint32_t)(min(f0 + (lane >> 2), (int)a.N - 1) - fb) * KB;  // past N: the last row, never stored
+
+  u32x4_t raw[UNITS];
+  float rscale[SCALES];
+  // unit u of this thread: 16 bytes v of block b of token slot r
+  auto fetch = [&](int b0) __attribute__((always_inline)) {
 #pragma unroll
-  for (int t = 0; t < NW; ++t) acc[t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  for (int64_t b0 = 4 * wave; b0 < KB; b0 += 4 * kWaves) {
-    // lane (column, c) loads block b0 + c of its feature; past the row: its
-    // last block with scale 0
-    const int64_t b = std::min<int64_t>(b0 + c, KB - 1);
-    u32x4_t w[NW];
-    uint32_t d[NW][4];
-#pragma unroll
-    for (int t = 0; t < NW; ++t) {
-      const int64_t f = std::min<int64_t>(f0 + 16 * t + col, a.N - 1);
-      w[t] = static_cast<const u32x4_t*>(a.nibbles)[f * KB + b];
-      const float s = b0 + c < KB ? half_to_float(a.w_scales[f * KB + b]) : 0.f;
-      broadcast4(__float_as_uint(s), d[t]);
-      transpose4(w[t]);
+    for (int u = 0; u < UNITS; ++u) {
+      const int q = threadIdx.x + THREADS * u, r = q / (CB * UPB), b = min(b0 + q / UPB % CB, KB - 1), v = q % UPB;
+      const char* p = static_cast<const char*>(a.x) + (t0 + min(r, live - 1)) * a.x_stride * value_size<XT>();
+      __builtin_memcpy(&raw[u], p + (int64_t)b * 16 * UPB + 16 * v, 16);
     }
+    if constexpr (Q8) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      u32x4_t x[TERMS];
-      chunk_of<XT>(xr, xs, std::min<int64_t>(b0 + i, KB - 1), c, x);
-      f32x4_t base = f32x4_t{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int k = 0; k < TERMS; ++k) base = mfma<XT>(x[k], minus24<XT>(), base);
-#pragma unroll
-      for (int t = 0; t < NW; ++t) {
-        const u32x4_t wt = weights_of<XT>(w[t][i]);
-        f32x4_t p = base;
-#pragma unroll
-        for (int k = 0; k < TERMS; ++k) p = mfma<XT>(x[k], wt, p);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) acc[t][r] = fmaf(__uint_as_float(d[t][i]), p[r], acc[t][r]);
+      for (int u = 0; u < SCALES; ++u) {
+        const int q = min((int)threadIdx.x + THREADS * u, ROWS * CB - 1);
+        rscale[u] = a.x_scales[(t0 + min(q / CB, live - 1)) * a.x_scales_stride + min(b0 + q % CB, KB - 1)];
       }
     }
+  };
+  // into LDS, zeros for blocks past the row
+  auto put8 = [&](int k, int b, int r, int cc, int half, uint32_t lo, uint32_t hi) __attribute__((always_inline)) {
+    uint32_t* p = reinterpret_cast<uint32_t*>(s_x + k * kTerm + ((b * ROWS + r) * 4 + (cc ^ ((r >> 2) & 3))) * 16 + 8 * half);
+    p[0] = lo, p[1] = hi;
+  };
+  auto store = [&](int b0) __attribute__((always_inline)) {
+#pragma unroll
+    for (int u = 0; u < UNITS; ++u) {
+      const int q = threadIdx.x + THREADS * u, r = q / (CB * UPB), b = q / UPB % CB, v = q % UPB;
+      u32x4_t x = b0 + b < KB ? raw[u] : u32x4_t{0, 0, 0, 0};
+      float sum = 0.f;
+      if constexpr (XT == MOE_F32) {  // elements 4v .. 4v + 3: chunk v % 4, half v / 4
+        float f[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f[i] = __uint_as_float(x[i]);
+        sum = (f[0] + f[1]) + (f[2] + f[3]);
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+          uint32_t w[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            w[i] = __float_as_uint(f[i]);
+            if (k < 2) f[i] -= __uint_as_float(w[i] & 0xFFFF0000u);  // exact: the bits below
+          }
+          put8(k, b, r, v & 3, v >> 2, upper_halves(w[0], w[2]), upper_halves(w[1], w[3]));
+        }
+      } else if constexpr (Q8) {  // elements 16 v .. : half v of every chunk
+        int n = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint32_t lo, hi;
+          codes_to_half(x[i], lo, hi);
+          n = __builtin_amdgcn_sdot4((int)x[i], 0x01010101, n, false);
+          put8(0, b, r, i, v, lo, hi);
+        }
+        sum = (float)n;
+      } else {  // elements 8 v .. : half v / 2 of chunks 2 (v % 2) and the next
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          put8(0, b, r, 2 * (v & 1) + i, v >> 1, lower_halves(x[2 * i], x[2 * i + 1]), upper_halves(x[2 * i], x[2 * i + 1]));
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          sum += XT == MOE_F16 ? half_to_float((uint16_t)x[i]) + half_to_float((uint16_t)(x[i] >> 16))
+                               : __uint_as_float(x[i] << 16) + __uint_as_float(x[i] & 0xFFFF0000u);
+      }
+      // the block's other units are in the neighbouring lanes
+      sum += __uint_as_float(route_dev::dpp32<route_dev::kDppQuadXor1>(__float_as_uint(sum)));
+      if constexpr (UPB >= 4) sum += __uint_as_float(route_dev::dpp32<route_dev::kDppQuadXor2>(__float_as_uint(sum)));
+      if constexpr (UPB >= 8) sum += __uint_as_float(route_dev::dpp32<route_dev::kDppRowHalfMirror>(__float_as_uint(sum)));
+      if (v == 0) s_base[b * ROWS + r] = -24.0f * sum;
+    }
+    if constexpr (Q8) {
+#pragma unroll
+      for (int u = 0; u < SCALES; ++u) {
+        const int q = threadIdx.x + THREADS * u;
+        if (q < ROWS * CB) s_scale[q % CB * ROWS + q / CB] = rscale[u];
+      }
+    }
+  };
+
+  f32x4_t acc[MT];
+#pragma unroll
+  for (int m = 0; m < MT; ++m) acc[m] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  auto compute = [&](int s, int lb, const StepWeights& st) __attribute__((always_inline)) {
+    uint32_t w[4];
+    float d[4];
+    step_ready(st, s, lane, KB, w, d);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const u32x4_t wt = weights_of<OP>(w[i]);
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        const int at = ((lb + i) * ROWS + 16 * m + col) * 4 + (c ^ (col >> 2));
+        f32x4_t p = *reinterpret_cast<const f32x4_t*>(s_base + (lb + i) * ROWS + 16 * m + 4 * c);
+#pragma unroll
+        for (int k = 0; k < TERMS; ++k)
+          p = mfma<OP>(*reinterpret_cast<const u32x4_t*>(s_x + k * kTerm + 16 * at), wt, p);
+        if constexpr (Q8) p *= *reinterpret_cast<const f32x4_t*>(s_scale + (lb + i) * ROWS + 16 * m + 4 * c);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) acc[m][r] = fmaf(d[i], p[r], acc[m][r]);
+        __asm__ volatile("" : "+v"(acc[m]));  // as in the wide kernel
+      }
+    }
+  };
+
+  // this wave's steps of the reduction: kw, kw + KW, ... of every chunk
+  StepWeights st;
+  load_step(nib, scl, wrow, min(kw, steps - 1), lane, KB, st);
+  fetch(0);
+#pragma unroll 1
+  for (int b0 = 0; b0 < KB; b0 += CB) {
+    if (b0) __syncthreads();  // every wave is done with the chunk before
+    store(b0);
+    __syncthreads();
+    if (b0 + CB < KB) fetch(b0 + CB);
+#pragma unroll 1
+    for (int lb = 4 * kw; lb < CB; lb += 4 * KW) {
+      const int s = b0 / 4 + lb / 4;
+      const StepWeights now = st;
+      load_step(nib, scl, wrow, min(s + KW, steps - 1), lane, KB, st);  // past the last step: never used
+      if (s < steps) compute(s, lb, now);
+    }
   }
+  if constexpr (KW == 1) {
+    // lane (column, c) holds tokens 4c + r of its feature
 #pragma unroll
-  for (int t = 0; t < NW; ++t) s_red[wave][t][lane] = acc[t];
-  __syncthreads();
-  // lane (column, c) holds tokens 4c + i of its feature
-  for (int e = threadIdx.x; e < 256 * NW; e += 64 * kWaves) {
-    const int f = e % (16 * NW), r = e / (16 * NW);
-    if (f0 + f >= a.N || t0 + r >= a.T) continue;
-    float v = 0.f;
+    for (int m = 0; m < MT; ++m)
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) v += s_red[w][f / 16][16 * (r / 4) + f % 16][r % 4];
-    put(a, t0 + r, f0 + f, v);
+      for (int r = 0; r < 4; ++r) {
+        const int tok = 16 * m + 4 * c + r, f = f0 + column_of(col);
+        if (tok < live && f < a.N) put(a, t0 + tok, f, acc[m][r]);
+      }
+  } else {
+    // the KW partial sums, in wave order
+    __syncthreads();
+    f32x4_t* s_sum = reinterpret_cast<f32x4_t*>(s_x);
+#pragma unroll
+    for (int m = 0; m < MT; ++m) s_sum[(wave * MT + m) * 64 + lane] = acc[m];
+    __syncthreads();
+#pragma unroll 1
+    for (int e = threadIdx.x; e < 16 * FW * live; e += THREADS) {
+      const int f = e % (16 * FW), tok = e / (16 * FW);
+      const float* p = reinterpret_cast<const float*>(s_sum) +
+                       ((f / 16 * KW * MT + tok / 16) * 64 + 16 * (tok / 4 % 4) + column_of(f % 16)) * 4 + tok % 4;
+      float v = 0.f;
+#pragma unroll
+      for (int w = 0; w < KW; ++w) v += p[w * MT * 256];
+      if ((int)blockIdx.x * 16 * FW + f < a.N) put(a, t0 + tok, (int)blockIdx.x * 16 * FW + f, v);
+    }
+  }
+}
+
+template <int XT, int MT, int KW, int CB>
+hipError_t launch_tile(const Q4Args& a, hipStream_t s) {
+  constexpr int F = 16 * kWaves / KW;
+  const dim3 grid((unsigned)((a.N + F - 1) / F), (unsigned)((a.T + 16 * MT - 1) / (16 * MT)));
+  return launch(q4_tile_kernel<XT, MT, KW, CB>, grid, dim3(64 * kWaves), Launch{s}, a);
+}
+template <int XT>
+hipError_t launch_tile_types(const Q4Args& a, hipStream_t s) {
+  const bool many = a.N > 16 * 512;
+  if (a.T <= 16) return many ? launch_tile<XT, 1, 1, 32>(a, s) : launch_tile<XT, 1, 8, 32>(a, s);
+  if constexpr (XT == MOE_F32) {
+    return many ? launch_tile<XT, 2, 1, 16>(a, s) : launch_tile<XT, 2, 4, 16>(a, s);
+  } else {
+    if (a.T <= 32) return many ? launch_tile<XT, 2, 1, 16>(a, s) : launch_tile<XT, 2, 8, 32>(a, s);
+    return many ? launch_tile<XT, 4, 1, 16>(a, s) : launch_tile<XT, 4, 4, 16>(a, s);
   }
 }
 
@@ -260,21 +815,14 @@ __global__ __launch_bounds__(256) void q4_operand_kernel(Q4Args a, Operand o) {
   if (unit >= o.rows / 16 * o.KB) return;
   const int64_t b = unit % o.KB, row = unit / o.KB * 16 + r;
   u32x4_t t[TERMS];
-  float sum = 0.f;
+  float sum;
 #pragma unroll
   for (int k = 0; k < TERMS; ++k) t[k] = u32x4_t{0, 0, 0, 0};
   if (row < a.T && b < a.K / 32)
-    chunk_of<XT>(static_cast<const char*>(a.x) + row * a.x_stride * value_size<XT>(),
-                 XT == MOE_Q8_32 ? a.x_scales + row * a.x_scales_stride : nullptr, b, c, t);
-#pragma unroll
-  for (int k = TERMS - 1; k >= 0; --k)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if constexpr (XT == MOE_F16)
-        sum += half_to_float((uint16_t)t[k][i]) + half_to_float((uint16_t)(t[k][i] >> 16));
-      else
-        sum += __uint_as_float(t[k][i] << 16) + __uint_as_float(t[k][i] & 0xFFFF0000u);
-    }
+    chunk_terms<XT>(load_chunk<XT>(static_cast<const char*>(a.x) + row * a.x_stride * value_size<XT>(),
+                                   XT == MOE_Q8_32 ? a.x_scales + row * a.x_scales_stride : nullptr, b, c),
+                    t);
+  sum = chunk_sum<XT>(t);
   sum += __shfl_xor(sum, 16, 64);
   sum += __shfl_xor(sum, 32, 64);
 #pragma unroll
@@ -320,16 +868,11 @@ __global__ __launch_bounds__(256, 2) void q4_wide_kernel(Q4Args a, Operand o, in
   const uint16_t* scl = a.w_scales + (int64_t)fb * KB;
   uint32_t wrow[4];
 #pragma unroll
-  for (int t = 0; t < 4; ++t) wrow[t] = (uint32_t)(min(f0 + 16 * t + col, (int)a.N - 1) - fb) * KB;
-  u32x4_t wn[4];
-  uint32_t dn[4];
+  for (int t = 0; t < 4; ++t) wrow[t] = (uint32_t)(min(f0 + 16 * t + (lane >> 2), (int)a.N - 1) - fb) * KB;
+  StepWeights wn[4];
   auto issue_weights = [&](int s) __attribute__((always_inline)) {
-    const int b = 4 * s + c, bc = min(b, KB - 1);
 #pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      wn[t] = nib[wrow[t] + bc];
-      dn[t] = scl[wrow[t] + bc];
-    }
+    for (int t = 0; t < 4; ++t) load_step(nib, scl, wrow[t], s, lane, KB, wn[t]);
   };
   // stage j (blocks SB j ..) into buffer j % 2: SB TERMS 2 operand pieces of 1 KiB per wave
   auto issue_stage = [&](int j) __attribute__((always_inline)) {
@@ -361,8 +904,8 @@ __global__ __launch_bounds__(256, 2) void q4_wide_kernel(Q4Args a, Operand o, in
   issue_weights(0);
   issue_stage(0);
   for (int s = 0; s < steps; ++s) {
-    u32x4_t w[4];
-    uint32_t d[4][4];
+    uint32_t w[4][4];
+    float d[4][4];
 #pragma unroll
     for (int h = 0; h < 4 / SB; ++h) {
       const int j = s * (4 / SB) + h;
@@ -371,12 +914,7 @@ __global__ __launch_bounds__(256, 2) void q4_wide_kernel(Q4Args a, Operand o, in
       __syncthreads();
       if (h == 0) {
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          w[t] = wn[t];
-          transpose4(w[t]);
-          // past the row: scale 0
-          broadcast4(4 * s + c < KB ? __float_as_uint(half_to_float((uint16_t)dn[t])) : 0u, d[t]);
-        }
+        for (int t = 0; t < 4; ++t) step_ready(wn[t], s, lane, KB, w[t], d[t]);
         if (s + 1 < steps) issue_weights(s + 1);
       }
       if (SB * (j + 1) < o.KB) issue_stage(j + 1);
@@ -397,7 +935,7 @@ __global__ __launch_bounds__(256, 2) void q4_wide_kernel(Q4Args a, Operand o, in
       };
       auto scale = [&](int g, int m) __attribute__((always_inline)) {
         const int t = g & 3;
-        const float dt = __uint_as_float(d[t][SB * h + (g >> 2)]);
+        const float dt = d[t][SB * h + (g >> 2)];
 #pragma unroll
         for (int r = 0; r < 4; ++r) acc[m][t][r] = fmaf(dt, p[g & 1][m][r], acc[m][t][r]);
         // a use of the sums here: otherwise the compiler sinks the scale FMAs to the end of the
@@ -406,7 +944,7 @@ __global__ __launch_bounds__(256, 2) void q4_wide_kernel(Q4Args a, Operand o, in
       };
       read_block(0);
       u32x4_t wt[2];
-      wt[0] = weights_of<XT>(w[0][SB * h]);
+      wt[0] = weights_of<op_of<XT>()>(w[0][SB * h]);
 #pragma unroll
       for (int g = 0; g < 4 * SB; ++g) {
         const int i = g >> 2;
@@ -419,8 +957,8 @@ __global__ __launch_bounds__(256, 2) void q4_wide_kernel(Q4Args a, Operand o, in
         for (int m = 0; m < 4; ++m) {
           p[g & 1][m] = base[i & 1][m];
 #pragma unroll
-          for (int k = 0; k < TERMS; ++k) p[g & 1][m] = mfma<XT>(x[i & 1][m][k], wt[g & 1], p[g & 1][m]);
-          if (g + 1 < 4 * SB) wt[(g + 1) & 1][m] = weights_part<XT>(w[(g + 1) & 3][SB * h + ((g + 1) >> 2)], m);
+          for (int k = 0; k < TERMS; ++k) p[g & 1][m] = mfma<op_of<XT>()>(x[i & 1][m][k], wt[g & 1], p[g & 1][m]);
+          if (g + 1 < 4 * SB) wt[(g + 1) & 1][m] = weights_part<op_of<XT>()>(w[(g + 1) & 3][SB * h + ((g + 1) >> 2)], m);
           if (g > 0) scale(g - 1, m);
           __builtin_amdgcn_sched_barrier(0);
         }
@@ -438,7 +976,7 @@ __global__ __launch_bounds__(256, 2) void q4_wide_kernel(Q4Args a, Operand o, in
       if (row >= a.T) continue;
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
-        const int f = f0 + 16 * t + col;
+        const int f = f0 + 16 * t + column_of(col);
         if (f < a.N) put(a, row, f, acc[m][t][r]);
       }
     }
@@ -477,8 +1015,8 @@ hipError_t launch_types(const Q4Args& a, hipStream_t s) {
     }
     return hipSuccess;
   }
-  const dim3 grid((unsigned)((a.N + 15) / 16), (unsigned)((a.T + 15) / 16));
-  return launch(q4_rows16_kernel<XT, 1>, grid, dim3(64 * kWaves), Launch{s}, a);
+  if (dot_fits<XT>(a)) return launch_dot_types<XT>(a, s);
+  return launch_tile_types<XT>(a, s);
 }
 
 }  // namespace
