@@ -570,12 +570,16 @@ __device__ __forceinline__ void step_ready(const StepWeights& st, int s, int lan
 }
 
 // ---------------------------------------------------------------------------
-// Up to 256 tokens, one launch: a work-group of 8 waves takes 16 MT tokens by
-// 16 FW features; KW = 8 / FW waves share the reduction in steps of four
-// blocks. A chunk of CB blocks of the activations at a time is brought into
-// operand form in LDS by the whole work-group, read from memory in whole lines
-// and converted once for all its features; the next chunk's values and weights are
-// on their way meanwhile.
+// Some tokens, one launch: a work-group of 8 waves takes 16 tokens by 16 FW
+// features; KW = 8 / FW waves share the reduction in steps of four blocks. A
+// chunk of CB blocks of the activations at a time is brought into operand form
+// in LDS by the whole work-group, read from memory in whole lines and converted
+// once for all its features; the next chunk's values and the next step's weights
+// are on their way meanwhile.
+//
+// 16 tokens a work-group: 32 or 64 would convert the weights once for more
+// tokens, but leave CUs idle at the sizes that come here (128 tokens, bf16, 1024 x
+// 1024: 7.0 us against 8.3 with 32; 5120 x 4096: 33 against 37; event times).
 
 constexpr int kWaves = 8;
 
@@ -590,27 +594,30 @@ constexpr int tile_op() {
   return XT == MOE_F16 || XT == MOE_Q8_32 ? MOE_F16 : MOE_BF16;
 }
 
-template <int XT, int MT, int KW, int CB>
-__global__ __launch_bounds__(64 * kWaves, 2) void q4_tile_kernel(Q4Args a) {
-  constexpr int TERMS = tile_terms<XT>(), OP = tile_op<XT>(), FW = kWaves / KW, ROWS = 16 * MT, THREADS = 64 * kWaves;
+template <int XT, int KW, int CB>
+__global__ __launch_bounds__(64 * kWaves, 2) void q4_tile_kernel(Q4Args a, int token_tiles) {
+  constexpr int TERMS = tile_terms<XT>(), OP = tile_op<XT>(), FW = kWaves / KW, ROWS = 16, THREADS = 64 * kWaves;
   constexpr bool Q8 = XT == MOE_Q8_32;
   constexpr int UPB = 2 * value_size<XT>();               // 16-byte units of a block of x
   constexpr int UNITS = ROWS * CB * UPB / THREADS;        // a thread's units of a chunk
   constexpr int SCALES = (ROWS * CB + THREADS - 1) / THREADS;
   static_assert(ROWS * CB * UPB % THREADS == 0 && CB % (4 * KW) == 0, "whole rounds");
-  // operand [term][block][token][c] of 16 bytes, c xor-ed by the token so that a
-  // fragment's reads spread over the banks; -24 sums and scales [block][token]
+  // operand [term][block][slot][c] of 16 bytes. Token r of block b sits in slot
+  // r + b (mod ROWS) and c is xor-ed by the slot, so that neither the stores (a row's
+  // blocks side by side) nor a fragment's reads meet in a bank; -24 sums and
+  // scales [block][token]
   constexpr int kTerm = CB * ROWS * 64, kBase = TERMS * kTerm, kScale = kBase + CB * ROWS * 4;
-  constexpr int kLds = kScale + (Q8 ? CB * ROWS * 4 : 0), kSums = KW > 1 ? kWaves * MT * 64 * 16 : 0;
+  constexpr int kLds = kScale + (Q8 ? CB * ROWS * 4 : 0), kSums = kWaves * 64 * 16;
   __shared__ __attribute__((aligned(16))) uint8_t s_x[kLds > kSums ? kLds : kSums];
   float* s_base = reinterpret_cast<float*>(s_x + kBase);
   float* s_scale = reinterpret_cast<float*>(s_x + kScale);
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 15, c = lane >> 4, kw = wave % KW, fw = wave / KW;
   const int KB = (int)(a.K / 32), steps = (KB + 3) / 4;
-  const int64_t t0 = (int64_t)blockIdx.y * ROWS;
+  const int ftile = blockIdx.x / token_tiles;
+  const int64_t t0 = (int64_t)(blockIdx.x - ftile * token_tiles) * ROWS;
   const int live = (int)std::min<int64_t>(a.T - t0, ROWS);
-  const int f0 = ((int)blockIdx.x * FW + fw) * 16, fb = min(f0, (int)a.N - 1);  // this wave's features
+  const int f0 = (ftile * FW + fw) * 16, fb = min(f0, (int)a.N - 1);  // this wave's features
   const u32x4_t* nib = static_cast<const u32x4_t*>(a.nibbles) + (int64_t)fb * KB;
   const uint16_t* scl = a.w_scales + (int64_t)fb * KB;
   const uint32_t wrow = (uint32_t)(min(f0 + (lane >> 2), (int)a.N - 1) - fb) * KB;  // past N: the last row, never stored
@@ -635,7 +642,9 @@ __global__ __launch_bounds__(64 * kWaves, 2) void q4_tile_kernel(Q4Args a) {
   };
   // into LDS, zeros for blocks past the row
   auto put8 = [&](int k, int b, int r, int cc, int half, uint32_t lo, uint32_t hi) __attribute__((always_inline)) {
-    uint32_t* p = reinterpret_cast<uint32_t*>(s_x + k * kTerm + ((b * ROWS + r) * 4 + (cc ^ ((r >> 2) & 3))) * 16 + 8 * half);
+    const int slot = (r + b) & (ROWS - 1);
+    uint32_t* p =
+        reinterpret_cast<uint32_t*>(s_x + k * kTerm + ((b * ROWS + slot) * 4 + (cc ^ ((slot >> 2) & 3))) * 16 + 8 * half);
     p[0] = lo, p[1] = hi;
   };
   auto store = [&](int b0) __attribute__((always_inline)) {
@@ -693,9 +702,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void q4_tile_kernel(Q4Args a) {
     }
   };
 
-  f32x4_t acc[MT];
-#pragma unroll
-  for (int m = 0; m < MT; ++m) acc[m] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  f32x4_t acc = f32x4_t{0.f, 0.f, 0.f, 0.f};
   auto compute = [&](int s, int lb, const StepWeights& st) __attribute__((always_inline)) {
     uint32_t w[4];
     float d[4];
@@ -703,18 +710,14 @@ __global__ __launch_bounds__(64 * kWaves, 2) void q4_tile_kernel(Q4Args a) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const u32x4_t wt = weights_of<OP>(w[i]);
+      const int slot = (col + lb + i) & (ROWS - 1), at = ((lb + i) * ROWS + slot) * 4 + (c ^ ((slot >> 2) & 3));
+      f32x4_t p = *reinterpret_cast<const f32x4_t*>(s_base + (lb + i) * ROWS + 4 * c);
 #pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        const int at = ((lb + i) * ROWS + 16 * m + col) * 4 + (c ^ (col >> 2));
-        f32x4_t p = *reinterpret_cast<const f32x4_t*>(s_base + (lb + i) * ROWS + 16 * m + 4 * c);
+      for (int k = 0; k < TERMS; ++k) p = mfma<OP>(*reinterpret_cast<const u32x4_t*>(s_x + k * kTerm + 16 * at), wt, p);
+      if constexpr (Q8) p *= *reinterpret_cast<const f32x4_t*>(s_scale + (lb + i) * ROWS + 4 * c);
 #pragma unroll
-        for (int k = 0; k < TERMS; ++k)
-          p = mfma<OP>(*reinterpret_cast<const u32x4_t*>(s_x + k * kTerm + 16 * at), wt, p);
-        if constexpr (Q8) p *= *reinterpret_cast<const f32x4_t*>(s_scale + (lb + i) * ROWS + 16 * m + 4 * c);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) acc[m][r] = fmaf(d[i], p[r], acc[m][r]);
-        __asm__ volatile("" : "+v"(acc[m]));  // as in the wide kernel
-      }
+      for (int r = 0; r < 4; ++r) acc[r] = fmaf(d[i], p[r], acc[r]);
+      __asm__ volatile("" : "+v"(acc));  // as in the wide kernel
     }
   };
 
@@ -736,51 +739,35 @@ __global__ __launch_bounds__(64 * kWaves, 2) void q4_tile_kernel(Q4Args a) {
       if (s < steps) compute(s, lb, now);
     }
   }
-  if constexpr (KW == 1) {
-    // lane (column, c) holds tokens 4c + r of its feature
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int tok = 16 * m + 4 * c + r, f = f0 + column_of(col);
-        if (tok < live && f < a.N) put(a, t0 + tok, f, acc[m][r]);
-      }
-  } else {
-    // the KW partial sums, in wave order
-    __syncthreads();
-    f32x4_t* s_sum = reinterpret_cast<f32x4_t*>(s_x);
-#pragma unroll
-    for (int m = 0; m < MT; ++m) s_sum[(wave * MT + m) * 64 + lane] = acc[m];
-    __syncthreads();
+  // the KW partial sums, in wave order; lane (column, c) holds tokens 4c + r of its feature
+  __syncthreads();
+  f32x4_t* s_sum = reinterpret_cast<f32x4_t*>(s_x);
+  s_sum[wave * 64 + lane] = acc;
+  __syncthreads();
 #pragma unroll 1
-    for (int e = threadIdx.x; e < 16 * FW * live; e += THREADS) {
-      const int f = e % (16 * FW), tok = e / (16 * FW);
-      const float* p = reinterpret_cast<const float*>(s_sum) +
-                       ((f / 16 * KW * MT + tok / 16) * 64 + 16 * (tok / 4 % 4) + column_of(f % 16)) * 4 + tok % 4;
-      float v = 0.f;
+  for (int e = threadIdx.x; e < 16 * FW * live; e += THREADS) {
+    const int f = e % (16 * FW), tok = e / (16 * FW);
+    const float* p =
+        reinterpret_cast<const float*>(s_sum) + (f / 16 * KW * 64 + 16 * (tok / 4) + column_of(f % 16)) * 4 + tok % 4;
+    float v = 0.f;
 #pragma unroll
-      for (int w = 0; w < KW; ++w) v += p[w * MT * 256];
-      if ((int)blockIdx.x * 16 * FW + f < a.N) put(a, t0 + tok, (int)blockIdx.x * 16 * FW + f, v);
-    }
+    for (int w = 0; w < KW; ++w) v += p[w * 256];
+    if (ftile * 16 * FW + f < a.N) put(a, t0 + tok, ftile * 16 * FW + f, v);
   }
 }
 
-template <int XT, int MT, int KW, int CB>
+template <int XT, int KW, int CB>
 hipError_t launch_tile(const Q4Args& a, hipStream_t s) {
   constexpr int F = 16 * kWaves / KW;
-  const dim3 grid((unsigned)((a.N + F - 1) / F), (unsigned)((a.T + 16 * MT - 1) / (16 * MT)));
-  return launch(q4_tile_kernel<XT, MT, KW, CB>, grid, dim3(64 * kWaves), Launch{s}, a);
+  const int64_t token_tiles = (a.T + 15) / 16, tiles = (a.N + F - 1) / F * token_tiles;
+  return launch(q4_tile_kernel<XT, KW, CB>, dim3((unsigned)tiles), dim3(64 * kWaves), Launch{s}, a, (int)token_tiles);
 }
 template <int XT>
 hipError_t launch_tile_types(const Q4Args& a, hipStream_t s) {
-  const bool many = a.N > 16 * 512;
-  if (a.T <= 16) return many ? launch_tile<XT, 1, 1, 32>(a, s) : launch_tile<XT, 1, 8, 32>(a, s);
-  if constexpr (XT == MOE_F32) {
-    return many ? launch_tile<XT, 2, 1, 16>(a, s) : launch_tile<XT, 2, 4, 16>(a, s);
-  } else {
-    if (a.T <= 32) return many ? launch_tile<XT, 2, 1, 16>(a, s) : launch_tile<XT, 2, 8, 32>(a, s);
-    return many ? launch_tile<XT, 4, 1, 16>(a, s) : launch_tile<XT, 4, 4, 16>(a, s);
-  }
+  // 16 features a work-group as long as each gets a CU of its own, else 32 (16 tokens, bf16, K = 4096, N =
+  // 4096: 10.7 us against 13.3; N = 65537: 87 against 57)
+  if ((a.T + 15) / 16 * ((a.N + 15) / 16) <= 256) return launch_tile<XT, 8, 32>(a, s);
+  return launch_tile<XT, 4, 16>(a, s);
 }
 
 // ---------------------------------------------------------------------------
@@ -788,7 +775,6 @@ hipError_t launch_tile_types(const Q4Args& a, hipStream_t s) {
 // TERMS KiB in the lanes' order, and -24 * sum of the block for each of them.
 // Tokens are padded to whole tiles and blocks to whole steps, both with zeros.
 
-constexpr int kTileRows = 128;  // tokens of a wide tile
 
 struct Operand {
   int64_t rows, KB, bytes;  // padded tokens, padded blocks, bytes with the sums
@@ -831,21 +817,34 @@ __global__ __launch_bounds__(256) void q4_operand_kernel(Q4Args a, Operand o) {
 }
 
 // ---------------------------------------------------------------------------
-// Wide tiles: 128 tokens x 128 features by 4 waves of 64 x 64. The operand
-// goes through LDS in stages of SB blocks, copied by the LDS-DMA loads two
-// deep; every wave loads its weights into registers one step (four blocks)
-// ahead.
+// Many tokens: tiles of 64 tokens x 64 features per wave. The operand goes
+// through LDS in a ring of stages of SB blocks, copied by the LDS-DMA loads; every
+// wave loads its weights into registers one step (four blocks) ahead.
+//   WK = 1: four waves make a tile of 128 x 128 and share two stages of four
+//           blocks (one: fp32), with a barrier each.
+//   WK = 4: four waves share one tile of 64 x 64 and split the reduction, step by
+//           step; each has stages of its own, one block each, three copies ahead
+//           (fp32: two) and no barrier; the sums are added at the end, in wave order.
+//           Four times the work-groups, for calls with few tiles: those have a
+//           wave per SIMD, whose copies nothing else covers.
 
 typedef __attribute__((address_space(3))) void lds_void_t;
 typedef __attribute__((address_space(1))) void glb_void_t;
 
-constexpr int kWideN = 128;
+// tokens, and features, of a work-group's tile
+constexpr int wide_side(int WK) { return WK == 1 ? 128 : 64; }
 
-template <int XT, int SB>
+// s_waitcnt immediate (GFX9 encoding) waiting for vmcnt <= n only
+constexpr int waitcnt_vm(int n) { return (n & 15) | (7 << 4) | (15 << 8) | ((n >> 4) << 14); }
+
+template <int XT, int SB, int WK, int RING>
 __global__ __launch_bounds__(256, 2) void q4_wide_kernel(Q4Args a, Operand o, int row_tiles, int col_tiles) {
-  constexpr int TERMS = terms_of<XT>();
-  constexpr int kTermBytes = 8 * SB * TERMS * 1024, kBaseBytes = 8 * SB * 64, kStage = kTermBytes + kBaseBytes;
-  __shared__ __attribute__((aligned(1024))) uint8_t s_x[2 * kStage];
+  constexpr int TERMS = terms_of<XT>(), SIDE = wide_side(WK), MG = SIDE / 16;  // row tiles of 16 in the stages
+  constexpr int kTermBytes = MG * SB * TERMS * 1024, kBaseBytes = MG * SB * 64, kStage = kTermBytes + kBaseBytes;
+  constexpr int kSums = WK > 1 ? WK * 16 * 64 * 16 : 0;
+  constexpr int kLds = RING * kStage * WK;
+  static_assert(RING == 2 || SB == 1, "the ring's waits count blocks");
+  __shared__ __attribute__((aligned(1024))) uint8_t s_lds[kLds > kSums ? kLds : kSums];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 15, c = lane >> 4;
   // work-groups go round the 8 XCDs: each XCD takes a run of the tiles, in
@@ -856,10 +855,12 @@ __global__ __launch_bounds__(256, 2) void q4_wide_kernel(Q4Args a, Operand o, in
   const int group = tile / (8 * col_tiles), in_group = tile - group * 8 * col_tiles;
   const int group_rows = min(8, row_tiles - 8 * group);
   const int rt = 8 * group + in_group % group_rows, ct = in_group / group_rows;
-  const int m0 = (wave & 1) * 4;                                     // row tiles of 16 within the tile
-  const int f0 = ct * kWideN + (wave >> 1) * 64;                     // this wave's features
+  const int m0 = WK == 1 ? (wave & 1) * 4 : 0;                       // row tiles of 16 within the tile
+  const int f0 = ct * SIDE + (WK == 1 ? (wave >> 1) * 64 : 0);       // this wave's features
+  const int wk = WK == 1 ? 0 : wave;                                 // its share of the reduction
   const int KB = (int)(a.K / 32), steps = (int)(o.KB / 4);
-  const int64_t u0 = (int64_t)rt * 8 * o.KB;                         // first operand unit of the tile's rows
+  const int64_t u0 = (int64_t)rt * MG * o.KB;                        // first operand unit of the tile's rows
+  uint8_t* s_x = s_lds + wk * RING * kStage;
 
   // block indexes of the lane's features (past N: the last one, never stored)
   // from the wave's first one: at most 63 rows of 2^15 blocks
@@ -874,23 +875,26 @@ __global__ __launch_bounds__(256, 2) void q4_wide_kernel(Q4Args a, Operand o, in
 #pragma unroll
     for (int t = 0; t < 4; ++t) load_step(nib, scl, wrow[t], s, lane, KB, wn[t]);
   };
-  // stage j (blocks SB j ..) into buffer j % 2: SB TERMS 2 operand pieces of 1 KiB per wave
-  auto issue_stage = [&](int j) __attribute__((always_inline)) {
-    uint8_t* dst = s_x + (j & 1) * kStage;
-    constexpr int kRun = SB * TERMS;  // KiB of a row tile
+  // blocks b0 .. b0 + SB - 1 into a buffer of the ring
+  auto issue_stage = [&](int buf, int b0) __attribute__((always_inline)) {
+    uint8_t* dst = s_x + buf * kStage;
+    constexpr int kRun = SB * TERMS;              // KiB of a row tile
+    constexpr int kMine = WK == 1 ? MG / 4 : MG;  // row tiles this wave copies
 #pragma unroll
-    for (int i = 0; i < 2 * kRun; ++i) {
-      const int m = 2 * wave + i / kRun, q = i % kRun;
-      const uint8_t* src = o.terms + ((u0 + m * o.KB + SB * j) * TERMS + q) * 1024 + 16 * lane;
+    for (int i = 0; i < kMine * kRun; ++i) {
+      const int m = (WK == 1 ? kMine * wave : 0) + i / kRun, q = i % kRun;
+      const uint8_t* src = o.terms + ((u0 + m * o.KB + b0) * TERMS + q) * 1024 + 16 * lane;
       __builtin_amdgcn_global_load_lds((glb_void_t*)src, (lds_void_t*)(dst + (m * kRun + q) * 1024), 16, 0, 0);
     }
-    // the sums: 64 SB bytes per row tile
+    // the sums: 64 SB bytes per row tile, 1 KiB per copy
     constexpr int kLanes = 4 * SB;  // lanes of a row tile
-    if (wave < kBaseBytes / 1024 || (kBaseBytes < 1024 && wave == 0)) {
-      const int at = 64 * wave + lane, m = at / kLanes;
-      if (m < 8) {
-        const uint8_t* src = reinterpret_cast<const uint8_t*>(o.base + (u0 + m * o.KB + SB * j) * 16) + 16 * (at % kLanes);
-        __builtin_amdgcn_global_load_lds((glb_void_t*)src, (lds_void_t*)(dst + kTermBytes + 1024 * wave), 16, 0, 0);
+#pragma unroll
+    for (int i = 0; i < (kBaseBytes + 1023) / 1024; ++i) {
+      if (WK == 1 && wave != i) continue;
+      const int at = 64 * i + lane, m = at / kLanes;
+      if (m < MG) {
+        const uint8_t* src = reinterpret_cast<const uint8_t*>(o.base + (u0 + m * o.KB + b0) * 16) + 16 * (at % kLanes);
+        __builtin_amdgcn_global_load_lds((glb_void_t*)src, (lds_void_t*)(dst + kTermBytes + 1024 * i), 16, 0, 0);
       }
     }
   };
@@ -901,24 +905,45 @@ __global__ __launch_bounds__(256, 2) void q4_wide_kernel(Q4Args a, Operand o, in
 #pragma unroll
     for (int t = 0; t < 4; ++t) acc[m][t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 
-  issue_weights(0);
-  issue_stage(0);
-  for (int s = 0; s < steps; ++s) {
+  // Stage j of the wave (SB blocks of its steps in turn; four blocks of a step
+  // are 4 / SB stages) lies in buffer j % RING and is copied RING - 1 stages ahead;
+  // past the last step that one's blocks again, never read, so that every stage
+  // is followed by the same number of loads.
+  constexpr int NS = 4 / SB;                                             // stages of a step
+  constexpr int kCopies = (WK == 1 ? MG / 4 : MG) * SB * TERMS + (WK == 1 ? 0 : (kBaseBytes + 1023) / 1024);
+  const int last = wk < steps ? wk + (steps - 1 - wk) / WK * WK : wk;   // the wave's last step
+  if (wk < steps) {
+    issue_weights(wk);
+#pragma unroll
+    for (int j = 0; j < RING - 1; ++j) issue_stage(j, 4 * min(wk + WK * (j / NS), last) + SB * (j % NS));
+  }
+#pragma unroll 1
+  for (int s = wk, n = 0; s < steps; s += WK, ++n) {
     uint32_t w[4][4];
     float d[4][4];
 #pragma unroll
-    for (int h = 0; h < 4 / SB; ++h) {
-      const int j = s * (4 / SB) + h;
-      // this wave's copies of stage j are done, then every wave's, and no wave reads stage j - 1 any more
-      __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0)
-      __syncthreads();
+    for (int h = 0; h < NS; ++h) {
+      const int j = n * NS + h, buf = NS % RING == 0 ? h % RING : j % RING;
+      // Stage j is there (WK = 1: all waves' shares, and no wave reads stage j - 1 any more). Loads come
+      // back in order: behind it are RING - 2 stages and, if they were issued in between, the step's weights.
+      constexpr int kAfter = (RING - 2) * kCopies;
+      if (RING > 2 && h >= 1 && h <= RING - 2)
+        __builtin_amdgcn_s_waitcnt(waitcnt_vm(kAfter + 8));
+      else
+        __builtin_amdgcn_s_waitcnt(waitcnt_vm(kAfter));
+      if constexpr (WK == 1) __syncthreads();
+      // nothing moves above the wait: LDS reads would come too early, and uses of the weights
+      // would be given a wait for every copy in flight
+      __asm__ volatile("" ::: "memory");
+      __builtin_amdgcn_sched_barrier(0);
       if (h == 0) {
 #pragma unroll
         for (int t = 0; t < 4; ++t) step_ready(wn[t], s, lane, KB, w[t], d[t]);
-        if (s + 1 < steps) issue_weights(s + 1);
+        issue_weights(min(s + WK, last));
       }
-      if (SB * (j + 1) < o.KB) issue_stage(j + 1);
-      const uint8_t* st = s_x + (j & 1) * kStage;
+      const int ahead = h + RING - 1;  // in stages from the step's first
+      issue_stage(NS % RING == 0 ? ahead % RING : (j + RING - 1) % RING, 4 * min(s + WK * (ahead / NS), last) + SB * (ahead % NS));
+      const uint8_t* st = s_x + buf * kStage;
       // One group per block and feature tile: the products of this tile (matrix
       // cores), beside them the scale FMAs of the tile before (VALU) and the
       // next tile's weights; the operand of the next block is read ahead.
@@ -967,19 +992,43 @@ __global__ __launch_bounds__(256, 2) void q4_wide_kernel(Q4Args a, Operand o, in
       for (int m = 0; m < 4; ++m) scale(4 * SB - 1, m);
     }
   }
-  // lane (column, c) holds tokens 4c + r of its features
+  if constexpr (WK == 1) {
+    // lane (column, c) holds tokens 4c + r of its features
 #pragma unroll
-  for (int m = 0; m < 4; ++m)
+    for (int m = 0; m < 4; ++m)
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int64_t row = (int64_t)rt * kTileRows + 16 * (m0 + m) + 4 * c + r;
-      if (row >= a.T) continue;
+      for (int r = 0; r < 4; ++r) {
+        const int64_t row = (int64_t)rt * SIDE + 16 * (m0 + m) + 4 * c + r;
+        if (row >= a.T) continue;
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        const int f = f0 + 16 * t + column_of(col);
-        if (f < a.N) put(a, row, f, acc[m][t][r]);
+        for (int t = 0; t < 4; ++t) {
+          const int f = f0 + 16 * t + column_of(col);
+          if (f < a.N) put(a, row, f, acc[m][t][r]);
+        }
       }
+  } else {
+    // every wave is done with its stages, the copies behind the last one too
+    __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
+    __syncthreads();
+    f32x4_t* s_sum = reinterpret_cast<f32x4_t*>(s_lds);
+#pragma unroll
+    for (int m = 0; m < 4; ++m)
+#pragma unroll
+      for (int t = 0; t < 4; ++t) s_sum[((wk * 4 + m) * 4 + t) * 64 + lane] = acc[m][t];
+    __syncthreads();
+#pragma unroll 1
+    for (int e = threadIdx.x; e < 64 * 64; e += 256) {
+      const int f = e & 63, tok = e >> 6;
+      const int64_t row = (int64_t)rt * SIDE + tok;
+      if (row >= a.T || f0 + f >= a.N) continue;
+      const float* p = reinterpret_cast<const float*>(s_sum) +
+                       ((tok / 16 * 4 + f / 16) * 64 + 16 * (tok / 4 % 4) + column_of(f % 16)) * 4 + tok % 4;
+      float v = 0.f;
+#pragma unroll
+      for (int w = 0; w < WK; ++w) v += p[w * 16 * 256];
+      put(a, row, f0 + f, v);
     }
+  }
 }
 
 template <int XT>
@@ -992,38 +1041,54 @@ hipError_t launch_operand(const Q4Args& a, const Operand& o, hipStream_t s) {
 // k = 2^20 are 2^25 operand units; 128 row tiles of 2^22 features 2^22 tiles)
 constexpr int64_t kPassTokens = 16384;
 
-bool wide(int64_t T) { return T > 256; }
+// 0: one launch without an operand pass; else the WK of the wide tiles.
+// Below about 2e9 products the one launch wins, whatever their shape (event times,
+// bf16: 128 x 2048 x 2048, 0.5e9, 11.8 us against 20.8; 64 x 5120 x 4096, 1.3e9, 23 against 29;
+// 128 x 5120 x 4096, 2.7e9, 33 against 30; 200 x 5120 x 4096, 53 against 42). Whole 128 x 128 tiles
+// pay from two work-groups per CU on (1024 x 5120 x 4096, 320 tiles, 121 us against 97 split; 2048 tokens,
+// 640 tiles, 180 either way; 4096 tokens, 1280 tiles, 290 against 318).
+int wide_split(int64_t T, int64_t N, int64_t K) {
+  if (T <= 32 || (double)T * (double)N * (double)K <= 2e9) return 0;
+  return ((T + 127) / 128) * ((N + 127) / 128) >= 512 ? 1 : 4;
+}
+
+template <int XT, int WK>
+hipError_t launch_wide(const Q4Args& a, hipStream_t s) {
+  constexpr int TERMS = terms_of<XT>(), SIDE = wide_side(WK), SB = TERMS == 3 || WK > 1 ? 1 : 4;
+  constexpr int RING = WK == 1 ? 2 : TERMS == 3 ? 3 : 4;
+  const int col_tiles = (int)((a.N + SIDE - 1) / SIDE);
+  for (int64_t t0 = 0; t0 < a.T; t0 += kPassTokens) {
+    Q4Args p = a;
+    p.T = std::min(a.T - t0, kPassTokens);
+    p.x = static_cast<const char*>(a.x) + t0 * a.x_stride * value_size<XT>();
+    p.x_scales = a.x_scales ? a.x_scales + t0 * a.x_scales_stride : nullptr;
+    p.y = static_cast<char*>(a.y) + t0 * a.y_stride * (a.y_type == MOE_F32 ? 4 : 2);
+    const Operand o = Operand::make(a.ws, p.T, a.K, TERMS, SIDE);
+    if (hipError_t e = launch_operand<XT>(p, o, s); e != hipSuccess) return e;
+    const int row_tiles = (int)(o.rows / SIDE);
+    const unsigned grid = (unsigned)(((int64_t)row_tiles * col_tiles + 7) / 8 * 8);
+    hipError_t e = launch(q4_wide_kernel<XT, SB, WK, RING>, dim3(grid), dim3(256), Launch{s}, p, o, row_tiles, col_tiles);
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
 
 template <int XT>
 hipError_t launch_types(const Q4Args& a, hipStream_t s) {
-  if (wide(a.T)) {
-    constexpr int TERMS = terms_of<XT>();
-    const int col_tiles = (int)((a.N + kWideN - 1) / kWideN);
-    for (int64_t t0 = 0; t0 < a.T; t0 += kPassTokens) {
-      Q4Args p = a;
-      p.T = std::min(a.T - t0, kPassTokens);
-      p.x = static_cast<const char*>(a.x) + t0 * a.x_stride * value_size<XT>();
-      p.x_scales = a.x_scales ? a.x_scales + t0 * a.x_scales_stride : nullptr;
-      p.y = static_cast<char*>(a.y) + t0 * a.y_stride * (a.y_type == MOE_F32 ? 4 : 2);
-      const Operand o = Operand::make(a.ws, p.T, a.K, TERMS, kTileRows);
-      if (hipError_t e = launch_operand<XT>(p, o, s); e != hipSuccess) return e;
-      const int row_tiles = (int)(o.rows / kTileRows);
-      const unsigned grid = (unsigned)(((int64_t)row_tiles * col_tiles + 7) / 8 * 8);
-      hipError_t e = launch(q4_wide_kernel<XT, TERMS == 1 ? 4 : 1>, dim3(grid), dim3(256), Launch{s}, p, o, row_tiles,
-                            col_tiles);
-      if (e != hipSuccess) return e;
-    }
-    return hipSuccess;
+  switch (wide_split(a.T, a.N, a.K)) {
+    case 1: return launch_wide<XT, 1>(a, s);
+    case 4: return launch_wide<XT, 4>(a, s);
   }
-  if (dot_fits<XT>(a)) return launch_dot_types<XT>(a, s);
-  return launch_tile_types<XT>(a, s);
+  return dot_fits<XT>(a) ? launch_dot_types<XT>(a, s) : launch_tile_types<XT>(a, s);
 }
 
 }  // namespace
 
 int64_t q4_workspace_bytes(int64_t T, int64_t N, int64_t K, int32_t x_type) {
-  if (!wide(T)) return 0;
-  return Operand::make(nullptr, std::min(T, kPassTokens), K, x_type == MOE_F32 || x_type == MOE_Q8_32 ? 3 : 1, kTileRows).bytes;
+  const int WK = wide_split(T, N, K);
+  if (!WK) return 0;
+  const int terms = x_type == MOE_F32 || x_type == MOE_Q8_32 ? 3 : 1;
+  return Operand::make(nullptr, std::min(T, kPassTokens), K, terms, wide_side(WK)).bytes;
 }
 
 hipError_t launch_q4_matmul(const Q4Args& a, hipStream_t s) {

@@ -68,16 +68,15 @@ def test_q4_matmul_refuses(change, what):
 
 def test_q4_matmul_refuses_a_small_workspace():
     for x_type in (moe.MOE_F32, moe.MOE_F16, moe.MOE_BF16, moe.MOE_Q8_32):
-        for T in (1, 16, 17, 64, 300, 4096):
-            need = moe.moe_q4_workspace_bytes(T, 8, 64, x_type)
-            assert need >= 0
-            if need:
-                a = {**Q4, "n_tokens": T, "x_type": x_type}
-                if x_type == moe.MOE_Q8_32:
-                    a.update(x_scales=6 * P, x_scales_stride=2)
-                _refused("moe_q4_matmul", {**a, "workspace_bytes": need - 1}, "workspace")
-                _refused("moe_q4_matmul", {**a, "workspace": None}, "workspace")
-                _refused("moe_q4_matmul", {**a, "workspace": P + 64}, "workspace")
+        for T in (200, 4096):
+            need = moe.moe_q4_workspace_bytes(T, 4096, 4096, x_type)
+            assert need > 0
+            a = {**Q4, "n_tokens": T, "n_out": 4096, "y_stride": 4096, "k": 4096, "x_stride": 4096, "x_type": x_type}
+            if x_type == moe.MOE_Q8_32:
+                a.update(x_scales=6 * P, x_scales_stride=128)
+            _refused("moe_q4_matmul", {**a, "workspace_bytes": need - 1}, "workspace")
+            _refused("moe_q4_matmul", {**a, "workspace": None}, "workspace")
+            _refused("moe_q4_matmul", {**a, "workspace": P + 64}, "workspace")
 
 
 def test_workspace_sizes_refuse_bad_sizes():

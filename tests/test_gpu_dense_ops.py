@@ -210,11 +210,15 @@ Q4_SHAPES = [(1, 1, 32), (1, 16, 32), (1, 2048, 2048), (1, 33, 96), (2, 17, 1056
              (16, 64, 256), (17, 65, 288), (32, 130, 1536), (33, 31, 64), (64, 256, 512), (65, 20, 2080), (100, 1001, 352),
              (128, 128, 128), (129, 127, 1024), (200, 512, 96), (256, 300, 640), (257, 70, 1312), (300, 260, 256),
              (515, 129, 416), (1030, 140, 128)]
+# above 2e9 products: 64 x 64 tiles with the reduction split, 128 x 128 tiles, and those in two passes of tokens
+Q4_LARGE = [(130, 2050, 8224), (2100, 3900, 256), (16500, 520, 256)]
 
 
-@pytest.mark.parametrize("T,N,K", Q4_SHAPES)
-@pytest.mark.parametrize("xt,yt", [("f32", "f32"), ("bf16", "f32"), ("f16", "f32"), ("q8", "f32"), ("bf16", "bf16"),
-                                   ("f16", "f16"), ("q8", "bf16")])
+@pytest.mark.parametrize("T,N,K,xt,yt", [s + (x, y) for s in Q4_SHAPES for x, y in
+                                         (("f32", "f32"), ("bf16", "f32"), ("f16", "f32"), ("q8", "f32"),
+                                          ("bf16", "bf16"), ("f16", "f16"), ("q8", "bf16"))]
+                         + [s + (x, y) for s in Q4_LARGE for x, y in
+                            (("f32", "f32"), ("bf16", "f32"), ("f16", "f16"), ("q8", "f32"))])
 def test_q4_matmul(T, N, K, xt, yt):
     p = Product(T, N, K, xt)
     pad, lead = (0, 0) if (T + N) % 2 else (5, 3)
@@ -237,30 +241,30 @@ def test_q4_matmul(T, N, K, xt, yt):
     assert (off <= p.bound + (u(dt) + E) * 1.01 * (np.abs(p.ref + 1.0) + p.bound) + smallest(dt)).all()
 
 
-@pytest.mark.parametrize("T", [1, 20, 300])
+@pytest.mark.parametrize("T,N,K", [(1, 40, 256), (20, 40, 256), (300, 40, 256), (40, 6000, 8704)])
 @pytest.mark.parametrize("xt,scale", [("f32", 2.0 ** 100), ("f32", 2.0 ** -90), ("bf16", 2.0 ** 100), ("f16", 2.0 ** -12),
                                       ("f16", 2.0 ** 12)])
-def test_q4_matmul_keeps_precision_far_from_unit_scale(T, xt, scale):
+def test_q4_matmul_keeps_precision_far_from_unit_scale(T, N, K, xt, scale):
     # fp16 at 2^-12: most values of x are subnormal or near it; they enter unrounded like any other
-    p = Product(T, 40, 256, xt, seed=1)
+    p = Product(T, N, K, xt, seed=1)
     g = rng_of(31, T)
-    x = torch.from_numpy(g.standard_normal((T, 256)) * scale).to(TYPES[xt]).cuda()
-    y = torch.zeros((T, 40), device="cuda")
+    x = torch.from_numpy(g.standard_normal((T, K)) * scale).to(TYPES[xt]).cuda()
+    y = torch.zeros((T, N), device="cuda")
     moe.moe_q4_matmul(x, p.nib, p.scl, y)
     q = torch.cat([p.nib & 15, p.nib >> 4], dim=2).cpu().double() - 8
-    w = (q * p.scl.cpu().double().unsqueeze(2)).view(40, 256)
+    w = (q * p.scl.cpu().double().unsqueeze(2)).view(N, K)
     ref = x.cpu().double() @ w.t()
     assert torch.linalg.norm(y.cpu().double() - ref) <= (p.rms + u(torch.float32)) * torch.linalg.norm(ref)
 
 
-@pytest.mark.parametrize("T", [3, 40, 260])
+@pytest.mark.parametrize("T,N,K", [(3, 50, 128), (40, 50, 128), (260, 50, 128), (260, 1000, 8000)])
 @pytest.mark.parametrize("xt", ["f32", "bf16", "f16"])
-def test_q4_matmul_values_that_are_not_finite_stay_in_their_token(T, xt):
-    p = Product(T, 50, 128, xt)
-    clean = torch.zeros((T, 50), device="cuda")
+def test_q4_matmul_values_that_are_not_finite_stay_in_their_token(T, N, K, xt):
+    p = Product(T, N, K, xt)
+    clean = torch.zeros((T, N), device="cuda")
     moe.moe_q4_matmul(p.x, p.nib, p.scl, clean)
     p.x[1, 5], p.x[2, 77] = float("nan"), float("inf")
-    y = torch.zeros((T, 50), device="cuda")
+    y = torch.zeros((T, N), device="cuda")
     moe.moe_q4_matmul(p.x, p.nib, p.scl, y)
     assert torch.isnan(y[1]).all() and torch.isnan(y[2]).all()
     rest = [t for t in range(T) if t not in (1, 2)]
