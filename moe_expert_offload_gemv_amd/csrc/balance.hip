@@ -83,6 +83,24 @@ __device__ __forceinline__ V sum_rows(V v) {
   return v;
 }
 
+// The same for 4 values at once, each lane row left with one of them: row g
+// with the sum of v[g] (v_permlane32_swap exchanges the upper half of the first
+// operand with the lower half of the second, v_permlane16_swap the odd rows of
+// the first with the even rows of the second).
+template <typename V>
+__device__ __forceinline__ V sum_rows4(const V* v) {
+  V h[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const auto s = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, v[i]),
+                                                    __builtin_bit_cast(uint32_t, v[i + 2]), false, false);
+    h[i] = __builtin_bit_cast(V, (uint32_t)s[0]) + __builtin_bit_cast(V, (uint32_t)s[1]);
+  }
+  const auto s = __builtin_amdgcn_permlane16_swap(__builtin_bit_cast(uint32_t, h[0]),
+                                                  __builtin_bit_cast(uint32_t, h[1]), false, false);
+  return __builtin_bit_cast(V, (uint32_t)s[0]) + __builtin_bit_cast(V, (uint32_t)s[1]);
+}
+
 // largest of a row's logits, NaNs passed over (-inf if there is none)
 template <int G, int NE>
 __device__ __forceinline__ float row_max(const float (&z)[NE]) {
@@ -98,29 +116,63 @@ __device__ __forceinline__ int expert_of(int j, int gl) {
   return (j >> 2) * 4 * G + gl * 4 + (j & 3);
 }
 
-// 4 values of a row of n from value i on; past it: -inf
+// The 4 values of a lane's run are read as one word whatever E is, without a
+// branch that would hold up the loads behind it: a run that passes the last
+// expert begins at E - 4 instead, and its first `skip` values, which are another
+// run's (or before expert 0, for E < 4), are left out.
+struct Run {
+  int at, skip;
+  __device__ __forceinline__ bool has(int i) const { return i >= skip; }
+};
+template <int G>
+__device__ __forceinline__ Run run_of(int j, int gl, int E) {
+  const int i = expert_of<G>(j & ~3, gl), at = min(i, E - 4);
+  return {at, i - at};
+}
+// the shares of MOE_BALANCE_SHAPE are filled by more than half, all but the
+// smallest: these of a lane's values are experts without a look
+template <int G, int NE>
+constexpr bool surely(int j) {
+  return NE > 4 && j < NE / 2;
+}
 template <int TYPE>
-__device__ __forceinline__ void load4(const char* p, int i, int n, float* v) {
-  if (i + 4 <= n) {
-    uint32_t w[4];
-    __builtin_memcpy(w, p + (int64_t)i * value_size<TYPE>(), 4 * value_size<TYPE>());
+struct Raw4 {
+  uint32_t w[TYPE == MOE_F32 ? 4 : 2];
+};
+template <int TYPE, int NE>
+__device__ __forceinline__ Raw4<TYPE> load_run(const char* p, Run r, int E) {
+  Raw4<TYPE> v;
+  if (NE == 4 && E < 4) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (uint32_t& w : v.w) w = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int e = max(r.at + i, 0);
       if constexpr (TYPE == MOE_F32)
-        v[j] = __uint_as_float(w[j]);
-      else if constexpr (TYPE == MOE_F16)
-        v[j] = half_to_float((uint16_t)(w[j >> 1] >> (16 * (j & 1))));
+        v.w[i] = reinterpret_cast<const uint32_t*>(p)[e];
       else
-        v[j] = bf16_to_float((w[j >> 1] >> (16 * (j & 1))) & 0xFFFFu);
+        v.w[i >> 1] |= (uint32_t)reinterpret_cast<const uint16_t*>(p)[e] << (16 * (i & 1));
     }
-  } else {
+    return v;
+  }
+  __builtin_memcpy(v.w, p + (int64_t)r.at * value_size<TYPE>(), sizeof v.w);
+  return v;
+}
+template <int TYPE>
+__device__ __forceinline__ void unpack4(const Raw4<TYPE>& r, float* v) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] = i + j < n ? load1<TYPE>(p, i + j) : kMinusInf;
+  for (int j = 0; j < 4; ++j) {
+    if constexpr (TYPE == MOE_F32)
+      v[j] = __uint_as_float(r.w[j]);
+    else if constexpr (TYPE == MOE_F16)
+      v[j] = half_to_float((uint16_t)(r.w[j >> 1] >> (16 * (j & 1))));
+    else
+      v[j] = bf16_to_float((r.w[j >> 1] >> (16 * (j & 1))) & 0xFFFFu);
   }
 }
 template <int TYPE>
-__device__ __forceinline__ void store4(char* p, int i, int n, const float* v) {
-  if (i + 4 <= n) {
+__device__ __forceinline__ void store_run(char* p, Run r, const float* v) {
+  if (r.skip == 0) {
     uint32_t w[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -130,37 +182,42 @@ __device__ __forceinline__ void store4(char* p, int i, int n, const float* v) {
         w[j] = TYPE == MOE_F16 ? (float_to_half(v[2 * j]) | (uint32_t)float_to_half(v[2 * j + 1]) << 16)
                                : (float_to_bf16(v[2 * j]) | (uint32_t)float_to_bf16(v[2 * j + 1]) << 16);
     }
-    __builtin_memcpy(p + (int64_t)i * value_size<TYPE>(), w, 4 * value_size<TYPE>());
+    __builtin_memcpy(p + (int64_t)r.at * value_size<TYPE>(), w, 4 * value_size<TYPE>());
   } else {
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (i + j < n) store1<TYPE>(p, i + j, v[j]);
+    for (int j = 1; j < 4; ++j)
+      if (r.has(j)) store1<TYPE>(p, r.at + j, v[j]);
   }
 }
-
-// order bits of a lane's logit (0: past the last expert)
-template <int G>
-__device__ __forceinline__ uint32_t bits_of(float z, int j, int gl, int E) {
-  return expert_of<G>(j, gl) < E ? route_dev::order_bits(z) : 0u;
+// d added to what the run holds, or in its place
+template <int TYPE, int NE>
+__device__ __forceinline__ void put_run(char* p, Run r, int E, bool accumulate, float* d) {
+  if (accumulate) {
+    float old[4];
+    unpack4<TYPE>(load_run<TYPE, NE>(p, r, E), old);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) d[i] += old[i];
+  }
+  store_run<TYPE>(p, r, d);
 }
 
-// order bits of the k-th largest logit of the row. k <= 8: each lane sorts
-// its logits eight at a time and keeps its 8 largest, then the lanes of the row
-// merge their lists (sorting networks of route_dev.h): 236 instructions for
-// four rows of 256 experts. k > 8: the bits are found from the top one down by
-// counting the logits not below each candidate.
+// The k-th largest of the row's order bits, and how many are larger. k <= 8:
+// each lane sorts its logits eight at a time and keeps its 8 largest, then the
+// lanes of the row merge their lists (sorting networks of route_dev.h): 236
+// instructions for four rows of 256 experts. k > 8: the bits are found from the
+// top one down by counting the logits not below each candidate.
 template <int G, int NE, bool TOP8>
-__device__ __forceinline__ uint32_t kth_bits(const float (&z)[NE], int gl, int E, int k) {
+__device__ __forceinline__ uint32_t kth_bits(const uint32_t (&b)[NE], int k, int& above) {
   if constexpr (TOP8) {
     uint32_t t[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) t[j] = j < NE ? bits_of<G>(z[j], j, gl, E) : 0u;
+    for (int j = 0; j < 8; ++j) t[j] = j < NE ? b[j < NE ? j : 0] : 0u;
     route_dev::sort8_desc(t);
 #pragma unroll
-    for (int b = 8; b < NE; b += 8) {
+    for (int o = 8; o < NE; o += 8) {
       uint32_t u[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) u[j] = bits_of<G>(z[b + j], b + j, gl, E);
+      for (int j = 0; j < 8; ++j) u[j] = b[o + j];
       route_dev::sort8_desc(u);
 #pragma unroll
       for (int j = 0; j < 8; ++j) t[j] = max(t[j], u[7 - j]);
@@ -177,16 +234,23 @@ __device__ __forceinline__ uint32_t kth_bits(const float (&z)[NE], int gl, int E
     uint32_t m = t[0];
 #pragma unroll
     for (int i = 1; i < 8; ++i) m = i < k ? t[i] : m;
+    above = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) above += t[i] > m ? 1 : 0;
     return m;
   } else {
     uint32_t m = 0;
-    for (int b = 31; b >= 0; --b) {
-      const uint32_t c = m | (1u << b);
+    for (int o = 31; o >= 0; --o) {
+      const uint32_t c = m | (1u << o);
       int n = 0;
 #pragma unroll
-      for (int j = 0; j < NE; ++j) n += bits_of<G>(z[j], j, gl, E) >= c ? 1 : 0;
+      for (int j = 0; j < NE; ++j) n += b[j] >= c ? 1 : 0;
       if (group_sum_int<G>(n) >= k) m = c;
     }
+    int n = 0;
+#pragma unroll
+    for (int j = 0; j < NE; ++j) n += b[j] > m ? 1 : 0;
+    above = group_sum_int<G>(n);
     return m;
   }
 }
@@ -206,73 +270,101 @@ __global__ __launch_bounds__(256) void balance_rows_kernel(BalanceArgs a) {
   for (int j = 0; j < NE; ++j) p[j] = 0.f, c[j] = 0;
   float z2 = 0.f;
   int n = 0;
-  for (int64_t row0 = ((int64_t)blockIdx.x * 4 + wave) * R; row0 < a.T; row0 += (int64_t)gridDim.x * 4 * R) {
-    const int64_t row = row0 + g;
-    const bool in = row < a.T && (!a.valid || a.valid[row]);
-    float z[NE];
-    const char* zr = static_cast<const char*>(a.logits) + (row < a.T ? row : 0) * a.z_stride * value_size<ZT>();
+  // a row's logits are on their way while the row before is worked on; for a
+  // token left out (or past the last) row 0 is read and counts as -inf
+  const int64_t stride = (int64_t)gridDim.x * 4 * R;
+  Raw4<ZT> raw[NE / 4];
+  bool in;
+  auto fetch = [&](int64_t row) __attribute__((always_inline)) {
+    in = row < a.T && (!a.valid || a.valid[row]);
+    const char* zr = static_cast<const char*>(a.logits) + (in ? row : 0) * a.z_stride * value_size<ZT>();
 #pragma unroll
-    for (int j = 0; j < NE; j += 4) load4<ZT>(zr, expert_of<G>(j, gl), E, z + j);
-    const float mx = row_max<G, NE>(z);
-    const float base = mx == kMinusInf ? 0.f : mx;  // a row of -inf alone: every exp is 0
-    float e[NE], sum = 0.f;
+    for (int j = 0; j < NE; j += 4) raw[j / 4] = load_run<ZT, NE>(zr, run_of<G>(j, gl, E), E);
+  };
+  int64_t row0 = ((int64_t)blockIdx.x * 4 + wave) * R;
+  fetch(row0 + g);
+  for (; row0 < a.T; row0 += stride) {
+    const int64_t row = row0 + g;
+    float e[NE];
+    uint32_t b[NE];
+#pragma unroll
+    for (int j = 0; j < NE; j += 4) unpack4<ZT>(raw[j / 4], e + j);
+    const bool used = in;
+    fetch(row + stride);
+    if (__ballot(!used)) {
+#pragma unroll
+      for (int j = 0; j < NE; ++j) e[j] = used ? e[j] : kMinusInf;
+    }
 #pragma unroll
     for (int j = 0; j < NE; ++j) {
-      e[j] = __expf(z[j] - base);
+      const bool yes = surely<G, NE>(j) || run_of<G>(j, gl, E).has(j & 3);
+      e[j] = yes ? e[j] : kMinusInf;
+      b[j] = yes ? route_dev::order_bits(e[j]) : 0u;
+    }
+    const float mx = row_max<G, NE>(e);
+    const float base = mx == kMinusInf ? 0.f : mx;  // a row of -inf alone: every exp is 0
+    float sum = 0.f;
+#pragma unroll
+    for (int j = 0; j < NE; ++j) {
+      e[j] = __expf(e[j] - base);
       sum += e[j];
     }
     sum = group_sum<G>(sum);
-    const float lse = in ? base + logf(sum) : kMinusInf;
-    const bool counted = in && lse != kMinusInf;
-    if (gl == 0 && row < a.T) a.lse[row] = lse;
+    const float lse = base + logf(sum);  // -inf for a row of -inf
+    const bool counted = used && lse != kMinusInf;
+    if (gl == 0 && row < a.T) a.lse[row] = used ? lse : kMinusInf;
     const float inv = counted ? 1.0f / sum : 0.f;
     z2 = counted ? fmaf(lse, lse, z2) : z2;
     n += counted ? 1 : 0;
-    const uint32_t m = kth_bits<G, NE, TOP8>(z, gl, E, k);
-    int above = 0, equal = 0;
+    int above;
+    const uint32_t m = kth_bits<G, NE, TOP8>(b, k, above);
+    // in the set: bits above floor, all ones for a row that does not count
+    const uint32_t floor = counted ? m - 1 : ~0u;
+    int chosen = 0;
 #pragma unroll
     for (int j = 0; j < NE; ++j) {
-      const uint32_t b = bits_of<G>(z[j], j, gl, E);
-      above += b > m ? 1 : 0;
-      equal += b == m ? 1 : 0;
+      p[j] = fmaf(e[j], inv, p[j]);
+      chosen += b[j] > floor ? 1 : 0;
     }
-    above = group_sum_int<G>(above);
-    equal = group_sum_int<G>(equal);
-    int last = E;  // equal ones up to this id are in the set
-    if (__ballot(above + equal > k)) {
-      // more equal logits than places: the lowest ids, one by one
-      int left = k - above;
-      last = -1;
+    if (__ballot(group_sum_int<G>(chosen) > k) == 0) {
+#pragma unroll
+      for (int j = 0; j < NE; ++j) c[j] += b[j] > floor ? 1 : 0;
+    } else {
+      // more equal logits than places: the lowest ids of them, one by one
+      int left = k - above, last = -1;
       while (__ballot(left > 0)) {
         int id = 0x7FFFFFFF;
 #pragma unroll
         for (int j = 0; j < NE; ++j) {
-          const int ex = expert_of<G>(j, gl);
-          if (bits_of<G>(z[j], j, gl, E) == m && ex > last) id = min(id, ex);
+          const int ex = run_of<G>(j, gl, E).at + (j & 3);
+          if (b[j] == m && ex > last) id = min(id, ex);
         }
         id = 0x7FFFFFFF - (int)group_max<G>((uint32_t)(0x7FFFFFFF - id));
         if (left > 0) last = id;
         --left;
       }
-    }
 #pragma unroll
-    for (int j = 0; j < NE; ++j) {
-      const uint32_t b = bits_of<G>(z[j], j, gl, E);
-      const bool chosen = b > m || (b == m && expert_of<G>(j, gl) <= last);
-      c[j] += counted && chosen ? 1 : 0;
-      p[j] = counted ? fmaf(e[j], inv, p[j]) : p[j];
+      for (int j = 0; j < NE; ++j) {
+        const bool yes = b[j] > m || (b[j] == m && run_of<G>(j, gl, E).at + (j & 3) <= last);
+        c[j] += counted && yes ? 1 : 0;
+      }
     }
   }
   // the wave's rows, then the waves in turn
   z2 = sum_rows<G>(z2);
   n = sum_rows<G>(n);
   if (lane == 0) s_z[wave] = z2, s_n[wave] = n;
-  for (int w = 0; w < 4; ++w) {
+  if constexpr (G == 16) {
 #pragma unroll
-    for (int j = 0; j < NE; ++j) {
-      if (w == 0) p[j] = sum_rows<G>(p[j]), c[j] = sum_rows<G>(c[j]);
-      if (wave == w && g == 0) {
-        const int ex = expert_of<G>(j, gl);
+    for (int j = 0; j < NE; j += 4) p[j / 4] = sum_rows4(p + j), c[j / 4] = sum_rows4(c + j);
+  }
+  for (int w = 0; w < 4; ++w) {
+    if (wave == w) {
+#pragma unroll
+      for (int j = 0; j < (G == 16 ? NE / 4 : NE); ++j) {
+        const Run r = run_of<G>(G == 16 ? 4 * j : j, gl, E);
+        const int i = G == 16 ? g : j & 3, ex = r.at + i;
+        if (!r.has(i)) continue;
         s_p[ex] = w ? s_p[ex] + p[j] : p[j];
         s_c[ex] = w ? s_c[ex] + c[j] : c[j];
       }
@@ -292,63 +384,68 @@ __global__ __launch_bounds__(256) void balance_rows_kernel(BalanceArgs a) {
   }
 }
 
-// Work-group b sums experts 32 b .. 32 b + 31 over the partial sums; the last
-// one to finish adds the groups' loss terms in order.
-__global__ __launch_bounds__(256) void balance_finish_kernel(BalanceArgs a, int blocks) {
-  __shared__ float s_p[8][kFinishExperts];
-  __shared__ int s_c[8][kFinishExperts];
-  __shared__ float s_z[4];
-  __shared__ int s_n[4], s_last;
+// Work-group b sums experts 32 b .. 32 b + 31 over the partial sums, 32 slices of
+// them side by side and a slice's loads at once; the last one to finish adds the
+// groups' loss terms in order.
+constexpr int kSlices = 32, kPerSlice = kBalanceBlocks / kSlices;
+__global__ __launch_bounds__(kFinishExperts * kSlices) void balance_finish_kernel(BalanceArgs a, int blocks) {
+  __shared__ float s_p[kSlices][kFinishExperts];
+  __shared__ int s_c[kSlices][kFinishExperts];
+  __shared__ float s_z[kSlices / 2];
+  __shared__ int s_n[kSlices / 2], s_last;
   const int t = threadIdx.x, E = a.E;
-  int n = 0;
-  float z2 = 0.f;
-  for (int b = t; b < blocks; b += 256) {
-    n += reinterpret_cast<const int*>(a.ws + kOffTokens)[b];
-    z2 += reinterpret_cast<const float*>(a.ws + kOffZ)[b];
+  static_assert(kBalanceBlocks <= kFinishExperts * kSlices, "a thread per partial sum");
+  int n = t < blocks ? reinterpret_cast<const int*>(a.ws + kOffTokens)[t] : 0;
+  float z2 = t < blocks ? reinterpret_cast<const float*>(a.ws + kOffZ)[t] : 0.f;
+  const int ex = blockIdx.x * kFinishExperts + (t & 31), slice = t >> 5;
+  const float* sums = reinterpret_cast<const float*>(a.ws + kOffSums) + min(ex, E - 1);
+  float vp[kPerSlice], vc[kPerSlice];
+#pragma unroll
+  for (int i = 0; i < kPerSlice; ++i) {
+    const int b = min(slice + kSlices * i, blocks - 1);  // past the last: it again, not added
+    vp[i] = sums[(int64_t)b * 2 * E];
+    vc[i] = sums[(int64_t)b * 2 * E + E];
   }
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) n += __shfl_xor(n, o, 64);
   z2 = route_dev::wave_sum(z2);
   if ((t & 63) == 0) s_n[t >> 6] = n, s_z[t >> 6] = z2;
-  const int ex = blockIdx.x * kFinishExperts + (t & 31), slice = t >> 5;
   float p = 0.f;
   int c = 0;
-  if (ex < E) {
-    const float* sums = reinterpret_cast<const float*>(a.ws + kOffSums) + ex;
-    for (int b = slice; b < blocks; b += 8) {
-      p += sums[(int64_t)b * 2 * E];
-      c += __float_as_int(sums[(int64_t)b * 2 * E + E]);
-    }
+#pragma unroll
+  for (int i = 0; i < kPerSlice; ++i) {
+    const bool yes = slice + kSlices * i < blocks;
+    p += yes ? vp[i] : 0.f;
+    c += yes ? __float_as_int(vc[i]) : 0;
   }
   s_p[slice][t & 31] = p;
   s_c[slice][t & 31] = c;
   __syncthreads();
-  n = (s_n[0] + s_n[1]) + (s_n[2] + s_n[3]);
-  z2 = (s_z[0] + s_z[1]) + (s_z[2] + s_z[3]);
+  if (t >= 64) return;
+  n = 0, z2 = 0.f;
+#pragma unroll
+  for (int i = 0; i < kSlices / 2; ++i) n += s_n[i], z2 += s_z[i];
   const float each = n > 0 ? 1.0f / (float)n : 0.f;
   float* terms = reinterpret_cast<float*>(a.ws + kOffTerms);
-  if (t < 64) {
-    float term = 0.f;
-    if (t < kFinishExperts && ex < E) {
-      p = 0.f, c = 0;
+  float term = 0.f;
+  if (t < kFinishExperts && ex < E) {
+    p = 0.f, c = 0;
 #pragma unroll
-      for (int s = 0; s < 8; ++s) p += s_p[s][t], c += s_c[s][t];
-      const float load = n > 0 ? (float)((double)E * c / ((double)a.k * n)) : 0.f;
-      a.load[ex] = load;
-      a.counts[ex] = a.accumulate ? a.counts[ex] + c : c;
-      term = load * (p * each);
-    }
-    term = route_dev::wave_sum(term);
-    if (t == 0) {
-      __hip_atomic_store(&terms[blockIdx.x], term, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-      // the term is visible to whoever sees this work-group's ticket
-      const uint32_t ticket = __hip_atomic_fetch_add(reinterpret_cast<uint32_t*>(a.ws), 1u, __ATOMIC_ACQ_REL,
-                                                     __HIP_MEMORY_SCOPE_AGENT);
-      s_last = ticket == gridDim.x - 1;
-    }
+    for (int s = 0; s < kSlices; ++s) p += s_p[s][t], c += s_c[s][t];
+    const float load = n > 0 ? (float)((double)E * c / ((double)a.k * n)) : 0.f;
+    a.load[ex] = load;
+    a.counts[ex] = a.accumulate ? a.counts[ex] + c : c;
+    term = load * (p * each);
   }
-  __syncthreads();
-  if (!s_last || t >= 64) return;
+  term = route_dev::wave_sum(term);
+  if (t == 0) {
+    __hip_atomic_store(&terms[blockIdx.x], term, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    // the term is visible to whoever sees this work-group's ticket
+    const uint32_t ticket = __hip_atomic_fetch_add(reinterpret_cast<uint32_t*>(a.ws), 1u, __ATOMIC_ACQ_REL,
+                                                   __HIP_MEMORY_SCOPE_AGENT);
+    s_last = ticket == gridDim.x - 1;
+  }
+  if (!__builtin_amdgcn_readfirstlane(s_last)) return;  // one wave: written above by its lane 0
   float bal = 0.f;
   for (int b = t; b < (int)gridDim.x; b += 64)
     bal += __hip_atomic_load(&terms[b], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
@@ -365,8 +462,9 @@ __global__ __launch_bounds__(256) void balance_grad_kernel(BalanceGradArgs a) {
   float load[NE];
 #pragma unroll
   for (int j = 0; j < NE; ++j) {
-    const int ex = expert_of<G>(j, gl);
-    load[j] = ex < E ? a.load[ex] : 0.f;
+    const Run r = run_of<G>(j, gl, E);
+    const float v = a.load[max(r.at + (j & 3), 0)];
+    load[j] = r.has(j & 3) ? v : 0.f;
   }
   const float n = a.stats[3];
   const float gain = n > 0.f ? (a.dloss ? *a.dloss : 1.0f) / n : 0.f;
@@ -376,7 +474,10 @@ __global__ __launch_bounds__(256) void balance_grad_kernel(BalanceGradArgs a) {
     const char* zr = static_cast<const char*>(a.logits) + (in ? row : 0) * a.z_stride * value_size<ZT>();
     float p[NE];
 #pragma unroll
-    for (int j = 0; j < NE; j += 4) load4<ZT>(zr, expert_of<G>(j, gl), E, p + j);
+    for (int j = 0; j < NE; j += 4) unpack4<ZT>(load_run<ZT, NE>(zr, run_of<G>(j, gl, E), E), p + j);
+#pragma unroll
+    for (int j = 0; j < NE; ++j)
+      if (!surely<G, NE>(j)) p[j] = run_of<G>(j, gl, E).has(j & 3) ? p[j] : kMinusInf;
     const float lse = in ? a.lse[row] : kMinusInf;
     const bool counted = lse != kMinusInf;
     // the softmax again as in the forward pass, not exp(z - lse): beside a
@@ -400,21 +501,14 @@ __global__ __launch_bounds__(256) void balance_grad_kernel(BalanceGradArgs a) {
       char* dr = static_cast<char*>(a.dlogits) + row * a.d_stride * (a.d_type == MOE_F32 ? 4 : 2);
 #pragma unroll
       for (int j = 0; j < NE; j += 4) {
-        const int ex = expert_of<G>(j, gl);
-        if (ex >= E) continue;
-        float d[4], old[4] = {0.f, 0.f, 0.f, 0.f};
+        const Run r = run_of<G>(j, gl, E);
+        if (!surely<G, NE>(j) && r.skip >= 4) continue;
+        float d[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) d[i] = counted ? scale * p[j + i] * fmaf(a.balance, load[j + i] - inner, rest) : 0.f;
-        if (a.accumulate) {
-          if (a.d_type == MOE_F32) load4<MOE_F32>(dr, ex, E, old);
-          else if (a.d_type == MOE_F16) load4<MOE_F16>(dr, ex, E, old);
-          else load4<MOE_BF16>(dr, ex, E, old);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) d[i] += old[i];
-        }
-        if (a.d_type == MOE_F32) store4<MOE_F32>(dr, ex, E, d);
-        else if (a.d_type == MOE_F16) store4<MOE_F16>(dr, ex, E, d);
-        else store4<MOE_BF16>(dr, ex, E, d);
+        if (a.d_type == MOE_F32) put_run<MOE_F32, NE>(dr, r, E, a.accumulate, d);
+        else if (a.d_type == MOE_F16) put_run<MOE_F16, NE>(dr, r, E, a.accumulate, d);
+        else put_run<MOE_BF16, NE>(dr, r, E, a.accumulate, d);
       }
     }
   }
@@ -431,7 +525,8 @@ hipError_t launch_rows(const BalanceArgs& a, hipStream_t s) {
   hipError_t e = a.k <= 8 ? launch(balance_rows_kernel<ZT, G, NE, true>, dim3(blocks), dim3(256), l, a)
                           : launch(balance_rows_kernel<ZT, G, NE, false>, dim3(blocks), dim3(256), l, a);
   if (e != hipSuccess) return e;
-  return launch(balance_finish_kernel, dim3((a.E + kFinishExperts - 1) / kFinishExperts), dim3(256), l, a, blocks);
+  return launch(balance_finish_kernel, dim3((a.E + kFinishExperts - 1) / kFinishExperts),
+                dim3(kFinishExperts * kSlices), l, a, blocks);
 }
 template <int ZT, int G, int NE>
 hipError_t launch_grad(const BalanceGradArgs& a, hipStream_t s) {
