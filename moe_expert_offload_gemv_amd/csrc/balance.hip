@@ -255,8 +255,10 @@ __device__ __forceinline__ uint32_t kth_bits(const uint32_t (&b)[NE], int k, int
   }
 }
 
+// Two waves a SIMD hide each other's latencies (one: 30 us for 32768 x 512 fp32);
+// 64 experts a lane do not fit in that many registers.
 template <int ZT, int G, int NE, bool TOP8>
-__global__ __launch_bounds__(256) void balance_rows_kernel(BalanceArgs a) {
+__global__ __launch_bounds__(256, NE <= 32 ? 2 : 1) void balance_rows_kernel(BalanceArgs a) {
   __shared__ float s_p[NE * G];
   __shared__ int s_c[NE * G];
   __shared__ float s_z[4];
@@ -332,11 +334,14 @@ __global__ __launch_bounds__(256) void balance_rows_kernel(BalanceArgs a) {
     } else {
       // more equal logits than places: the lowest ids of them, one by one
       int left = k - above, last = -1;
+      // its compares stay in here: kept from row to row they would take all scalar registers
+      int gt = gl;
+      asm volatile("" : "+v"(gt));
       while (__ballot(left > 0)) {
         int id = 0x7FFFFFFF;
 #pragma unroll
         for (int j = 0; j < NE; ++j) {
-          const int ex = run_of<G>(j, gl, E).at + (j & 3);
+          const int ex = run_of<G>(j, gt, E).at + (j & 3);
           if (b[j] == m && ex > last) id = min(id, ex);
         }
         id = 0x7FFFFFFF - (int)group_max<G>((uint32_t)(0x7FFFFFFF - id));
@@ -345,7 +350,7 @@ __global__ __launch_bounds__(256) void balance_rows_kernel(BalanceArgs a) {
       }
 #pragma unroll
       for (int j = 0; j < NE; ++j) {
-        const bool yes = b[j] > m || (b[j] == m && run_of<G>(j, gl, E).at + (j & 3) <= last);
+        const bool yes = b[j] > m || (b[j] == m && run_of<G>(j, gt, E).at + (j & 3) <= last);
         c[j] += counted && yes ? 1 : 0;
       }
     }
