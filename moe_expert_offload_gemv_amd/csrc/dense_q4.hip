@@ -837,6 +837,35 @@ constexpr int wide_side(int WK) { return WK == 1 ? 128 : 64; }
 // s_waitcnt immediate (GFX9 encoding) waiting for vmcnt <= n only
 constexpr int waitcnt_vm(int n) { return (n & 15) | (7 << 4) | (15 << 8) | ((n >> 4) << 14); }
 
+// What step_ready does, through LDS: a wave writes a tile's words and scales as
+// loaded, lane (feature, block), and reads chunk c of every block back; the wave's
+// own accesses are in order, no wait in between. Beside matrix products that take
+// the place of register moves this saves 140 instructions a step
+// (4096 x 5120 x 4096 bf16: 288 us with the moves). Block b of feature f lies in
+// quarter b ^ (f >> 2) of the feature's 64 bytes: without conflicts either way.
+constexpr int kTurnBytes = 1024 + 256;
+struct Turn {
+  uint8_t *write_w, *write_d;
+  const uint8_t *read_w[4], *read_d;
+  static __device__ __forceinline__ Turn make(uint8_t* s, int lane) {
+    const int col = lane & 15, c = lane >> 4;
+    Turn t;
+    t.write_w = s + (lane >> 2) * 64 + ((lane & 3) ^ (lane >> 4)) * 16;
+    t.write_d = s + 1024 + lane * 4;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) t.read_w[i] = s + col * 64 + (i ^ (col >> 2)) * 16 + c * 4;
+    t.read_d = s + 1024 + col * 16;
+    return t;
+  }
+  __device__ __forceinline__ void step(const StepWeights& st, int s, int lane, int KB, uint32_t (&w)[4], float (&d)[4]) const {
+    *reinterpret_cast<u32x4_t*>(write_w) = st.w;
+    *reinterpret_cast<float*>(write_d) = 4 * s + (lane & 3) < KB ? half_to_float((uint16_t)st.d) : 0.f;
+    const f32x4_t v = *reinterpret_cast<const f32x4_t*>(read_d);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const uint32_t*>(read_w[i]), d[i] = v[i];
+  }
+};
+
 template <int XT, int SB, int WK, int RING>
 __global__ __launch_bounds__(256, 2) void q4_wide_kernel(Q4Args a, Operand o, int row_tiles, int col_tiles) {
   constexpr int TERMS = terms_of<XT>(), SIDE = wide_side(WK), MG = SIDE / 16;  // row tiles of 16 in the stages
@@ -844,9 +873,10 @@ __global__ __launch_bounds__(256, 2) void q4_wide_kernel(Q4Args a, Operand o, in
   constexpr int kSums = WK > 1 ? WK * 16 * 64 * 16 : 0;
   constexpr int kLds = RING * kStage * WK;
   static_assert(RING == 2 || SB == 1, "the ring's waits count blocks");
-  __shared__ __attribute__((aligned(1024))) uint8_t s_lds[kLds > kSums ? kLds : kSums];
+  __shared__ __attribute__((aligned(1024))) uint8_t s_lds[kLds + 4 * kTurnBytes > kSums ? kLds + 4 * kTurnBytes : kSums];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 15, c = lane >> 4;
+  const Turn turn = Turn::make(s_lds + kLds + wave * kTurnBytes, lane);
   // work-groups go round the 8 XCDs: each XCD takes a run of the tiles, in
   // groups of 8 row tiles by all column tiles, so that the tiles it works on at
   // a time share operand rows and weights in its L2
@@ -938,7 +968,7 @@ __global__ __launch_bounds__(256, 2) void q4_wide_kernel(Q4Args a, Operand o, in
       __builtin_amdgcn_sched_barrier(0);
       if (h == 0) {
 #pragma unroll
-        for (int t = 0; t < 4; ++t) step_ready(wn[t], s, lane, KB, w[t], d[t]);
+        for (int t = 0; t < 4; ++t) turn.step(wn[t], s, lane, KB, w[t], d[t]);
         issue_weights(min(s + WK, last));
       }
       const int ahead = h + RING - 1;  // in stages from the step's first
@@ -1002,7 +1032,7 @@ __global__ __launch_bounds__(256, 2) void q4_wide_kernel(Q4Args a, Operand o, in
         if (row >= a.T) continue;
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
-          const int f = f0 + 16 * t + column_of(col);
+          const int f = f0 + 16 * t + col;
           if (f < a.N) put(a, row, f, acc[m][t][r]);
         }
       }
@@ -1022,7 +1052,7 @@ __global__ __launch_bounds__(256, 2) void q4_wide_kernel(Q4Args a, Operand o, in
       const int64_t row = (int64_t)rt * SIDE + tok;
       if (row >= a.T || f0 + f >= a.N) continue;
       const float* p = reinterpret_cast<const float*>(s_sum) +
-                       ((tok / 16 * 4 + f / 16) * 64 + 16 * (tok / 4 % 4) + column_of(f % 16)) * 4 + tok % 4;
+                       ((tok / 16 * 4 + f / 16) * 64 + 16 * (tok / 4 % 4) + f % 16) * 4 + tok % 4;
       float v = 0.f;
 #pragma unroll
       for (int w = 0; w < WK; ++w) v += p[w * 16 * 256];
