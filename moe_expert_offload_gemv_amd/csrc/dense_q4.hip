@@ -841,7 +841,7 @@ constexpr int waitcnt_vm(int n) { return (n & 15) | (7 << 4) | (15 << 8) | ((n >
 // loaded, lane (feature, block), and reads chunk c of every block back; the wave's
 // own accesses are in order, no wait in between. Beside matrix products that take
 // the place of register moves this saves 140 instructions a step
-// (4096 x 5120 x 4096 bf16: 288 us with the moves). Block b of feature f lies in
+// (4096 x 5120 x 4096 bf16: 302 us with the moves, 285 so). Block b of feature f lies in
 // quarter b ^ (f >> 2) of the feature's 64 bytes: without conflicts either way.
 constexpr int kTurnBytes = 1024 + 256;
 struct Turn {
@@ -1072,14 +1072,14 @@ hipError_t launch_operand(const Q4Args& a, const Operand& o, hipStream_t s) {
 constexpr int64_t kPassTokens = 16384;
 
 // 0: one launch without an operand pass; else the WK of the wide tiles.
-// Below about 2e9 products the one launch wins, whatever their shape (event times,
-// bf16: 128 x 2048 x 2048, 0.5e9, 11.8 us against 20.8; 64 x 5120 x 4096, 1.3e9, 23 against 29;
-// 128 x 5120 x 4096, 2.7e9, 33 against 30; 200 x 5120 x 4096, 53 against 42). Whole 128 x 128 tiles
-// pay from two work-groups per CU on (1024 x 5120 x 4096, 320 tiles, 121 us against 97 split; 2048 tokens,
-// 640 tiles, 180 either way; 4096 tokens, 1280 tiles, 290 against 318).
+// Below about 2e9 products the one launch wins, whatever their shape (bf16, us on the GPU:
+// 128 x 2048 x 2048, 0.5e9, 10.4 against 16.7 split; 64 x 5120 x 4096, 1.3e9, 21.5 against 24.6;
+// 300 x 1024 x 8192, 2.5e9, 37.8 against 39.6; 128 x 5120 x 4096, 2.7e9, 33.0 against 25.2). Whole
+// 128 x 128 tiles pay from four work-groups per CU on (1024 x 5120 x 4096, 320 tiles, 107 against
+// 80 split; 2048 tokens, 640 tiles, 161 against 153; 4096 tokens, 1280 tiles, 275 against 306).
 int wide_split(int64_t T, int64_t N, int64_t K) {
   if (T <= 32 || (double)T * (double)N * (double)K <= 2e9) return 0;
-  return ((T + 127) / 128) * ((N + 127) / 128) >= 512 ? 1 : 4;
+  return ((T + 127) / 128) * ((N + 127) / 128) >= 1024 ? 1 : 4;
 }
 
 template <int XT, int WK>

@@ -211,7 +211,7 @@ Q4_SHAPES = [(1, 1, 32), (1, 16, 32), (1, 2048, 2048), (1, 33, 96), (2, 17, 1056
              (128, 128, 128), (129, 127, 1024), (200, 512, 96), (256, 300, 640), (257, 70, 1312), (300, 260, 256),
              (515, 129, 416), (1030, 140, 128)]
 # above 2e9 products: 64 x 64 tiles with the reduction split, 128 x 128 tiles, and those in two passes of tokens
-Q4_LARGE = [(130, 2050, 8224), (2100, 3900, 256), (16500, 520, 256)]
+Q4_LARGE = [(130, 2050, 8224), (2100, 3900, 256), (16500, 520, 256), (4100, 4100, 160), (16500, 1100, 128)]
 
 
 @pytest.mark.parametrize("T,N,K,xt,yt", [s + (x, y) for s in Q4_SHAPES for x, y in
