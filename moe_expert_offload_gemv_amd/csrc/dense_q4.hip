@@ -40,14 +40,21 @@ typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 
-// wide tiles: bf16 terms an activation is split into, and the operands' type
+// Terms an activation is split into, and the operands' type: fp32 values are
+// cut into three of bf16; 8-bit codes stay one exact fp16 term and their scales
+// join the scale FMAs (880 x 3470 x 4992: Q8_FIGURES).
 template <int XT>
 constexpr int op_of() {
-  return XT == MOE_F16 ? MOE_F16 : MOE_BF16;
+  return XT == MOE_F16 || XT == MOE_Q8_32 ? MOE_F16 : MOE_BF16;
 }
 template <int XT>
 constexpr int terms_of() {
-  return XT == MOE_F32 || XT == MOE_Q8_32 ? 3 : 1;
+  return XT == MOE_F32 ? 3 : 1;
+}
+// runs of 16 floats beside a unit's operand: -24 sums, and the scales of codes
+template <int XT>
+constexpr int runs_of() {
+  return XT == MOE_Q8_32 ? 2 : 1;
 }
 
 // OP: the 16-bit type of the products' operands, MOE_F16 or MOE_BF16
@@ -155,42 +162,36 @@ __device__ __forceinline__ void codes_to_half(uint32_t codes, uint32_t& even, ui
 }
 
 // The values of chunk c of a block of a row, elements 4c .. 4c + 3 and 16 + 4c
-// .. 16 + 4c + 3, as loaded; scale: of 8-bit codes.
+// .. 16 + 4c + 3, as loaded.
 template <int XT>
 struct RawChunk {
   uint32_t lo[XT == MOE_F32 ? 4 : XT == MOE_Q8_32 ? 1 : 2], hi[XT == MOE_F32 ? 4 : XT == MOE_Q8_32 ? 1 : 2];
-  float scale;
 };
 template <int XT>
-__device__ __forceinline__ RawChunk<XT> load_chunk(const char* row, const float* scale, int64_t b, int c) {
+__device__ __forceinline__ RawChunk<XT> load_chunk(const char* row, int64_t b, int c) {
   RawChunk<XT> r;
   const char* p = row + (32 * b + 4 * c) * value_size<XT>();
   __builtin_memcpy(r.lo, p, 4 * value_size<XT>());
   __builtin_memcpy(r.hi, p + 16 * value_size<XT>(), 4 * value_size<XT>());
-  if constexpr (XT == MOE_Q8_32) r.scale = scale[b];
   return r;
 }
 
-// Its operand, in the slots' order: 16-bit values, or fp32 values (scale * code)
+// Its operand, in the slots' order: 16-bit values, codes as fp16, or fp32 values
 // cut into bf16 terms.
 template <int XT, int TERMS>
 __device__ __forceinline__ void chunk_terms(const RawChunk<XT>& r, u32x4_t (&t)[TERMS]) {
   if constexpr (XT == MOE_F16 || XT == MOE_BF16) {
     t[0] = u32x4_t{lower_halves(r.lo[0], r.lo[1]), upper_halves(r.lo[0], r.lo[1]), lower_halves(r.hi[0], r.hi[1]),
                    upper_halves(r.hi[0], r.hi[1])};
+  } else if constexpr (XT == MOE_Q8_32) {
+    uint32_t h[4];
+    codes_to_half(r.lo[0], h[0], h[1]);
+    codes_to_half(r.hi[0], h[2], h[3]);
+    t[0] = u32x4_t{h[0], h[1], h[2], h[3]};
   } else {
     float v[8];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if constexpr (XT == MOE_F32) {
-        v[j] = __uint_as_float(r.lo[j]);
-        v[4 + j] = __uint_as_float(r.hi[j]);
-      } else {
-        v[j] = (float)(int8_t)(r.lo[0] >> (8 * j));
-        v[4 + j] = (float)(int8_t)(r.hi[0] >> (8 * j));
-        v[j] *= r.scale, v[4 + j] *= r.scale;
-      }
-    }
+    for (int j = 0; j < 4; ++j) v[j] = __uint_as_float(r.lo[j]), v[4 + j] = __uint_as_float(r.hi[j]);
 #pragma unroll
     for (int k = 0; k < TERMS; ++k) {
       uint32_t u[8];
@@ -213,7 +214,7 @@ __device__ __forceinline__ float chunk_sum(const u32x4_t (&t)[TERMS]) {
   for (int k = TERMS - 1; k >= 0; --k)
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      if constexpr (XT == MOE_F16)
+      if constexpr (op_of<XT>() == MOE_F16)
         sum += half_to_float((uint16_t)t[k][i]) + half_to_float((uint16_t)(t[k][i] >> 16));
       else
         sum += __uint_as_float(t[k][i] << 16) + __uint_as_float(t[k][i] & 0xFFFF0000u);
@@ -411,12 +412,17 @@ __device__ __forceinline__ float row_sums(const float (&v)[V]) {
 
 constexpr int kDotWaves = 4;
 
-// T: tokens held, at least those there are (the last one again, never stored)
-template <int XT, int LPR, int BPL, int T, int NR>
+// T: tokens held, at least those there are (the last one again, never stored).
+// KS = 4: a row of more blocks than a wave's registers hold tokens for is shared
+// by the work-group's waves, which add up through LDS (KS_FIGURES).
+template <int XT, int LPR, int BPL, int T, int NR, int KS>
 __global__ __launch_bounds__(64 * kDotWaves) void q4_dot_kernel(Q4Args a) {
   constexpr int RPW = 64 / LPR;  // rows side by side
-  const int lane = threadIdx.x & 63, lb = lane & (LPR - 1), side = lane / LPR;
+  __shared__ float s_sum[KS > 1 ? 2 : 1][KS > 1 ? kDotWaves : 1][64];
+  static_assert(KS == 1 || (KS == kDotWaves && LPR == 64), "a row's slices: the waves of its work-group");
+  const int lane = threadIdx.x & 63, side = lane / LPR;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int lb = (lane & (LPR - 1)) + (KS > 1 ? wave * LPR * BPL : 0);  // the lane's first block
   const int KB = (int)(a.K / 32), N = (int)a.N;
   const u32x4_t* nib = static_cast<const u32x4_t*>(a.nibbles);
   u32x4_t w[NR][BPL];
@@ -433,8 +439,9 @@ __global__ __launch_bounds__(64 * kDotWaves) void q4_dot_kernel(Q4Args a) {
       }
     }
   };
-  const int groups = (N + NR * RPW - 1) / (NR * RPW), stride = gridDim.x * kDotWaves;
-  int g = blockIdx.x * kDotWaves + wave;
+  const int groups = (N + NR * RPW - 1) / (NR * RPW), stride = gridDim.x * (kDotWaves / KS);
+  int g = KS > 1 ? blockIdx.x : blockIdx.x * kDotWaves + wave;
+  int turn = 0;
   issue(g);
   BlockX<XT> x[BPL][T];
 #pragma unroll
@@ -467,29 +474,41 @@ __global__ __launch_bounds__(64 * kDotWaves) void q4_dot_kernel(Q4Args a) {
     float flat[NR * T];
 #pragma unroll
     for (int i = 0; i < NR * T; ++i) flat[i] = acc[i % NR][i / NR];
-    const float v = row_sums<LPR>(flat);
-    const int64_t row = ((int64_t)g * NR + lb % NR) * RPW + side;
-    if (lb < NR * (int)a.T && row < N) put(a, lb / NR, row, v);
+    float v = row_sums<LPR>(flat);
+    if constexpr (KS > 1) {
+      // every wave of the work-group has the same groups; a buffer is written again
+      // only past the next barrier, when its reader has its values
+      s_sum[turn][wave][lane] = v;
+      __syncthreads();
+      v = 0.f;
+#pragma unroll
+      for (int w = 0; w < KS; ++w) v += s_sum[turn][w][lane];
+      turn ^= 1;
+    }
+    const int i = lane & (LPR - 1);
+    const int64_t row = ((int64_t)g * NR + i % NR) * RPW + side;
+    if (i < NR * (int)a.T && row < N && (KS == 1 || wave == 0)) put(a, i / NR, row, v);
   }
 }
 
-template <int XT, int LPR, int BPL, int T, int NR>
+template <int XT, int LPR, int BPL, int T, int NR, int KS>
 hipError_t launch_dot_rows(const Q4Args& a, hipStream_t s) {
-  constexpr int RPW = 64 / LPR;
+  constexpr int RPW = 64 / LPR, GPW = kDotWaves / KS;  // rows side by side, groups of a work-group at a time
   static_assert(NR * T <= LPR && NR * T <= 8, "a lane per output of a row group");
   // as many work-groups as a CU holds at about this many registers, every wave
   // the same number of row groups
   constexpr int kRegs = 32 + BPL * T * (BlockX<XT>::WORDS + 2) + 7 * NR * BPL;
-  constexpr int kWaves = 256 * kDotWaves * std::max(1, std::min(8, 512 / kRegs));
-  const int64_t groups = (a.N + NR * RPW - 1) / (NR * RPW), rounds = (groups + kWaves - 1) / kWaves;
-  const dim3 grid((unsigned)((groups + kDotWaves * rounds - 1) / (kDotWaves * rounds)));
-  return launch(q4_dot_kernel<XT, LPR, BPL, T, NR>, grid, dim3(64 * kDotWaves), Launch{s}, a);
+  constexpr int kGroups = 256 * GPW * std::max(1, std::min(8, 512 / kRegs));
+  const int64_t groups = (a.N + NR * RPW - 1) / (NR * RPW), rounds = (groups + kGroups - 1) / kGroups;
+  const dim3 grid((unsigned)((groups + GPW * rounds - 1) / (GPW * rounds)));
+  return launch(q4_dot_kernel<XT, LPR, BPL, T, NR, KS>, grid, dim3(64 * kDotWaves), Launch{s}, a);
 }
-template <int XT, int LPR, int BPL, int T>
+template <int XT, int LPR, int BPL, int T, int KS>
 hipError_t launch_dot(const Q4Args& a, hipStream_t s) {
   // rows in flight: 64 bytes per lane; up to 8192 rows one at a time, so that every CU has some
   constexpr int kMany = std::max(1, std::min(4 / BPL, 8 / T));
-  return a.N <= 8192 ? launch_dot_rows<XT, LPR, BPL, T, 1>(a, s) : launch_dot_rows<XT, LPR, BPL, T, kMany>(a, s);
+  return a.N <= 8192 / KS ? launch_dot_rows<XT, LPR, BPL, T, 1, KS>(a, s)
+                          : launch_dot_rows<XT, LPR, BPL, T, kMany, KS>(a, s);
 }
 
 // tokens times blocks per lane whose values the kernel keeps in registers
@@ -497,36 +516,44 @@ template <int XT>
 constexpr int dot_limit() {
   return XT == MOE_F32 ? 2 : XT == MOE_Q8_32 ? 12 : 4;
 }
-template <int XT, int LPR, int BPL>
+template <int XT, int LPR, int BPL, int KS>
 hipError_t launch_dot_tokens(const Q4Args& a, hipStream_t s) {
   constexpr int L = dot_limit<XT>() / BPL;
-  if (a.T <= 1) return launch_dot<XT, LPR, BPL, 1>(a, s);
+  if constexpr (L >= 1)
+    if (a.T <= 1) return launch_dot<XT, LPR, BPL, 1, KS>(a, s);
   if constexpr (L >= 2)
-    if (a.T <= 2) return launch_dot<XT, LPR, BPL, 2>(a, s);
+    if (a.T <= 2) return launch_dot<XT, LPR, BPL, 2, KS>(a, s);
   if constexpr (L >= 4)
-    if (a.T <= 4) return launch_dot<XT, LPR, BPL, 4>(a, s);
+    if (a.T <= 4) return launch_dot<XT, LPR, BPL, 4, KS>(a, s);
   if constexpr (L >= 6)
-    if (a.T <= 6) return launch_dot<XT, LPR, BPL, 6>(a, s);
+    if (a.T <= 6) return launch_dot<XT, LPR, BPL, 6, KS>(a, s);
   return hipErrorInvalidValue;
 }
+// blocks per lane, of a row of KB blocks shared by lanes of one wave, or by four
+constexpr int kNoDot = 1 << 20;
+constexpr int dot_blocks(int64_t KB) {
+  return KB <= 16 ? 1 : KB <= 32 ? 2 : KB <= 64 ? 1 : KB <= 128 ? 2 : KB <= 256 ? 4 : kNoDot;
+}
+constexpr int split_blocks(int64_t KB) { return KB <= 64 ? kNoDot : KB <= 256 ? 1 : KB <= 512 ? 2 : KB <= 1024 ? 4 : kNoDot; }
+// slices of a row in the dot kernel, 0: it has no room for the tokens
 template <int XT>
-int dot_blocks(int64_t KB) {  // per lane
-  return KB <= 16 ? 1 : KB <= 32 ? 2 : KB <= 64 ? 1 : KB <= 128 ? 2 : KB <= 256 ? 4 : 1 << 20;
+int dot_slices(const Q4Args& a) {
+  const int64_t T = a.T <= 2 ? a.T : a.T <= 4 ? 4 : a.T <= 6 ? 6 : 1 << 10, KB = a.K / 32;
+  return T * dot_blocks(KB) <= dot_limit<XT>() ? 1 : T * split_blocks(KB) <= dot_limit<XT>() ? 4 : 0;
 }
 template <int XT>
-bool dot_fits(const Q4Args& a) {
-  const int64_t T = a.T <= 2 ? a.T : a.T <= 4 ? 4 : a.T <= 6 ? 6 : 1 << 10;
-  return T * dot_blocks<XT>(a.K / 32) <= dot_limit<XT>();
-}
-template <int XT>
-hipError_t launch_dot_types(const Q4Args& a, hipStream_t s) {
+hipError_t launch_dot_types(const Q4Args& a, int slices, hipStream_t s) {
   const int64_t KB = a.K / 32;
-  if (KB <= 16) return launch_dot_tokens<XT, 16, 1>(a, s);
-  if (KB <= 32) return launch_dot_tokens<XT, 16, 2>(a, s);
-  if (KB <= 64) return launch_dot_tokens<XT, 64, 1>(a, s);
-  if (KB <= 128) return launch_dot_tokens<XT, 64, 2>(a, s);
-  if constexpr (dot_limit<XT>() >= 4) return launch_dot_tokens<XT, 64, 4>(a, s);
-  return hipErrorInvalidValue;
+  if (slices == 4) {
+    if (KB <= 256) return launch_dot_tokens<XT, 64, 1, 4>(a, s);
+    if (KB <= 512) return launch_dot_tokens<XT, 64, 2, 4>(a, s);
+    return launch_dot_tokens<XT, 64, 4, 4>(a, s);
+  }
+  if (KB <= 16) return launch_dot_tokens<XT, 16, 1, 1>(a, s);
+  if (KB <= 32) return launch_dot_tokens<XT, 16, 2, 1>(a, s);
+  if (KB <= 64) return launch_dot_tokens<XT, 64, 1, 1>(a, s);
+  if (KB <= 128) return launch_dot_tokens<XT, 64, 2, 1>(a, s);
+  return launch_dot_tokens<XT, 64, 4, 1>(a, s);
 }
 
 // The weights of one step, four blocks of 16 features, as loaded: lane l has
@@ -583,20 +610,9 @@ __device__ __forceinline__ void step_ready(const StepWeights& st, int s, int lan
 
 constexpr int kWaves = 8;
 
-// 8-bit codes stay one exact fp16 term here and their scales join the scale
-// FMAs: a third of the LDS and of the products
-template <int XT>
-constexpr int tile_terms() {
-  return XT == MOE_F32 ? 3 : 1;
-}
-template <int XT>
-constexpr int tile_op() {
-  return XT == MOE_F16 || XT == MOE_Q8_32 ? MOE_F16 : MOE_BF16;
-}
-
 template <int XT, int KW, int CB>
 __global__ __launch_bounds__(64 * kWaves, 2) void q4_tile_kernel(Q4Args a, int token_tiles) {
-  constexpr int TERMS = tile_terms<XT>(), OP = tile_op<XT>(), FW = kWaves / KW, ROWS = 16, THREADS = 64 * kWaves;
+  constexpr int TERMS = terms_of<XT>(), OP = op_of<XT>(), FW = kWaves / KW, ROWS = 16, THREADS = 64 * kWaves;
   constexpr bool Q8 = XT == MOE_Q8_32;
   constexpr int UPB = 2 * value_size<XT>();               // 16-byte units of a block of x
   constexpr int UNITS = ROWS * CB * UPB / THREADS;        // a thread's units of a chunk
@@ -779,15 +795,15 @@ hipError_t launch_tile_types(const Q4Args& a, hipStream_t s) {
 struct Operand {
   int64_t rows, KB, bytes;  // padded tokens, padded blocks, bytes with the sums
   uint8_t* terms;
-  float* base;              // [rows / 16][KB][16]
-  __host__ __device__ static Operand make(uint8_t* ws, int64_t T, int64_t K, int n_terms, int tile_rows) {
+  float* base;              // [rows / 16][KB][runs][16]
+  __host__ __device__ static Operand make(uint8_t* ws, int64_t T, int64_t K, int n_terms, int runs, int tile_rows) {
     Operand o;
     o.rows = (T + tile_rows - 1) / tile_rows * tile_rows;
     o.KB = (K / 32 + 3) / 4 * 4;
     const int64_t units = o.rows / 16 * o.KB;
     o.terms = ws;
     o.base = reinterpret_cast<float*>(ws + units * n_terms * 1024);
-    o.bytes = units * (n_terms * 1024 + 64);
+    o.bytes = units * (n_terms * 1024 + runs * 64);
     return o;
   }
 };
@@ -804,16 +820,16 @@ __global__ __launch_bounds__(256) void q4_operand_kernel(Q4Args a, Operand o) {
   float sum;
 #pragma unroll
   for (int k = 0; k < TERMS; ++k) t[k] = u32x4_t{0, 0, 0, 0};
-  if (row < a.T && b < a.K / 32)
-    chunk_terms<XT>(load_chunk<XT>(static_cast<const char*>(a.x) + row * a.x_stride * value_size<XT>(),
-                                   XT == MOE_Q8_32 ? a.x_scales + row * a.x_scales_stride : nullptr, b, c),
-                    t);
+  const bool in = row < a.T && b < a.K / 32;
+  if (in)
+    chunk_terms<XT>(load_chunk<XT>(static_cast<const char*>(a.x) + row * a.x_stride * value_size<XT>(), b, c), t);
   sum = chunk_sum<XT>(t);
   sum += __shfl_xor(sum, 16, 64);
   sum += __shfl_xor(sum, 32, 64);
 #pragma unroll
   for (int k = 0; k < TERMS; ++k) reinterpret_cast<u32x4_t*>(o.terms)[(unit * TERMS + k) * 64 + lane] = t[k];
-  if (c == 0) o.base[unit * 16 + r] = -24.0f * sum;
+  if (c == 0) o.base[unit * 16 * runs_of<XT>() + r] = -24.0f * sum;
+  if (XT == MOE_Q8_32 && c == 0) o.base[unit * 32 + 16 + r] = in ? a.x_scales[row * a.x_scales_stride + b] : 0.f;
 }
 
 // ---------------------------------------------------------------------------
@@ -869,7 +885,8 @@ struct Turn {
 template <int XT, int SB, int WK, int RING>
 __global__ __launch_bounds__(256, 2) void q4_wide_kernel(Q4Args a, Operand o, int row_tiles, int col_tiles) {
   constexpr int TERMS = terms_of<XT>(), SIDE = wide_side(WK), MG = SIDE / 16;  // row tiles of 16 in the stages
-  constexpr int kTermBytes = MG * SB * TERMS * 1024, kBaseBytes = MG * SB * 64, kStage = kTermBytes + kBaseBytes;
+  constexpr int RUNS = runs_of<XT>(), kBlockBase = 64 * RUNS;
+  constexpr int kTermBytes = MG * SB * TERMS * 1024, kBaseBytes = MG * SB * kBlockBase, kStage = kTermBytes + kBaseBytes;
   constexpr int kSums = WK > 1 ? WK * 16 * 64 * 16 : 0;
   constexpr int kLds = RING * kStage * WK;
   static_assert(RING == 2 || SB == 1, "the ring's waits count blocks");
@@ -916,14 +933,14 @@ __global__ __launch_bounds__(256, 2) void q4_wide_kernel(Q4Args a, Operand o, in
       const uint8_t* src = o.terms + ((u0 + m * o.KB + b0) * TERMS + q) * 1024 + 16 * lane;
       __builtin_amdgcn_global_load_lds((glb_void_t*)src, (lds_void_t*)(dst + (m * kRun + q) * 1024), 16, 0, 0);
     }
-    // the sums: 64 SB bytes per row tile, 1 KiB per copy
-    constexpr int kLanes = 4 * SB;  // lanes of a row tile
+    // the sums (and scales): 1 KiB per copy
+    constexpr int kLanes = 4 * SB * RUNS;  // lanes of a row tile
 #pragma unroll
     for (int i = 0; i < (kBaseBytes + 1023) / 1024; ++i) {
       if (WK == 1 && wave != i) continue;
       const int at = 64 * i + lane, m = at / kLanes;
       if (m < MG) {
-        const uint8_t* src = reinterpret_cast<const uint8_t*>(o.base + (u0 + m * o.KB + b0) * 16) + 16 * (at % kLanes);
+        const uint8_t* src = reinterpret_cast<const uint8_t*>(o.base + (u0 + m * o.KB + b0) * 16 * RUNS) + 16 * (at % kLanes);
         __builtin_amdgcn_global_load_lds((glb_void_t*)src, (lds_void_t*)(dst + kTermBytes + 1024 * i), 16, 0, 0);
       }
     }
@@ -978,21 +995,22 @@ __global__ __launch_bounds__(256, 2) void q4_wide_kernel(Q4Args a, Operand o, in
       // cores), beside them the scale FMAs of the tile before (VALU) and the
       // next tile's weights; the operand of the next block is read ahead.
       u32x4_t x[2][4][TERMS];
-      f32x4_t base[2][4], p[2][4];
+      f32x4_t base[2][4], p[2][4], dx[4];
       auto read_block = [&](int i) __attribute__((always_inline)) {
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
 #pragma unroll
           for (int k = 0; k < TERMS; ++k)
             x[i & 1][m][k] = *reinterpret_cast<const u32x4_t*>(st + (((m0 + m) * SB + i) * TERMS + k) * 1024 + 16 * lane);
-          base[i & 1][m] = *reinterpret_cast<const f32x4_t*>(st + kTermBytes + ((m0 + m) * SB + i) * 64 + 16 * c);
+          base[i & 1][m] = *reinterpret_cast<const f32x4_t*>(st + kTermBytes + ((m0 + m) * SB + i) * kBlockBase + 16 * c);
         }
       };
       auto scale = [&](int g, int m) __attribute__((always_inline)) {
         const int t = g & 3;
         const float dt = d[t][SB * h + (g >> 2)];
 #pragma unroll
-        for (int r = 0; r < 4; ++r) acc[m][t][r] = fmaf(dt, p[g & 1][m][r], acc[m][t][r]);
+        for (int r = 0; r < 4; ++r)
+          acc[m][t][r] = fmaf(dt, XT == MOE_Q8_32 ? p[g & 1][m][r] * dx[m][r] : p[g & 1][m][r], acc[m][t][r]);
         // a use of the sums here: otherwise the compiler sinks the scale FMAs to the end of the
         // unrolled blocks and keeps all their products live
         __asm__ volatile("" : "+v"(acc[m][t]));
@@ -1015,6 +1033,8 @@ __global__ __launch_bounds__(256, 2) void q4_wide_kernel(Q4Args a, Operand o, in
           for (int k = 0; k < TERMS; ++k) p[g & 1][m] = mfma<op_of<XT>()>(x[i & 1][m][k], wt[g & 1], p[g & 1][m]);
           if (g + 1 < 4 * SB) wt[(g + 1) & 1][m] = weights_part<op_of<XT>()>(w[(g + 1) & 3][SB * h + ((g + 1) >> 2)], m);
           if (g > 0) scale(g - 1, m);
+          if (XT == MOE_Q8_32 && (g & 3) == 0)  // wanted by the next tile's turn
+            dx[m] = *reinterpret_cast<const f32x4_t*>(st + kTermBytes + ((m0 + m) * SB + i) * kBlockBase + 64 + 16 * c);
           __builtin_amdgcn_sched_barrier(0);
         }
       }
@@ -1093,7 +1113,7 @@ hipError_t launch_wide(const Q4Args& a, hipStream_t s) {
     p.x = static_cast<const char*>(a.x) + t0 * a.x_stride * value_size<XT>();
     p.x_scales = a.x_scales ? a.x_scales + t0 * a.x_scales_stride : nullptr;
     p.y = static_cast<char*>(a.y) + t0 * a.y_stride * (a.y_type == MOE_F32 ? 4 : 2);
-    const Operand o = Operand::make(a.ws, p.T, a.K, TERMS, SIDE);
+    const Operand o = Operand::make(a.ws, p.T, a.K, TERMS, runs_of<XT>(), SIDE);
     if (hipError_t e = launch_operand<XT>(p, o, s); e != hipSuccess) return e;
     const int row_tiles = (int)(o.rows / SIDE);
     const unsigned grid = (unsigned)(((int64_t)row_tiles * col_tiles + 7) / 8 * 8);
@@ -1109,7 +1129,8 @@ hipError_t launch_types(const Q4Args& a, hipStream_t s) {
     case 1: return launch_wide<XT, 1>(a, s);
     case 4: return launch_wide<XT, 4>(a, s);
   }
-  return dot_fits<XT>(a) ? launch_dot_types<XT>(a, s) : launch_tile_types<XT>(a, s);
+  const int slices = dot_slices<XT>(a);
+  return slices ? launch_dot_types<XT>(a, slices, s) : launch_tile_types<XT>(a, s);
 }
 
 }  // namespace
@@ -1117,8 +1138,8 @@ hipError_t launch_types(const Q4Args& a, hipStream_t s) {
 int64_t q4_workspace_bytes(int64_t T, int64_t N, int64_t K, int32_t x_type) {
   const int WK = wide_split(T, N, K);
   if (!WK) return 0;
-  const int terms = x_type == MOE_F32 || x_type == MOE_Q8_32 ? 3 : 1;
-  return Operand::make(nullptr, std::min(T, kPassTokens), K, terms, wide_side(WK)).bytes;
+  const int terms = x_type == MOE_F32 ? terms_of<MOE_F32>() : 1, runs = x_type == MOE_Q8_32 ? runs_of<MOE_Q8_32>() : 1;
+  return Operand::make(nullptr, std::min(T, kPassTokens), K, terms, runs, wide_side(WK)).bytes;
 }
 
 hipError_t launch_q4_matmul(const Q4Args& a, hipStream_t s) {

@@ -210,11 +210,14 @@ Q4_SHAPES = [(1, 1, 32), (1, 16, 32), (1, 2048, 2048), (1, 33, 96), (2, 17, 1056
              (16, 64, 256), (17, 65, 288), (32, 130, 1536), (33, 31, 64), (64, 256, 512), (65, 20, 2080), (100, 1001, 352),
              (128, 128, 128), (129, 127, 1024), (200, 512, 96), (256, 300, 640), (257, 70, 1312), (300, 260, 256),
              (515, 129, 416), (1030, 140, 128)]
+# rows shared by four waves (some with nothing left for the last ones), and the longest of them and past it
+Q4_LONG = [(1, 37, 8224), (1, 2100, 8224), (1, 19, 16384), (1, 20, 32768), (1, 9, 32800), (2, 33, 4128), (2, 50, 8192),
+           (3, 40, 16384), (4, 70, 8128), (6, 30, 16352), (2, 2049, 6368)]
 # above 2e9 products: 64 x 64 tiles with the reduction split, 128 x 128 tiles, and those in two passes of tokens
 Q4_LARGE = [(130, 2050, 8224), (2100, 3900, 256), (16500, 520, 256), (4100, 4100, 160), (16500, 1100, 128)]
 
 
-@pytest.mark.parametrize("T,N,K,xt,yt", [s + (x, y) for s in Q4_SHAPES for x, y in
+@pytest.mark.parametrize("T,N,K,xt,yt", [s + (x, y) for s in Q4_SHAPES + Q4_LONG for x, y in
                                          (("f32", "f32"), ("bf16", "f32"), ("f16", "f32"), ("q8", "f32"),
                                           ("bf16", "bf16"), ("f16", "f16"), ("q8", "bf16"))]
                          + [s + (x, y) for s in Q4_LARGE for x, y in
