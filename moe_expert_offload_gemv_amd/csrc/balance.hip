@@ -6,7 +6,7 @@
 //   balance_finish_kernel  the work-groups' sums, counts, loads and losses
 //   balance_grad_kernel    logits once more: dlogits
 //
-// A token's row is shared by G lanes (16 up to 512 experts, else a wave), so
+// A token's row is shared by G lanes (16, or a wave: lanes_of), so
 // its maximum, sums and top-k are a few DPP steps, and a wave works on 64 / G
 // rows at once. A lane holds NE logits of its row, always of the same experts:
 // the sums over tokens stay in its registers (p and count per expert) until
@@ -31,6 +31,7 @@ using namespace value_dev;
 
 constexpr int kBalanceBlocks = 512;  // work-groups that sum rows, two per CU
 constexpr int kFinishExperts = 32;   // experts per finishing work-group
+constexpr int kWaveRows = 2048;      // rows up to which each has a wave
 constexpr int kMaxExperts = 4096;
 constexpr float kMinusInf = -__builtin_inff();
 
@@ -201,52 +202,72 @@ __device__ __forceinline__ void put_run(char* p, Run r, int E, bool accumulate, 
   store_run<TYPE>(p, r, d);
 }
 
-// The k-th largest of the row's order bits, and how many are larger. k <= 8:
-// each lane sorts its logits eight at a time and keeps its 8 largest, then the
-// lanes of the row merge their lists (sorting networks of route_dev.h): 236
-// instructions for four rows of 256 experts. k > 8: the bits are found from the
-// top one down by counting the logits not below each candidate.
+// the 8 largest order bits of the row that are not above `below`, each lane's
+// eight at a time, then the lanes' lists (sorting networks of route_dev.h)
+template <int G, int NE, bool ALL>
+__device__ __forceinline__ void top8(const uint32_t (&b)[NE], uint32_t below, uint32_t (&t)[8]) {
+  auto at = [&](int j) { return ALL || b[j] <= below ? b[j] : 0u; };
+#pragma unroll
+  for (int j = 0; j < 8; ++j) t[j] = j < NE ? at(j < NE ? j : 0) : 0u;
+  route_dev::sort8_desc(t);
+#pragma unroll
+  for (int o = 8; o < NE; o += 8) {
+    uint32_t u[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) u[j] = at(o + j);
+    route_dev::sort8_desc(u);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) t[j] = max(t[j], u[7 - j]);
+    route_dev::clean8_desc(t);
+  }
+  route_dev::merge8_dpp<route_dev::kDppQuadXor1>(t);
+  route_dev::merge8_dpp<route_dev::kDppQuadXor2>(t);
+  route_dev::merge8_dpp<route_dev::kDppRowHalfMirror>(t);
+  route_dev::merge8_dpp<route_dev::kDppRowMirror>(t);
+  if constexpr (G == 64) {
+    route_dev::merge8_swap<16>(t);
+    route_dev::merge8_swap<32>(t);
+  }
+}
+// t[i] of a descending list, as the least of the first: chosen by index, the list
+// would be moved to LDS
+__device__ __forceinline__ uint32_t pick(const uint32_t (&t)[8], int i) {
+  uint32_t m = t[0];
+#pragma unroll
+  for (int j = 1; j < 8; ++j) m = min(m, j <= i ? t[j] : ~0u);
+  return m;
+}
+// The k-th largest of the row's order bits, and how many are larger. k <= 8: one
+// pass of top8. k > 8: passes of 8 below what the passes before have passed over,
+// equal logits together, until the k-th is among them (1967 x 305, 10 picks: 22 us for forward
+// and gradient, 29 with the bits found one by one; 12288 x 128, 16 picks: 17 and 21.5).
 template <int G, int NE, bool TOP8>
 __device__ __forceinline__ uint32_t kth_bits(const uint32_t (&b)[NE], int k, int& above) {
+  uint32_t t[8], m;
+  above = 0;
   if constexpr (TOP8) {
-    uint32_t t[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) t[j] = j < NE ? b[j < NE ? j : 0] : 0u;
-    route_dev::sort8_desc(t);
-#pragma unroll
-    for (int o = 8; o < NE; o += 8) {
-      uint32_t u[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) u[j] = b[o + j];
-      route_dev::sort8_desc(u);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) t[j] = max(t[j], u[7 - j]);
-      route_dev::clean8_desc(t);
-    }
-    route_dev::merge8_dpp<route_dev::kDppQuadXor1>(t);
-    route_dev::merge8_dpp<route_dev::kDppQuadXor2>(t);
-    route_dev::merge8_dpp<route_dev::kDppRowHalfMirror>(t);
-    route_dev::merge8_dpp<route_dev::kDppRowMirror>(t);
-    if constexpr (G == 64) {
-      route_dev::merge8_swap<16>(t);
-      route_dev::merge8_swap<32>(t);
-    }
-    uint32_t m = t[0];
-#pragma unroll
-    for (int i = 1; i < 8; ++i) m = i < k ? t[i] : m;
-    above = 0;
+    top8<G, NE, true>(b, 0, t);
+    m = pick(t, k - 1);
 #pragma unroll
     for (int i = 0; i < 8; ++i) above += t[i] > m ? 1 : 0;
     return m;
   } else {
-    uint32_t m = 0;
-    for (int o = 31; o >= 0; --o) {
-      const uint32_t c = m | (1u << o);
-      int n = 0;
+    // a row keeps its place while others of the wave go on; at most k / 8 passes,
+    // for each but the last leaves 8 logits or more behind
+    uint32_t below = ~0u;
+    int left = k;  // > 0: the k-th is the left-th of those not above `below`
+    m = 0;
+    do {
+      top8<G, NE, false>(b, below, t);
+      const uint32_t v = pick(t, min(left, 8) - 1);
+      int n = 0;  // of those not above `below`: equal to v or larger
 #pragma unroll
-      for (int j = 0; j < NE; ++j) n += b[j] >= c ? 1 : 0;
-      if (group_sum_int<G>(n) >= k) m = c;
-    }
+      for (int j = 0; j < NE; ++j) n += b[j] >= v && b[j] <= below ? 1 : 0;
+      n = group_sum_int<G>(n);
+      m = left > 0 ? v : m;
+      left -= left > 0 ? n : 0;
+      below = v - 1;  // v > 0: fewer than k logits are above it
+    } while (__ballot(left > 0));
     int n = 0;
 #pragma unroll
     for (int j = 0; j < NE; ++j) n += b[j] > m ? 1 : 0;
@@ -540,9 +561,18 @@ hipError_t launch_grad(const BalanceGradArgs& a, hipStream_t s) {
   return launch(balance_grad_kernel<ZT, G, NE>, dim3((unsigned)std::min<int64_t>(want, 2048)), dim3(256), Launch{s}, a);
 }
 
+// Lanes of a row. Few rows are latency alone: a wave each, with a quarter of the
+// values per lane (forward and gradient, bf16: 91 x 512, 10 picks, 15.4 us against 22.7 with
+// 16 lanes; 2048 x 512, 18.5 against 22.3; 2048 x 256, 8 picks, 14.1 against 14.9; up to 128
+// experts 16 lanes are as quick or quicker: 2048 x 128, 12.6 against 13.5).
+int lanes_of(int64_t T, int E) { return E > 512 || (E > 128 && T <= kWaveRows) ? 64 : 16; }
+
 // f<ZT, G, NE>: the smallest lane share that holds E experts
 #define MOE_BALANCE_SHAPE(f, ZT, a, s)                 \
-  (a.E <= 64     ? f<ZT, 16, 4>(a, s)                  \
+  (a.E <= 512 && lanes_of(a.T, a.E) == 64              \
+       ? (a.E <= 256 ? f<ZT, 64, 4>(a, s)              \
+                     : f<ZT, 64, 8>(a, s))             \
+   : a.E <= 64   ? f<ZT, 16, 4>(a, s)                  \
    : a.E <= 128  ? f<ZT, 16, 8>(a, s)                  \
    : a.E <= 256  ? f<ZT, 16, 16>(a, s)                 \
    : a.E <= 512  ? f<ZT, 16, 32>(a, s)                 \
@@ -553,7 +583,7 @@ hipError_t launch_grad(const BalanceGradArgs& a, hipStream_t s) {
 }  // namespace
 
 int64_t balance_workspace_bytes(int64_t T, int32_t E) {
-  const int blocks = balance_blocks(T, E <= 512 ? 16 : 4);
+  const int blocks = balance_blocks(T, 4 * 64 / lanes_of(T, E));
   return (kOffSums + (int64_t)blocks * 2 * E * 4 + 255) / 256 * 256;
 }
 

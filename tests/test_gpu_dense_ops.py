@@ -388,7 +388,9 @@ class Balance:
 
 BALANCE_SHAPES = [(1, 1, 1), (1, 8, 2), (3, 5, 5), (17, 60, 4), (64, 64, 8), (65, 100, 6), (40, 128, 1), (33, 256, 8),
                   (50, 257, 9), (100, 512, 8), (19, 512, 17), (21, 700, 8), (9, 1024, 32), (11, 1500, 8), (5, 2048, 12),
-                  (7, 4095, 8), (6, 4096, 32), (20000, 16, 2)]
+                  (7, 4095, 8), (6, 4096, 32), (20000, 16, 2),
+                  # 16 lanes a row, not a wave
+                  (2100, 200, 8), (2049, 256, 12), (2500, 300, 8), (2049, 509, 32)]
 
 
 @pytest.mark.parametrize("T,n_e,k", BALANCE_SHAPES)
@@ -406,6 +408,16 @@ def test_router_balance_ties_go_to_the_lower_id(n_e, k):
     z = torch.from_numpy(g.integers(0, 3, (37, n_e)).astype(np.float32))
     z[0] = 0.0
     z[1] = torch.where(torch.arange(n_e) % 2 == 0, 0.0, -0.0)  # equal, whatever the sign of zero
+    Balance(z, k).check()
+
+
+@pytest.mark.parametrize("n_e,k", [(130, 32), (256, 9), (300, 12), (512, 8), (511, 31)])
+def test_router_balance_ties_in_many_rows(n_e, k):
+    g = rng_of(15, n_e, k)
+    z = torch.from_numpy(g.integers(0, 40, (2200, n_e)).astype(np.float32))
+    z[:7] = 0.0
+    z[7] = torch.arange(n_e) // 8  # eight of a kind
+    z[8] = torch.arange(n_e) // 9
     Balance(z, k).check()
 
 
