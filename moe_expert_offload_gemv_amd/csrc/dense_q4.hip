@@ -42,7 +42,7 @@ typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 
 // Terms an activation is split into, and the operands' type: fp32 values are
 // cut into three of bf16; 8-bit codes stay one exact fp16 term and their scales
-// join the scale FMAs (880 x 3470 x 4992: Q8_FIGURES).
+// join the scale FMAs (880 x 3470 x 4992: 85 us, 160 as three terms of scale times code).
 template <int XT>
 constexpr int op_of() {
   return XT == MOE_F16 || XT == MOE_Q8_32 ? MOE_F16 : MOE_BF16;
@@ -414,7 +414,7 @@ constexpr int kDotWaves = 4;
 
 // T: tokens held, at least those there are (the last one again, never stored).
 // KS = 4: a row of more blocks than a wave's registers hold tokens for is shared
-// by the work-group's waves, which add up through LDS (KS_FIGURES).
+// by the work-group's waves, which add up through LDS (1 x 4096 x 14336 bf16: 9.1 us, 24.7 in tiles).
 template <int XT, int LPR, int BPL, int T, int NR, int KS>
 __global__ __launch_bounds__(64 * kDotWaves) void q4_dot_kernel(Q4Args a) {
   constexpr int RPW = 64 / LPR;  // rows side by side
@@ -512,13 +512,13 @@ hipError_t launch_dot(const Q4Args& a, hipStream_t s) {
 }
 
 // tokens times blocks per lane whose values the kernel keeps in registers
-template <int XT>
+template <int XT, int KS>
 constexpr int dot_limit() {
-  return XT == MOE_F32 ? 2 : XT == MOE_Q8_32 ? 12 : 4;
+  return (XT == MOE_F32 ? 2 : XT == MOE_Q8_32 ? 12 : 4) * (KS > 1 && XT != MOE_Q8_32 ? 2 : 1);
 }
 template <int XT, int LPR, int BPL, int KS>
 hipError_t launch_dot_tokens(const Q4Args& a, hipStream_t s) {
-  constexpr int L = dot_limit<XT>() / BPL;
+  constexpr int L = dot_limit<XT, KS>() / BPL;
   if constexpr (L >= 1)
     if (a.T <= 1) return launch_dot<XT, LPR, BPL, 1, KS>(a, s);
   if constexpr (L >= 2)
@@ -527,6 +527,8 @@ hipError_t launch_dot_tokens(const Q4Args& a, hipStream_t s) {
     if (a.T <= 4) return launch_dot<XT, LPR, BPL, 4, KS>(a, s);
   if constexpr (L >= 6)
     if (a.T <= 6) return launch_dot<XT, LPR, BPL, 6, KS>(a, s);
+  if constexpr (L >= 8 && KS > 1)
+    if (a.T <= 8) return launch_dot<XT, LPR, BPL, 8, KS>(a, s);
   return hipErrorInvalidValue;
 }
 // blocks per lane, of a row of KB blocks shared by lanes of one wave, or by four
@@ -535,11 +537,23 @@ constexpr int dot_blocks(int64_t KB) {
   return KB <= 16 ? 1 : KB <= 32 ? 2 : KB <= 64 ? 1 : KB <= 128 ? 2 : KB <= 256 ? 4 : kNoDot;
 }
 constexpr int split_blocks(int64_t KB) { return KB <= 64 ? kNoDot : KB <= 256 ? 1 : KB <= 512 ? 2 : KB <= 1024 ? 4 : kNoDot; }
-// slices of a row in the dot kernel, 0: it has no room for the tokens
+// Slices of a row in the dot kernel; 0: the tile kernel. Four slices have 256 or
+// more block places a row, of which KB are filled: with many rows they pay while
+// places times a block's instructions stay below what the tiles take for the KB
+// blocks, C instructions each (us, dots against tiles: 4 x 70000 x 2080 bf16, 73 against 31;
+// 4 x 4096 x 14336, 14.6 against 24.7; 8 x 5120 x 4096, 15.5 against 12.4; fp32 4 x 5120 x 4096, 13.2
+// against 16.6; codes 8 x 5120 x 4096, 11.2 against 12.3;
+// bf16 4 x 5120 x 4096, 10.9 against 12.2). Up to 2048 rows both are
+// latency, and the tiles have more of it (8 x 1018 x 6464: bf16 7.9 against 12.0, codes 5.5
+// against 11.3; fp32 4 x 1018 x 6464, 9.4 against 18.9).
 template <int XT>
 int dot_slices(const Q4Args& a) {
-  const int64_t T = a.T <= 2 ? a.T : a.T <= 4 ? 4 : a.T <= 6 ? 6 : 1 << 10, KB = a.K / 32;
-  return T * dot_blocks(KB) <= dot_limit<XT>() ? 1 : T * split_blocks(KB) <= dot_limit<XT>() ? 4 : 0;
+  const int64_t T = a.T <= 2 ? a.T : (a.T + 1) / 2 * 2, KB = a.K / 32;
+  if (T <= 6 && T * dot_blocks(KB) <= dot_limit<XT, 1>()) return 1;
+  if (T > 8 || T * split_blocks(KB) > dot_limit<XT, 4>()) return 0;
+  const int64_t instructions = XT == MOE_F32 ? 44 + 34 * T : XT == MOE_Q8_32 ? 12 + 11 * T : 32 + 18 * T;
+  constexpr int C = XT == MOE_F32 ? 400 : XT == MOE_Q8_32 ? 200 : 208;
+  return a.N <= 2048 || 256 * split_blocks(KB) * instructions <= KB * C ? 4 : 0;
 }
 template <int XT>
 hipError_t launch_dot_types(const Q4Args& a, int slices, hipStream_t s) {
@@ -719,10 +733,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void q4_tile_kernel(Q4Args a, int t
   };
 
   f32x4_t acc = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  auto compute = [&](int s, int lb, const StepWeights& st) __attribute__((always_inline)) {
-    uint32_t w[4];
-    float d[4];
-    step_ready(st, s, lane, KB, w, d);
+  auto compute = [&](int lb, const uint32_t (&w)[4], const float (&d)[4]) __attribute__((always_inline)) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const u32x4_t wt = weights_of<OP>(w[i]);
@@ -737,23 +748,30 @@ __global__ __launch_bounds__(64 * kWaves, 2) void q4_tile_kernel(Q4Args a, int t
     }
   };
 
-  // this wave's steps of the reduction: kw, kw + KW, ... of every chunk
-  StepWeights st;
-  load_step(nib, scl, wrow, min(kw, steps - 1), lane, KB, st);
+  // A wave has one step of every chunk: kw, kw + KW, ... Its weights come two chunks
+  // ahead, in two sets of registers (8 x 4096 x 14336 bf16: 20.0 us, 25.0 with one chunk ahead;
+  // 16 x 5120 x 4096: 9.9 and 12.6).
+  static_assert(CB == 4 * KW, "a step per wave and chunk");
+  StepWeights st[2];
   fetch(0);
-#pragma unroll 1
-  for (int b0 = 0; b0 < KB; b0 += CB) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) load_step(nib, scl, wrow, min(kw + i * KW, steps - 1), lane, KB, st[i]);
+  auto chunk = [&](int b0, StepWeights& st) __attribute__((always_inline)) {
     if (b0) __syncthreads();  // every wave is done with the chunk before
     store(b0);
     __syncthreads();
-    if (b0 + CB < KB) fetch(b0 + CB);
+    fetch(b0 + CB);  // past the row its last block, never stored: a branch would make the weights' wait cover it
+    const int s = b0 / 4 + kw;
+    uint32_t w[4];
+    float d[4];
+    step_ready(st, s, lane, KB, w, d);
+    load_step(nib, scl, wrow, min(s + 2 * KW, steps - 1), lane, KB, st);  // past the last step: never used
+    if (s < steps) compute(4 * kw, w, d);
+  };
 #pragma unroll 1
-    for (int lb = 4 * kw; lb < CB; lb += 4 * KW) {
-      const int s = b0 / 4 + lb / 4;
-      const StepWeights now = st;
-      load_step(nib, scl, wrow, min(s + KW, steps - 1), lane, KB, st);  // past the last step: never used
-      if (s < steps) compute(s, lb, now);
-    }
+  for (int b0 = 0; b0 < KB; b0 += 2 * CB) {
+    chunk(b0, st[0]);
+    if (b0 + CB < KB) chunk(b0 + CB, st[1]);
   }
   // the KW partial sums, in wave order; lane (column, c) holds tokens 4c + r of its feature
   __syncthreads();
