@@ -15,6 +15,11 @@
 // Only the k-th largest logit is needed, not the order of the picks: an
 // expert counts if its logit is larger, or equal and one of the lowest ids
 // that fill the set.
+//
+// Measured (kernels alone): 32768 x 512 fp32, 8 picks: rows 23-26 us for 67 MB (bound by
+// instructions, 1150 for four rows of a wave: 16 us of them, two waves a SIMD), finishing 5.5, gradient 27.5 for
+// 134 MB = 4.9 TB/s, the rate of a copy. 12288 x 256 bf16: 10.6, 5 and 7.5 us; 999 x 60 fp16:
+// 3.9, 5 and 3.2 us, each a launch and a few dependent trips to memory.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -305,7 +310,7 @@ __global__ __launch_bounds__(256, NE <= 32 ? 2 : 1) void balance_rows_kernel(Bal
     for (int j = 0; j < NE; j += 4) raw[j / 4] = load_run<ZT, NE>(zr, run_of<G>(j, gl, E), E);
   };
   int64_t row0 = ((int64_t)blockIdx.x * 4 + wave) * R;
-  fetch(row0 + g);
+  if (row0 < a.T) fetch(row0 + g);  // without tokens there is no row 0 either
   for (; row0 < a.T; row0 += stride) {
     const int64_t row = row0 + g;
     float e[NE];

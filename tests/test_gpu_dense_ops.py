@@ -455,6 +455,13 @@ def test_router_balance_without_tokens():
         d = torch.full(tuple(zz.shape), GUARD, device="cuda")
         b.backward(d)
         assert (d == 0).all() and (b.lse == float("-inf")).all()
+    # nor is there a row to read: the address of an empty tensor is null
+    none = torch.empty((0, 300), device="cuda")
+    out = [torch.ones(300, dtype=torch.int32, device="cuda"), torch.ones(300, device="cuda"), torch.ones(4, device="cuda")]
+    assert none.data_ptr() == 0
+    moe.moe_router_balance(none, 8, *out, torch.empty(0, device="cuda"))
+    moe.moe_router_balance_grad(none, out[1], out[2], torch.empty(0, device="cuda"), torch.empty((0, 300), device="cuda"))
+    assert all((o == 0).all() for o in out)
 
 
 @pytest.mark.parametrize("bad", [float("nan"), float("inf")])
