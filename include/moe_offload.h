@@ -509,9 +509,10 @@ MOE_API int moe_q4_split(int32_t rows, int32_t k, const void* blocks, void* nibb
  * contiguous, 16-byte aligned. x_type MOE_F32, MOE_F16, MOE_BF16, or MOE_Q8_32
  * with x_scales fp32 [n_tokens][k/32] (x = scale * code); y_type MOE_F32,
  * MOE_F16 or MOE_BF16. n_out >= 1, k a multiple of 32, 32..2^20.
- * Weights and activations enter the products unrounded (MOE_Q8_32: scale *
- * code rounded to fp32) and sums are fp32; y is rounded once. |x| up to 2^115;
- * a token with a value that is not finite gives NaN.
+ * Weights and activations enter the products unrounded (8-bit codes as whole
+ * numbers, their scales times the sums of a block); sums are fp32; y is rounded
+ * once. |x| up to 2^115; a token with a value that is not finite has no finite
+ * result.
  * workspace: moe_q4_workspace_bytes bytes of device memory, 256-byte aligned,
  * with any content, NULL if 0; calls that may run at once (other streams,
  * graphs replayed side by side) need one each. flags: MOE_ACCUMULATE or 0. */

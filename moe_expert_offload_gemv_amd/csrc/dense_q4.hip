@@ -4,19 +4,30 @@
 //
 //   y[t][n] = sum_b d[n][b] * sum_{j<32} (q[n][b][j] - 8) * x[t][32 b + j]
 //
-// The products run on the matrix cores as 16 tokens x 16 features x one block
-// (v_mfma_f32_16x16x32), also for a single token: the weights' bytes bound
-// few tokens, and the other rows of the tile cost nothing that is needed.
+// Three kernels, by the work of a call:
+//   q4_dot_kernel   a few tokens: dot products on the vector unit, the tokens' values in
+//                   registers. Bound by the weights' bytes (1 x 65537 x 4096 bf16, 151 MB, 28 us =
+//                   5.4 TB/s, a streaming read) or, for few rows, by a launch and two trips to memory
+//                   (1 x 2048 x 2048 fp32, 4.0 us).
+//   q4_tile_kernel  up to 2e9 products: 16 tokens a work-group on the matrix cores, one
+//                   launch (32 x 4096 x 1536 fp32, 7.4 us; 201 x 1001 x 1056 fp16, 7.3: rounds of
+//                   load, convert, barrier and product, 1 us each).
+//   q4_wide_kernel  more: the activations are brought into operand form once, 64 x 64 tiles
+//                   per wave (4096 x 5120 x 4096 bf16, 172 GFLOP, 267-285 us = 0.62 PFLOP/s, 17 of them the
+//                   operand pass; the library's plain bf16 product of the same sizes would take 153). Per step of
+//                   four blocks a wave issues 64 products and 460 vector instructions, 256 of them the scale
+//                   FMAs that keep the weights exact; the two do not overlap on a SIMD
+//                   (counters: vector unit 323, matrix cores 164 of 593 kcycles).
+// The matrix cores take 16 tokens x 16 features x one block (v_mfma_f32_16x16x32).
 //
 // Exactness. A block's weight operand is 16 + q, exact in both 16-bit types
 // and formed by a shift and one v_bitop3 per two weights (q into the mantissa
 // of 16.0: no subtraction, no conversion); the accumulator of a block's product
-// starts at -24 * sum_j x_j, which makes it (q - 8), and comes from the same
-// matrix instruction with a constant -24 operand, once for all features of a
-// wave. The block's scale is applied to the sum in fp32. Activations enter
-// unrounded: bf16 and fp16 as they are, fp32 (and scale * code of 8-bit
-// activations) as three bf16 terms cut from the top, 8 bits each, whose sum
-// is the value.
+// starts at -24 * sum_j x_j, which makes it (q - 8); these sums are formed with the
+// activations' operand. The block's scale is applied to the sum in fp32. Activations enter
+// unrounded: bf16 and fp16 as they are, 8-bit codes as whole numbers whose scale
+// joins the block's, fp32 as three bf16 terms cut from the top, 8 bits each, whose
+// sum is the value.
 //
 // Operand order: as in grouped_mfma.hip. Lane l covers row/column l % 16 and
 // chunk c = l / 16 of a block, the elements 4c + {0, 2, 1, 3, 16, 18, 17, 19};
@@ -93,11 +104,6 @@ __device__ __forceinline__ uint32_t weights_part(uint32_t w, int i) {
 template <int OP>
 __device__ __forceinline__ u32x4_t weights_of(uint32_t w) {
   return u32x4_t{weights_part<OP>(w, 0), weights_part<OP>(w, 1), weights_part<OP>(w, 2), weights_part<OP>(w, 3)};
-}
-template <int OP>
-__device__ __forceinline__ u32x4_t minus24() {
-  const uint32_t v = OP == MOE_F16 ? 0xCE00CE00u : 0xC1C0C1C0u;
-  return u32x4_t{v, v, v, v};
 }
 
 // (lane group g, dword d) -> (lane group d, dword g) within each 16-lane
