@@ -275,6 +275,25 @@ def test_q4_matmul_values_that_are_not_finite_stay_in_their_token(T, N, K, xt):
     assert torch.equal(y[rest], clean[rest])
 
 
+@pytest.mark.parametrize("T,N,K", [(3, 50, 6400), (8, 50, 4128)])
+@pytest.mark.parametrize("xt", ["f32", "bf16", "f16"])
+def test_q4_matmul_values_that_are_not_finite_in_split_rows(T, N, K, xt):
+    test_q4_matmul_values_that_are_not_finite_stay_in_their_token(T, N, K, xt)
+
+
+@pytest.mark.parametrize("T,N,K", [(3, 50, 128), (5, 50, 6400), (40, 50, 128), (260, 1000, 8000)])
+def test_q4_matmul_scales_that_are_not_finite_stay_in_their_token(T, N, K):
+    p = Product(T, N, K, "q8")
+    clean = torch.zeros((T, N), device="cuda")
+    moe.moe_q4_matmul(p.x, p.nib, p.scl, clean, scales=p.scales)
+    p.scales[1, 1], p.scales[2, 3] = float("nan"), float("inf")
+    y = torch.zeros((T, N), device="cuda")
+    moe.moe_q4_matmul(p.x, p.nib, p.scl, y, scales=p.scales)
+    assert torch.isnan(y[1]).all() and not torch.isfinite(y[2]).any()
+    rest = [t for t in range(T) if t not in (1, 2)]
+    assert torch.equal(y[rest], clean[rest])
+
+
 def test_q4_matmul_of_no_tokens():
     p = Product(1, 8, 64, "f32")
     moe.moe_q4_matmul(p.x[:0], p.nib, p.scl, torch.zeros((0, 8), device="cuda"))
@@ -564,6 +583,37 @@ def test_calls_on_another_stream_and_two_at_once():
             moe.moe_q4_matmul(ps[0].x, ps[0].nib, ps[0].scl, ys[0], stream=streams[0])
     with pytest.raises(ValueError):
         moe.moe_router_balance(zs[0].z, 6, zs[0].counts, zs[0].load, zs[0].stats, zs[0].lse, stream=streams[0])
+
+
+@pytest.mark.parametrize("T,N,K,xt", [(260, 1000, 8000, "f32"), (260, 1000, 8000, "q8"), (4100, 4100, 160, "bf16"),
+                                      (4, 300, 8192, "bf16")])
+def test_large_and_split_products_at_once_and_captured(T, N, K, xt):
+    ps = [Product(T, N, K, xt, seed=s) for s in (1, 2)]
+    streams = [torch.cuda.Stream() for _ in ps]
+    ys = [torch.zeros((T, N), device="cuda") for _ in ps]
+    wss = [moe.moe_q4_workspace(p.x, p.nib) for p in ps]
+    for p, y, ws in zip(ps, ys, wss):
+        moe.moe_q4_matmul(p.x, p.nib, p.scl, y, scales=p.scales, workspace=ws)
+    torch.cuda.synchronize()
+    want = [y.clone() for y in ys]
+    for _ in range(5):
+        for p, y, ws, s in zip(ps, ys, wss, streams):
+            moe.moe_q4_matmul(p.x, p.nib, p.scl, y, scales=p.scales, workspace=ws, stream=s)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(ys, want))
+    # both in one graph, one after the other through the same workspace; another's eager calls between the replays
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for p, y in zip(ps, ys):
+            moe.moe_q4_matmul(p.x, p.nib, p.scl, y, scales=p.scales, workspace=wss[0])
+    for _ in range(3):
+        for y in ys:
+            y.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(ys, want))
+        moe.moe_q4_matmul(ps[1].x, ps[1].nib, ps[1].scl, ys[0], scales=ps[1].scales, workspace=wss[0])
+        torch.cuda.synchronize()
 
 
 @pytest.mark.parametrize("T", [1, 24, 300])
