@@ -617,22 +617,20 @@ __device__ __forceinline__ void step_ready(const StepWeights& st, int s, int lan
 }
 
 // ---------------------------------------------------------------------------
-// Some tokens, one launch: a work-group of 8 waves takes 16 tokens by 16 FW
-// features; KW = 8 / FW waves share the reduction in steps of four blocks. A
+// Some tokens, one launch: a work-group of W waves takes 16 tokens by 16 FW
+// features; KW = W / FW waves share the reduction in steps of four blocks. A
 // chunk of CB blocks of the activations at a time is brought into operand form
 // in LDS by the whole work-group, read from memory in whole lines and converted
-// once for all its features; the next chunk's values and the next step's weights
+// once for all its features; the next chunk's values and the next two steps' weights
 // are on their way meanwhile.
 //
 // 16 tokens a work-group: 32 or 64 would convert the weights once for more
 // tokens, but leave CUs idle at the sizes that come here (128 tokens, bf16, 1024 x
 // 1024: 7.0 us against 8.3 with 32; 5120 x 4096: 33 against 37; event times).
 
-constexpr int kWaves = 8;
-
-template <int XT, int KW, int CB>
-__global__ __launch_bounds__(64 * kWaves, 2) void q4_tile_kernel(Q4Args a, int token_tiles) {
-  constexpr int TERMS = terms_of<XT>(), OP = op_of<XT>(), FW = kWaves / KW, ROWS = 16, THREADS = 64 * kWaves;
+template <int XT, int W, int KW, int CB>
+__global__ __launch_bounds__(64 * W, W / 4) void q4_tile_kernel(Q4Args a, int token_tiles) {
+  constexpr int TERMS = terms_of<XT>(), OP = op_of<XT>(), FW = W / KW, ROWS = 16, THREADS = 64 * W;
   constexpr bool Q8 = XT == MOE_Q8_32;
   constexpr int UPB = 2 * value_size<XT>();               // 16-byte units of a block of x
   constexpr int UNITS = ROWS * CB * UPB / THREADS;        // a thread's units of a chunk
@@ -643,7 +641,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void q4_tile_kernel(Q4Args a, int t
   // blocks side by side) nor a fragment's reads meet in a bank; -24 sums and
   // scales [block][token]
   constexpr int kTerm = CB * ROWS * 64, kBase = TERMS * kTerm, kScale = kBase + CB * ROWS * 4;
-  constexpr int kLds = kScale + (Q8 ? CB * ROWS * 4 : 0), kSums = kWaves * 64 * 16;
+  constexpr int kLds = kScale + (Q8 ? CB * ROWS * 4 : 0), kSums = W * 64 * 16;
   __shared__ __attribute__((aligned(16))) uint8_t s_x[kLds > kSums ? kLds : kSums];
   float* s_base = reinterpret_cast<float*>(s_x + kBase);
   float* s_scale = reinterpret_cast<float*>(s_x + kScale);
@@ -796,18 +794,24 @@ __global__ __launch_bounds__(64 * kWaves, 2) void q4_tile_kernel(Q4Args a, int t
   }
 }
 
-template <int XT, int KW, int CB>
+template <int XT, int W, int KW, int CB>
 hipError_t launch_tile(const Q4Args& a, hipStream_t s) {
-  constexpr int F = 16 * kWaves / KW;
+  constexpr int F = 16 * W / KW;
   const int64_t token_tiles = (a.T + 15) / 16, tiles = (a.N + F - 1) / F * token_tiles;
-  return launch(q4_tile_kernel<XT, KW, CB>, dim3((unsigned)tiles), dim3(64 * kWaves), Launch{s}, a, (int)token_tiles);
+  return launch(q4_tile_kernel<XT, W, KW, CB>, dim3((unsigned)tiles), dim3(64 * W), Launch{s}, a, (int)token_tiles);
 }
 template <int XT>
 hipError_t launch_tile_types(const Q4Args& a, hipStream_t s) {
-  // 16 features a work-group as long as each gets a CU of its own, else 32 (16 tokens, bf16, K = 4096, N =
-  // 4096: 10.7 us against 13.3; N = 65537: 87 against 57)
-  if ((a.T + 15) / 16 * ((a.N + 15) / 16) <= 256) return launch_tile<XT, 8, 32>(a, s);
-  return launch_tile<XT, 4, 16>(a, s);
+  // As long as a work-group has a CU of its own it has all the waves that its features can use: 16
+  // features and 8 waves, else 32 and 16 (rows long enough for their chunks of 32 blocks), else 32
+  // and 8. us, bf16 and fp32: 16 x 4096 x 4096, 256 work-groups of 16 features, 8.1 and 12.3 against 9.9
+  // and 14.3 in the last form; 16 x 5120 x 4096, 160 of 32, 9.5 and 12.6 in the second, 9.9 and 14.2 in
+  // the last; 16 x 14336 x 4096, 448 of 32, 17.1 and 23.6 against 14.1 and 21.6; 32 x 4096 x 1536, fp32, 7.9
+  // against 7.4.
+  const int64_t tiles = (a.T + 15) / 16;
+  if (tiles * ((a.N + 15) / 16) <= 256) return launch_tile<XT, 8, 8, 32>(a, s);
+  if (tiles * ((a.N + 31) / 32) <= 256 && a.K > 2048) return launch_tile<XT, 16, 8, 32>(a, s);
+  return launch_tile<XT, 8, 4, 16>(a, s);
 }
 
 // ---------------------------------------------------------------------------

@@ -213,7 +213,8 @@ Q4_SHAPES = [(1, 1, 32), (1, 16, 32), (1, 2048, 2048), (1, 33, 96), (2, 17, 1056
 # rows shared by four waves (some with nothing left for the last ones), and the longest of them and past it
 Q4_LONG = [(1, 37, 8224), (1, 2100, 8224), (1, 19, 16384), (1, 20, 32768), (1, 9, 32800), (2, 33, 4128), (2, 50, 8192),
            (3, 40, 16384), (4, 70, 8128), (6, 30, 16352), (2, 2049, 6368), (8, 90, 6400), (8, 2100, 8160),
-           (7, 33, 2080), (5, 2100, 2080), (4, 2100, 16000)]
+           (7, 33, 2080), (5, 2100, 2080), (4, 2100, 16000),
+           (16, 4200, 1056), (31, 4000, 4128)]
 # above 2e9 products: 64 x 64 tiles with the reduction split, 128 x 128 tiles, and those in two passes of tokens
 Q4_LARGE = [(130, 2050, 8224), (2100, 3900, 256), (16500, 520, 256), (4100, 4100, 160), (16500, 1100, 128)]
 
