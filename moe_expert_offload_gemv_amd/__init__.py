@@ -333,6 +333,7 @@ def moe_last_error(ctx) -> str:
 # microseconds on the GPU, so the checks here are kept to a few of the host.
 
 _types = {}  # torch dtype -> type code, filled with torch's first use
+_dtypes = {}  # name -> torch dtype, likewise: comparing names would format one per argument and call
 _raw_stream = None
 
 
@@ -343,6 +344,7 @@ def _dense():
         import torch
 
         _types.update({torch.float32: MOE_F32, torch.float16: MOE_F16, torch.bfloat16: MOE_BF16, torch.int8: MOE_Q8_32})
+        _dtypes.update({str(d): d for d in (torch.float32, torch.float16, torch.int32, torch.uint8, torch.bool)})
         # the stream's handle without a Stream object around it, where this torch has that
         _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
             lambda dev: torch.cuda.current_stream(dev).cuda_stream)
@@ -373,7 +375,7 @@ def _flat(name, t, dev, shape, dtype):
     """Address of a contiguous tensor (None -> NULL); dtype: its name in torch."""
     if t is None:
         return None
-    if t.shape != shape or t.get_device() != dev or dev < 0 or str(t.dtype) != dtype or not t.is_contiguous():
+    if t.shape != shape or t.get_device() != dev or dev < 0 or t.dtype is not _dtypes[dtype] or not t.is_contiguous():
         raise ValueError(f"{name}: {t.dtype} {tuple(t.shape)} on {t.device}; a contiguous {dtype} tensor of shape "
                          f"{tuple(shape)} on cuda device {max(dev, 0)} is needed")
     return t.data_ptr()
@@ -508,7 +510,7 @@ def moe_router_balance(logits, top_k: int, counts, load, stats, lse, valid=None,
     zt, zp, zs = _rows("logits", logits, dev, shape)
     vp = None
     if valid is not None:
-        vp = _flat("valid", valid, dev, (T,), "torch.bool" if str(valid.dtype) == "torch.bool" else "torch.uint8")
+        vp = _flat("valid", valid, dev, (T,), "torch.bool" if valid.dtype is _dtypes["torch.bool"] else "torch.uint8")
     cp = _flat("counts", counts, dev, (E,), "torch.int32")
     lp = _flat("load", load, dev, (E,), "torch.float32")
     tp = _flat("stats", stats, dev, (4,), "torch.float32")
