@@ -490,7 +490,8 @@ MOE_API const char* moe_last_error(moe_ctx* ctx);
  * MOE_F32, MOE_F16 or MOE_BF16. residual and residual_out may be the same
  * (update in place) and NULL together; out may be x when type and stride are
  * the same. scales (fp32 [n_tokens][hidden/32]) belongs to MOE_Q8_32 and is
- * NULL otherwise. eps >= 0. */
+ * NULL otherwise. eps >= 0. Any finite s has its norm, however large or small
+ * its squares; a row of zeros with eps = 0 gives NaN. */
 MOE_API int moe_add_rmsnorm(int32_t device, void* stream, int32_t n_tokens, int32_t hidden,
                             int32_t x_type, const void* x, int64_t x_stride,
                             int32_t res_type, const void* residual, int64_t res_stride,

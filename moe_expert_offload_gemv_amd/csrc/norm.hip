@@ -10,7 +10,9 @@
 // work-group as small as holds the row, so that several rows' loads are in flight
 // in a CU while one waits for its sum); longer rows are read twice. The sum of squares,
 // the mean and the scaling are fp32; the norm uses the sum before its rounding to the
-// residual's type.
+// residual's type. Squares leave fp32's range long before the values do: a row whose sum
+// of squares is not finite, or whose mean is too small to have kept them all, is summed again
+// scaled by a power of two.
 //
 // Measured (kernel alone): 12287 x 4096, fp32 x, bf16 residual and out, 504 MB, 92-95 us =
 // 5.4 TB/s, the rate of a streaming read (a copy: 4.95); 4096 x 2048 bf16 to codes, 60 MB,
@@ -34,6 +36,9 @@ constexpr int kNoResidual = -1;
 // zeros: 127 / a stays finite above it
 constexpr uint32_t kMinGroupMax = (127u - 100u) << 23;
 constexpr uint32_t kInfBits = 0x7F800000u;
+// A square rounded below fp32's normal range is off by at most 2^-150: beside a mean
+// of this size, or an eps of it, that is nothing
+constexpr float kSmallMean = 0x1p-100f;
 
 // s = x + residual of values i .. i + 7
 template <int XT, int RT>
@@ -91,7 +96,9 @@ __device__ __forceinline__ void put_codes8(int8_t* out, float* scales, int64_t i
   if ((i & 31) == 0) scales[i >> 5] = scale;
 }
 
-__device__ __forceinline__ void put_out8(const NormArgs& a, int64_t row, int64_t i, const float (&s)[8], float r) {
+// v = s * half * r * weight; half is 1 but for rows summed again
+__device__ __forceinline__ void put_out8(const NormArgs& a, int64_t row, int64_t i, const float (&s)[8], float r,
+                                         float half) {
   float v[8], w[8];
   if (a.weight) {
     if (i + 8 <= a.H)
@@ -100,7 +107,7 @@ __device__ __forceinline__ void put_out8(const NormArgs& a, int64_t row, int64_t
       load8_tail<MOE_F32>(a.weight, i, a.H, w);
   }
 #pragma unroll
-  for (int j = 0; j < 8; ++j) v[j] = a.weight ? s[j] * r * w[j] : s[j] * r;
+  for (int j = 0; j < 8; ++j) v[j] = a.weight ? s[j] * half * r * w[j] : s[j] * half * r;
   char* out = static_cast<char*>(a.out);
   if (a.out_type == MOE_F32)
     put8<MOE_F32>(out + 4 * row * a.out_stride, i, a.H, v);
@@ -114,11 +121,14 @@ __device__ __forceinline__ void put_out8(const NormArgs& a, int64_t row, int64_t
 
 // One work-group per row, rows in turn. NV > 0: the row's sums stay in NV
 // chunks of 8 registers per thread; NV = 0: any length, read twice (the sums
-// are formed again, so the residual may be updated in place).
+// are formed again, so the residual may be updated in place). 16 waves with a row in
+// registers: two work-groups a CU, at the price of a few spilled scalars (4096 x 8192
+// bf16: 59 us, one work-group 64; fp32 101 and 106).
 template <int XT, int RT, int THREADS, int NV>
-__global__ __launch_bounds__(THREADS) void add_rmsnorm_kernel(NormArgs a) {
+__global__ __launch_bounds__(THREADS, THREADS == 1024 && NV > 0 ? 8 : 1) void add_rmsnorm_kernel(NormArgs a) {
   constexpr int W = THREADS / 64;
-  __shared__ float s_sum[2][W];
+  __shared__ float s_sum[2][W], s_again[W];
+  const float least = a.eps < kSmallMean ? kSmallMean * (float)a.H : 0.f;
   int turn = 0;
   for (int64_t row = blockIdx.x; row < a.T; row += gridDim.x, turn ^= 1) {
     const char* x = static_cast<const char*>(a.x) + row * a.x_stride * value_size<XT>();
@@ -161,21 +171,53 @@ __global__ __launch_bounds__(THREADS) void add_rmsnorm_kernel(NormArgs a) {
 #pragma unroll
       for (int w = 0; w < W; ++w) ss += s_sum[turn][w];
     }
-    const float r = 1.0f / sqrtf(ss / (float)a.H + a.eps);
+    float r = 1.0f / sqrtf(ss / (float)a.H + a.eps), half = 1.0f;
+    // the same for every thread of the work-group
+    if (__builtin_expect(__builtin_amdgcn_readfirstlane(!(ss >= least && ss < __builtin_inff())), 0)) {
+      // 2^-80: values of any size and number stay below 2^120, a mean of 2^104, the least that
+      // overflows, above 2^-56; 2^100: a mean below 2^-100 becomes 2^100 at most, the smallest square 2^-98
+      const bool large = !(ss < __builtin_inff());
+      const float k = large ? 0x1p-80f : 0x1p100f;
+      float again = 0.f;
+      auto add = [&](float v) __attribute__((always_inline)) { v *= k, again = fmaf(v, v, again); };
+      if constexpr (NV > 0) {
+#pragma unroll
+        for (int c = 0; c < NV; ++c)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) add(s[c][j]);
+      } else {
+        for (int64_t i = 8 * (int64_t)threadIdx.x; i < a.H; i += 8 * THREADS) {
+          sum8<XT, RT>(x, res, i, a.H, s[0]);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) add(s[0][j]);
+        }
+      }
+      again = route_dev::wave_sum(again);
+      if constexpr (W > 1) {
+        const int lane = threadIdx.x & 63;
+        if (lane == 0) s_again[threadIdx.x >> 6] = again;
+        __syncthreads();  // written again past the next row's barrier at the earliest
+        again = route_dev::wave_sum(lane < W ? s_again[lane & (W - 1)] : 0.f);
+      }
+      // 1 / sqrt(mean + eps) = k / sqrt(again / hidden + eps k^2), k as two factors so that neither
+      // r (the root is 2^-61 at the least) nor s * half leaves the normal range before v does
+      r = 1.0f / sqrtf(again / (float)a.H + a.eps * k * k) * (large ? 0x1p-40f : 0x1p66f);
+      half = large ? 0x1p-40f : 0x1p34f;
+    }
     if constexpr (NV > 0) {
 #pragma unroll
       for (int c = 0; c < NV; ++c) {
         const int64_t i = 8 * ((int64_t)c * THREADS + threadIdx.x);
         if (i < a.H) {
           if constexpr (RT != kNoResidual) put8<RT>(res_out, i, a.H, s[c]);
-          put_out8(a, row, i, s[c], r);
+          put_out8(a, row, i, s[c], r, half);
         }
       }
     } else {
       for (int64_t i = 8 * (int64_t)threadIdx.x; i < a.H; i += 8 * THREADS) {
         sum8<XT, RT>(x, res, i, a.H, s[0]);
         if constexpr (RT != kNoResidual) put8<RT>(res_out, i, a.H, s[0]);
-        put_out8(a, row, i, s[0], r);
+        put_out8(a, row, i, s[0], r, half);
       }
     }
   }

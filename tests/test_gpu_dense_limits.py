@@ -1,0 +1,82 @@
+"""The operators beside the experts at the limits of their types: rows whose
+squares leave fp32's range, values that are not finite, and calls after
+somebody else's error.
+
+Tolerances count roundings as in test_gpu_dense_ops.py.
+"""
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import moe_expert_offload_gemv_amd as moe  # noqa: E402
+from tests.test_gpu_dense_ops import E, TYPES, norm_ref, norm_tol, rng_of, smallest, u  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+
+
+# ---------------------------------------------------------------------------
+# residual add + RMS norm: finite rows whose squares overflow or underflow
+
+# one wave, four, sixteen, and rows that are read twice
+NORM_WIDTHS = [1, 64, 100, 2048, 2051, 4096, 8200, 16384, 16400]
+
+
+@pytest.mark.parametrize("H", NORM_WIDTHS)
+@pytest.mark.parametrize("xt,rt,ot", [("f32", None, "f32"), ("f32", "f32", "f32"), ("bf16", "bf16", "bf16"),
+                                      ("f32", "bf16", "f16"), ("bf16", None, "f32")])
+def test_add_rmsnorm_far_from_unit_scale(H, xt, rt, ot):
+    for size, eps in ((1e17, 1e-6), (1e19, 1e-6), (1e25, 1e-6), (5e37, 1e-6), (1e25, 1e35), (1e-14, 0.0), (1e-17, 0.0),
+                      (1e-17, 1e-34), (1e-24, 0.0), (1e-30, 0.0), (1e-30, 1e-38), (1e-37, 0.0), (1e-30, 1e-6)):
+        far_from_unit_scale(H, xt, rt, ot, size, eps)
+
+
+def far_from_unit_scale(H, xt, rt, ot, size, eps):
+    T = 3
+    g = rng_of(40, H)
+    x = torch.from_numpy(g.standard_normal((T, H)) * size).to(TYPES[xt]).cuda()
+    x[1] = torch.from_numpy(g.standard_normal(H)).to(TYPES[xt]).cuda() * (1.0 if eps else 1e-3)  # a row of ordinary size
+    r = torch.from_numpy(g.standard_normal((T, H)) * size / 4).to(TYPES[rt]).cuda() if rt else None
+    w = torch.from_numpy(1 + 0.1 * g.standard_normal(H)).float().cuda() if H % 3 else None
+    out = torch.zeros((T, H), dtype=TYPES[ot], device="cuda")
+    ro = torch.zeros_like(r) if rt else None
+    s, v = norm_ref(x, r, w, eps)
+    moe.moe_add_rmsnorm(x, w, out, residual=r, residual_out=ro, eps=eps)
+    dt = TYPES[ot]
+    # one rounding more than an ordinary row: of s off its power of two
+    assert ((out.double() - v).abs() <= (norm_tol(H) + E + u(dt)) * 1.001 * v.abs() + smallest(dt)).all(), (size, eps)
+    if rt:
+        assert ((ro.double() - s).abs() <= (E + u(TYPES[rt])) * 1.001 * s.abs() + smallest(TYPES[rt])).all()
+        moe.moe_add_rmsnorm(x, w, out.clone(), residual=r, eps=eps)  # in place
+        assert torch.equal(r, ro)
+
+
+@pytest.mark.parametrize("H", [64, 2048, 8192, 16416])
+@pytest.mark.parametrize("size", [1e24, 1e-28])
+def test_add_rmsnorm_8_bit_far_from_unit_scale(H, size):
+    g = rng_of(41, H)
+    x = torch.from_numpy(g.standard_normal((2, H)) * size).float().cuda()
+    out, scales = torch.zeros((2, H), dtype=torch.int8, device="cuda"), torch.zeros((2, H // 32), device="cuda")
+    moe.moe_add_rmsnorm(x, None, out, scales=scales, eps=0.0)
+    v = norm_ref(x, None, None, 0.0)[1].view(2, H // 32, 32)
+    step = scales.double()
+    top = v.abs().amax(dim=2)
+    tol = norm_tol(H) + E
+    assert ((step * 127 - top).abs() <= (tol + 2 * E) * 1.001 * top).all()
+    off = (out.view(2, H // 32, 32).double() * step.unsqueeze(2) - v).abs()
+    assert (off <= (0.5 + 127 * (2 * tol + 3 * E)) * 1.001 * step.unsqueeze(2)).all()
+
+
+@pytest.mark.parametrize("H", [64, 2048, 8192, 16400])
+def test_add_rmsnorm_rows_of_zeros_and_of_one_value(H):
+    x = torch.zeros((5, H), device="cuda")
+    x[1, 3] = 1e-45  # fp32's smallest
+    x[2, 5] = 3e38
+    x[3] = 3e38
+    out = torch.zeros_like(x)
+    moe.moe_add_rmsnorm(x, None, out, eps=0.0)
+    v = norm_ref(x[1:4], None, None, 0.0)[1]
+    assert ((out[1:4].double() - v).abs() <= (norm_tol(H) + 2 * E) * 1.001 * v.abs()).all()
+    assert torch.isnan(out[[0, 4]]).all()  # 0 / 0
+    moe.moe_add_rmsnorm(x, None, out, eps=1e-6)
+    assert (out[[0, 4]] == 0).all()
