@@ -768,8 +768,7 @@ hipError_t launch_gemv_route_gateup(const GemvArgs& a, const RouteArgs& r, const
 }
 hipError_t launch_group_picks(const GroupArgs& a, hipStream_t s) {
   if (a.P < 1 || a.E < 1 || a.E > 4096) return hipErrorInvalidValue;
-  hipLaunchKernelGGL(group_picks_kernel, dim3(1), dim3(256), 0, s, a);
-  return hipGetLastError();
+  return launch(group_picks_kernel, dim3(1), dim3(256), Launch{s}, a);
 }
 hipError_t launch_grouped_gateup(const GemvArgs& a, const GroupArgs& g, const Launch& l) {
   if (g.P < 1) return hipErrorInvalidValue;

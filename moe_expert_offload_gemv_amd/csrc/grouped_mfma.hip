@@ -396,8 +396,7 @@ bool mfma_grouped_shape_ok(int32_t H, int32_t F) {
 
 hipError_t launch_split_rows(const float* src, int32_t rows, int32_t K, uint8_t* dst, int32_t* sig, hipStream_t s) {
   if (rows < 1 || K % 32 || ((uintptr_t)src & 15) || ((uintptr_t)dst & 15)) return hipErrorInvalidValue;
-  hipLaunchKernelGGL(split_rows_kernel, dim3(rows), dim3(256), 0, s, src, K, reinterpret_cast<uint4*>(dst), sig);
-  return hipGetLastError();
+  return launch(split_rows_kernel, dim3(rows), dim3(256), Launch{s}, src, K, reinterpret_cast<uint4*>(dst), sig);
 }
 
 hipError_t launch_mfma_gateup(const GemvArgs& a, const GroupArgs& g, const SplitArgs& sp, const Launch& l) {

@@ -5,6 +5,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <tuple>
+
 namespace moe {
 
 // Per-device control words read and written by the kernels. Living in device
@@ -55,10 +57,11 @@ constexpr uint8_t kCaptured = 2;  // flag on a cold pick: its reads are written 
 enum { kAll = 0, kOnlyHot = 1, kOnlyCold = 2 };
 
 // Stream of a launch; with start/stop events the launch is timed by the
-// dispatch itself (hipExtLaunchKernelGGL).
+// dispatch itself (hipExtLaunchKernel). lds: bytes of dynamic LDS.
 struct Launch {
   hipStream_t stream = nullptr;
   hipEvent_t start = nullptr, stop = nullptr;
+  uint32_t lds = 0;
 };
 
 struct RouteArgs {
@@ -101,14 +104,20 @@ struct RouteArgs {
 };
 hipError_t launch_route(const RouteArgs& a, const Launch& l);
 
-// Launch on l.stream; timed by the dispatch itself when l carries events.
+// Launch on l.stream; timed by the dispatch itself when l carries events. The
+// status is this launch's own: hipGetLastError would also tell of an error that
+// some other call left with the thread, though the kernel runs.
 template <typename... Args, typename... P>
 inline hipError_t launch(void (*kern)(Args...), dim3 grid, dim3 block, const Launch& l, P... params) {
-  if (l.start)
-    hipExtLaunchKernelGGL(kern, grid, block, 0, l.stream, l.start, l.stop, 0, params...);
-  else
-    hipLaunchKernelGGL(kern, grid, block, 0, l.stream, params...);
-  return hipGetLastError();
+  std::tuple<Args...> values(params...);
+  return std::apply(
+      [&](Args&... v) {
+        void* args[] = {const_cast<void*>(static_cast<const void*>(&v))...};
+        const void* f = reinterpret_cast<const void*>(kern);
+        return l.start ? hipExtLaunchKernel(f, grid, block, args, l.lds, l.stream, l.start, l.stop, 0)
+                       : hipLaunchKernel(f, grid, block, args, l.lds, l.stream);
+      },
+      values);
 }
 
 struct GemvArgs {

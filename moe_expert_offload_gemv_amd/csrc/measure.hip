@@ -6,6 +6,7 @@
 #include <stdint.h>
 
 #include "../../include/moe_offload.h"
+#include "kernels.h"
 
 namespace moe {
 namespace {
@@ -62,11 +63,12 @@ extern "C" int moe_measure_read_bandwidth(const void* ptr, int64_t bytes, int32_
     rc = MOE_E_HIP;
   } else {
     const uint4* p = reinterpret_cast<const uint4*>(src);
-    hipLaunchKernelGGL(moe::read_stream_kernel, dim3(blocks), dim3(256), 0, s, p, n16, sink);  // warm-up
+    auto read = [&] { return moe::launch(moe::read_stream_kernel, dim3(blocks), dim3(256), moe::Launch{s}, p, n16, sink); };
+    hipError_t e = read();  // warm-up
     hipEventRecord(e0, s);
-    for (int r = 0; r < reps; ++r) hipLaunchKernelGGL(moe::read_stream_kernel, dim3(blocks), dim3(256), 0, s, p, n16, sink);
+    for (int r = 0; r < reps && e == hipSuccess; ++r) e = read();
     hipEventRecord(e1, s);
-    if (hipGetLastError() != hipSuccess || hipEventSynchronize(e1) != hipSuccess ||
+    if (e != hipSuccess || hipEventSynchronize(e1) != hipSuccess ||
         hipEventElapsedTime(&ms, e0, e1) != hipSuccess || ms <= 0.f)
       rc = MOE_E_HIP;
     else

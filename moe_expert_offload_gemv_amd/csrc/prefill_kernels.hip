@@ -644,24 +644,22 @@ hipError_t launch_expert_counts(const int32_t* ids, int32_t n_pairs, int32_t E, 
                                 int32_t* counts, hipStream_t s) {
   if (n_pairs <= 0 || E <= 0 || E > 4096) return hipErrorInvalidValue;
   const int32_t nc = sort_chunks(n_pairs);
-  hipLaunchKernelGGL(chunk_rank_kernel, dim3(nc), dim3(64), sizeof(int32_t) * E, s, ids, n_pairs, E, nc, rank,
-                     ccount);
-  hipLaunchKernelGGL(chunk_scan_kernel, dim3(E), dim3(64), 0, s, ccount, nc, counts);
-  return hipGetLastError();
+  Launch l{s};
+  l.lds = (uint32_t)(sizeof(int32_t) * E);
+  const hipError_t e = launch(chunk_rank_kernel, dim3(nc), dim3(64), l, ids, n_pairs, E, nc, rank, ccount);
+  if (e != hipSuccess) return e;
+  return launch(chunk_scan_kernel, dim3(E), dim3(64), Launch{s}, ccount, nc, counts);
 }
 hipError_t launch_expert_scatter(const int32_t* ids, int32_t n_pairs, int32_t E, const int32_t* offsets,
                                  const int32_t* ccount, const int32_t* rank, int32_t* perm, int32_t* inv,
                                  hipStream_t s) {
   if (n_pairs <= 0 || E <= 0) return hipErrorInvalidValue;
-  hipLaunchKernelGGL(expert_scatter_kernel, dim3((n_pairs + 255) / 256), dim3(256), 0, s, ids, n_pairs, E,
-                     sort_chunks(n_pairs), offsets, ccount, rank, perm, inv);
-  return hipGetLastError();
+  return launch(expert_scatter_kernel, dim3((n_pairs + 255) / 256), dim3(256), Launch{s}, ids, n_pairs, E,
+                sort_chunks(n_pairs), offsets, ccount, rank, perm, inv);
 }
 hipError_t launch_scale_rows(const float* src, int64_t rows, int32_t K, _Float16* dst, int32_t* sig, hipStream_t s) {
   if (K % KS || rows <= 0 || rows > 0x7fffffff || ((uintptr_t)src & 15)) return hipErrorInvalidValue;
-  hipLaunchKernelGGL(scale_rows_kernel, dim3((unsigned)rows), dim3(256), 0, s, src, K, reinterpret_cast<uint4*>(dst),
-                     sig);
-  return hipGetLastError();
+  return launch(scale_rows_kernel, dim3((unsigned)rows), dim3(256), Launch{s}, src, K, reinterpret_cast<uint4*>(dst), sig);
 }
 int64_t sclT_elements(const ExpertLayout& lay) {
   return 2 * (int64_t)lay.F * (lay.H / 32) + (int64_t)lay.H * (lay.F / 32);
@@ -694,16 +692,14 @@ hipError_t launch_stage_experts(const uint8_t* host_layer, const int32_t* expert
   if (n <= 0 || bytes <= 0 || bytes % 16 || ((uintptr_t)host_layer & 15) || ((uintptr_t)staging & 15))
     return hipErrorInvalidValue;
   const int64_t b16 = bytes / 16;
-  hipLaunchKernelGGL(stage_experts_kernel, dim3(128), dim3(256), 0, s, reinterpret_cast<const uint4*>(host_layer),
-                     experts, (int64_t)n * b16, b16, reinterpret_cast<uint4*>(staging));
-  return hipGetLastError();
+  return launch(stage_experts_kernel, dim3(128), dim3(256), Launch{s}, reinterpret_cast<const uint4*>(host_layer), experts,
+                (int64_t)n * b16, b16, reinterpret_cast<uint4*>(staging));
 }
 hipError_t launch_combine_pairs(const float* ypair, const int32_t* inv, const float* w, int32_t T, int32_t k,
                                 int32_t H, float* y, int32_t accumulate, hipStream_t s) {
   if (H % 4) return hipErrorInvalidValue;
-  hipLaunchKernelGGL(combine_pairs_kernel<8>, dim3((H / 4 + 255) / 256, T), dim3(256), 0, s, ypair, inv, w, k, H, y,
-                     accumulate);
-  return hipGetLastError();
+  return launch(combine_pairs_kernel<8>, dim3((H / 4 + 255) / 256, T), dim3(256), Launch{s}, ypair, inv, w, k, H, y,
+                accumulate);
 }
 
 }  // namespace moe

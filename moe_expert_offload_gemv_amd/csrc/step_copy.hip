@@ -65,8 +65,7 @@ hipError_t launch_copy_list(const CopyList& l, hipStream_t s) {
   }
   const int64_t chunks = (longest + kCopyChunk - 1) / kCopyChunk;
   if (chunks > 0x7fffffff) return hipErrorInvalidValue;
-  hipLaunchKernelGGL(copy_list_kernel, dim3((unsigned)chunks, l.n), dim3(256), 0, s, l);
-  return hipGetLastError();
+  return launch(copy_list_kernel, dim3((unsigned)chunks, l.n), dim3(256), Launch{s}, l);
 }
 
 }  // namespace moe

@@ -10,7 +10,10 @@ import pytest
 torch = pytest.importorskip("torch")
 
 import moe_expert_offload_gemv_amd as moe  # noqa: E402
-from tests.test_gpu_dense_ops import E, TYPES, norm_ref, norm_tol, rng_of, smallest, u  # noqa: E402
+from tests._gpu import Decode  # noqa: E402
+from tests.test_gpu_dense_ops import (  # noqa: E402
+    E, TYPES, Balance, Product, norm_ref, norm_tol, rng_of, smallest, u)
+from workload import Workload, activations, zipf_logits  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 
@@ -80,3 +83,59 @@ def test_add_rmsnorm_rows_of_zeros_and_of_one_value(H):
     assert torch.isnan(out[[0, 4]]).all()  # 0 / 0
     moe.moe_add_rmsnorm(x, None, out, eps=1e-6)
     assert (out[[0, 4]] == 0).all()
+
+
+# ---------------------------------------------------------------------------
+# an error that another HIP call left with the thread
+
+
+class PendingError:
+    """A host-side error of the thread, left unread: no such device."""
+
+    def __enter__(self):
+        torch.cuda.synchronize()
+        assert moe.lib().hipSetDevice(9999) != 0
+
+    def __exit__(self, *exc):
+        moe.lib().hipGetLastError()  # or the next call of torch would raise it
+
+
+def test_a_pending_error_of_another_call_is_not_a_launchs():
+    p = Product(5, 33, 64, "f32")
+    x, out, y = torch.ones((3, 64), device="cuda"), torch.zeros((3, 64), device="cuda"), torch.zeros((5, 33), device="cuda")
+    residual = torch.ones((3, 64), device="cuda")
+    with PendingError():
+        moe.moe_add_rmsnorm(x, None, out, residual=residual)
+        moe.moe_q4_matmul(p.x, p.nib, p.scl, y)
+    assert (residual == 2).all() and (out - 1).abs().max() < 1e-6
+    p.check(y, torch.float32)
+    # calls of several launches: the operand pass and the tiles; rows, finish and gradient
+    p = Product(200, 4100, 4096, "bf16")
+    y, ws = torch.zeros((200, 4100), device="cuda"), moe.moe_q4_workspace(p.x, p.nib)
+    assert ws is not None
+    b = Balance(torch.randn(50, 96), 6)
+    d = torch.zeros((50, 96), device="cuda")
+    with PendingError():
+        moe.moe_q4_matmul(p.x, p.nib, p.scl, y, workspace=ws)
+        b.forward()
+        b.backward(d)
+    p.check(y, torch.float32)
+    assert int(b.counts.sum()) == 300 and b.stats[3] == 50 and d.abs().max() > 0
+    b.check()
+
+
+def test_a_pending_error_of_another_call_is_not_the_experts():
+    wl = Workload("decode-e64k8-h256f512-t5-pending", 323, 1, 64, 8, 256, 512, tokens=5, steps=2, zipf_s=1.1, slots=24)
+    d = Decode(wl)
+    try:
+        x, z = torch.from_numpy(activations(wl, 0)).cuda(), torch.from_numpy(zipf_logits(wl)[0, 0]).cuda()
+        y, want = torch.zeros_like(x), torch.zeros_like(x)
+        moe.moe_forward(d.ctx, 0, 5, x, z, want)
+        moe.moe_cache_step(d.ctx)
+        with PendingError():
+            moe.moe_forward(d.ctx, 0, 5, x, z, y)
+            moe.moe_cache_step(d.ctx)
+            gbps = moe.moe_measure_read_bandwidth(nbytes=1 << 20)
+        assert gbps > 0 and (y - want).abs().max() <= 1e-5 * want.abs().max()
+    finally:
+        d.close()
