@@ -513,7 +513,8 @@ MOE_API int moe_q4_split(int32_t rows, int32_t k, const void* blocks, void* nibb
  * Weights and activations enter the products unrounded (8-bit codes as whole
  * numbers, their scales times the sums of a block); sums are fp32; y is rounded
  * once. |x| up to 2^115; a token with a value that is not finite has no finite
- * result.
+ * result; a weight scale that is not finite shows in its feature alone, as the
+ * formula has it.
  * workspace: moe_q4_workspace_bytes bytes of device memory, 256-byte aligned,
  * with any content, NULL if 0; calls that may run at once (other streams,
  * graphs replayed side by side) need one each. flags: MOE_ACCUMULATE or 0. */

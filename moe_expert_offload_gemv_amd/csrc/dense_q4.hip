@@ -467,7 +467,9 @@ __global__ __launch_bounds__(64 * kDotWaves) void q4_dot_kernel(Q4Args a) {
       for (int t = 0; t < T; ++t) acc[r][t] = 0.f;
 #pragma unroll
       for (int j = 0; j < BPL; ++j) {
-        block_dots<XT, T>(w[r][j], half_to_float(d[r][j]), x[j], acc[r]);
+        // past the row the last block again, with zeros for x: its scale may be infinite
+        const uint16_t scale = lb + LPR * j < KB ? d[r][j] : (uint16_t)0;
+        block_dots<XT, T>(w[r][j], half_to_float(scale), x[j], acc[r]);
         // the row's registers are free: its loads of the next group
         const int row = min(((g + stride) * NR + r) * RPW + side, N - 1);
         const int64_t at = (int64_t)row * KB + min(lb + LPR * j, KB - 1);

@@ -139,3 +139,23 @@ def test_a_pending_error_of_another_call_is_not_the_experts():
         assert gbps > 0 and (y - want).abs().max() <= 1e-5 * want.abs().max()
     finally:
         d.close()
+
+
+# ---------------------------------------------------------------------------
+# dense product: an infinite weight scale belongs to its feature and block alone
+
+
+# the dot product's lane layouts with places past the row, tiles, and split tiles
+@pytest.mark.parametrize("T,N,K", [(1, 9, 96), (1, 9, 544), (1, 40, 2080), (2, 40, 1056), (1, 40, 4128), (1, 40, 8224),
+                                   (4, 40, 2080), (8, 33, 4128), (20, 33, 96), (40, 33, 2080), (200, 3001, 3744)])
+@pytest.mark.parametrize("xt", ["f32", "bf16", "f16", "q8"])
+def test_q4_matmul_infinite_scale_of_the_last_block(T, N, K, xt):
+    p = Product(T, N, K, xt, seed=2)
+    y = torch.zeros((T, N), device="cuda")
+    p.scl[3, -1], p.scl[5, -1], p.scl[7, -1] = float("inf"), float("-inf"), float("nan")
+    p.nib[3, -1] = p.nib[5, -1] = 0x99  # q - 8 = 1: the block's sum is that of x
+    p.x[:, -32:] = p.x[:, -32:].abs() + 1 if xt != "q8" else p.x[:, -32:].clamp(1)
+    moe.moe_q4_matmul(p.x, p.nib, p.scl, y, scales=p.scales)
+    assert (y[:, 3] == float("inf")).all() and (y[:, 5] == float("-inf")).all() and torch.isnan(y[:, 7]).all()
+    rest = [n for n in range(N) if n not in (3, 5, 7)]
+    assert torch.isfinite(y[:, rest]).all()
