@@ -381,10 +381,23 @@ def _flat(name, t, dev, shape, dtype):
     return t.data_ptr()
 
 
-def _two_dims(name, t):
-    if t.dim() != 2:
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, two dimensions are needed")
-    return t.shape
+def _fits(*values) -> bool:
+    """Whether ctypes hands each on as it is: it cuts an int to an int32 parameter's bits without a word."""
+    return all(-0x80000000 <= v <= 0x7FFFFFFF for v in values)
+
+
+def _dims(name, t, n):
+    """The shape of a tensor of n dimensions (two: rows)."""
+    shape = t.shape
+    if len(shape) != n or shape[0] > 0x7FFFFFFF or shape[1] > 0x7FFFFFFF:
+        raise ValueError(f"{name}: shape {tuple(shape)}; {n} dimensions of at most 2147483647 are needed")
+    return shape
+
+
+def _number(name, v):
+    if not -0x80000000 <= v <= 0xFFFFFFFF:  # within it the library sees the value, or one that it refuses
+        raise ValueError(f"{name}: {v} is out of range")
+    return v
 
 
 def _workspace(t, dev, stream, make):
@@ -407,7 +420,7 @@ def moe_add_rmsnorm(x, weight, out, residual=None, residual_out=None, scales=Non
     scales fp32 [T][H/32] (MOE_Q8_32). residual [T][H] is updated in place unless residual_out is given.
     """
     L = _dense()
-    shape, dev = _two_dims("x", x), x.get_device()
+    shape, dev = _dims("x", x, 2), x.get_device()
     T, H = shape
     xt, xp, xs = _rows("x", x, dev, shape)
     ot, op, os_ = _rows("out", out, dev, shape)
@@ -444,7 +457,7 @@ def moe_q4_split(blocks):
 
 
 def moe_q4_workspace_bytes(n_tokens: int, n_out: int, k: int, x_type: int) -> int:
-    return int(lib().moe_q4_workspace_bytes(n_tokens, n_out, k, x_type))
+    return int(lib().moe_q4_workspace_bytes(n_tokens, n_out, k, x_type)) if _fits(n_tokens, n_out, k, x_type) else -1
 
 
 def moe_q4_workspace(x, nibbles):
@@ -452,7 +465,8 @@ def moe_q4_workspace(x, nibbles):
     import torch
 
     _dense()
-    n = moe_q4_workspace_bytes(x.shape[0], nibbles.shape[0], x.shape[1], _types.get(x.dtype, -1))
+    T, K = _dims("x", x, 2)
+    n = moe_q4_workspace_bytes(T, _dims("nibbles", nibbles, 3)[0], K, _types.get(x.dtype, -1))
     if n < 0:
         raise ValueError(f"no product of x {x.dtype} {tuple(x.shape)} with weights {tuple(nibbles.shape)}")
     return torch.empty(n, dtype=torch.uint8, device=x.device) if n else None
@@ -465,9 +479,9 @@ def moe_q4_matmul(x, nibbles, w_scales, y, scales=None, workspace=None, flags: i
     a call that needs one allocates it from torch.
     """
     L = _dense()
-    shape, dev = _two_dims("x", x), x.get_device()
+    shape, dev = _dims("x", x, 2), x.get_device()
     T, K = shape
-    N = nibbles.shape[0]
+    N = _dims("nibbles", nibbles, 3)[0]
     xt, xp, xs = _rows("x", x, dev, shape)
     np_ = _flat("nibbles", nibbles, dev, (N, K // 32, 16), "torch.uint8")
     wp = _flat("w_scales", w_scales, dev, (N, K // 32), "torch.float16")
@@ -478,20 +492,21 @@ def moe_q4_matmul(x, nibbles, w_scales, y, scales=None, workspace=None, flags: i
         if st != MOE_F32:
             raise ValueError(f"scales: {scales.dtype}")
     workspace, kp, kn = _workspace(workspace, dev, stream, lambda: moe_q4_workspace(x, nibbles))
-    rc = L.moe_q4_matmul(dev, _stream_of(stream, dev), T, N, K, xt, xp, xs, sp, ss, np_, wp, yt, yp, ys, kp, kn, flags)
+    rc = L.moe_q4_matmul(dev, _stream_of(stream, dev), T, N, K, xt, xp, xs, sp, ss, np_, wp, yt, yp, ys, kp, kn,
+                         _number("flags", flags))
     if rc:
         _check(None, rc)
 
 
 def moe_router_balance_workspace_bytes(n_tokens: int, n_experts: int) -> int:
-    return int(lib().moe_router_balance_workspace_bytes(n_tokens, n_experts))
+    return int(lib().moe_router_balance_workspace_bytes(n_tokens, n_experts)) if _fits(n_tokens, n_experts) else -1
 
 
 def moe_router_balance_workspace(logits):
     """A workspace tensor for moe_router_balance of these logits."""
     import torch
 
-    n = moe_router_balance_workspace_bytes(*logits.shape)
+    n = moe_router_balance_workspace_bytes(*_dims("logits", logits, 2))
     if n < 0:
         raise ValueError(f"no balance of logits {tuple(logits.shape)}")
     return torch.empty(n, dtype=torch.uint8, device=logits.device)
@@ -505,7 +520,7 @@ def moe_router_balance(logits, top_k: int, counts, load, stats, lse, valid=None,
     out tokens. Without a workspace the call allocates it from torch.
     """
     L = _dense()
-    shape, dev = _two_dims("logits", logits), logits.get_device()
+    shape, dev = _dims("logits", logits, 2), logits.get_device()
     T, E = shape
     zt, zp, zs = _rows("logits", logits, dev, shape)
     vp = None
@@ -516,8 +531,8 @@ def moe_router_balance(logits, top_k: int, counts, load, stats, lse, valid=None,
     tp = _flat("stats", stats, dev, (4,), "torch.float32")
     ep = _flat("lse", lse, dev, (T,), "torch.float32")
     workspace, kp, kn = _workspace(workspace, dev, stream, lambda: moe_router_balance_workspace(logits))
-    rc = L.moe_router_balance(dev, _stream_of(stream, dev), T, E, top_k, zt, zp, zs, vp, balance, z, cp, lp, tp, ep, kp,
-                              kn, flags)
+    rc = L.moe_router_balance(dev, _stream_of(stream, dev), T, E, _number("top_k", top_k), zt, zp, zs, vp, balance, z, cp, lp,
+                              tp, ep, kp, kn, _number("flags", flags))
     if rc:
         _check(None, rc)
 
@@ -526,7 +541,7 @@ def moe_router_balance_grad(logits, load, stats, lse, dlogits, dloss=None, balan
                             stream=None) -> None:
     """dlogits [T][E] = gradient of stats[0] to the logits, times dloss (fp32 [1], None: 1)."""
     L = _dense()
-    shape, dev = _two_dims("logits", logits), logits.get_device()
+    shape, dev = _dims("logits", logits, 2), logits.get_device()
     T, E = shape
     zt, zp, zs = _rows("logits", logits, dev, shape)
     lp = _flat("load", load, dev, (E,), "torch.float32")
@@ -535,6 +550,6 @@ def moe_router_balance_grad(logits, load, stats, lse, dlogits, dloss=None, balan
     gp = _flat("dloss", dloss, dev, (1,), "torch.float32")
     dt, dp, ds = _rows("dlogits", dlogits, dev, shape)
     rc = L.moe_router_balance_grad(dev, _stream_of(stream, dev), T, E, zt, zp, zs, lp, tp, ep, gp, balance, z, dt, dp, ds,
-                                   flags)
+                                   _number("flags", flags))
     if rc:
         _check(None, rc)

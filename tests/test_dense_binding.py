@@ -1,0 +1,100 @@
+"""The binding of the operators beside the experts (CPU only): sizes and
+flags that do not fit the library's 32-bit parameters are refused, not cut."""
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import moe_expert_offload_gemv_amd as moe  # noqa: E402
+
+
+class Rows:
+    """A tensor of the sizes asked for, in nobody's memory: no call here may get as far as touching it."""
+
+    def __init__(self, *shape, dtype=torch.float32):
+        self.shape, self.dtype, self.device = torch.Size(shape), dtype, torch.device("cuda", 0)
+
+    def dim(self):
+        return len(self.shape)
+
+    def get_device(self):
+        return 0
+
+    def stride(self):
+        n = [1]
+        for d in reversed(self.shape[1:]):
+            n.insert(0, n[0] * d)
+        return tuple(n)
+
+    def is_contiguous(self):
+        return True
+
+    def data_ptr(self):
+        return 0x10000
+
+    def numel(self):
+        return self.shape.numel()
+
+    def element_size(self):
+        return torch.empty((), dtype=self.dtype).element_size()
+
+
+def planes(n, k):
+    return Rows(n, k // 32, 16, dtype=torch.uint8), Rows(n, k // 32, dtype=torch.float16)
+
+
+MANY = (1 << 32) + 2  # 2 in 32 bits
+
+
+def test_sizes_past_32_bits_are_refused():
+    with pytest.raises(ValueError, match="x: shape"):
+        moe.moe_add_rmsnorm(Rows(MANY, 64), None, Rows(MANY, 64))
+    with pytest.raises(ValueError, match="x: shape"):
+        moe.moe_add_rmsnorm(Rows(2, MANY), None, Rows(2, MANY))
+    with pytest.raises(ValueError, match="x: shape"):
+        moe.moe_q4_matmul(Rows(MANY, 64), *planes(8, 64), Rows(MANY, 8))
+    with pytest.raises(ValueError, match="nibbles: shape"):
+        moe.moe_q4_matmul(Rows(2, 64), *planes(MANY, 64), Rows(2, MANY))
+    for ws in (moe.moe_q4_workspace, lambda x, nib: moe.moe_q4_matmul(x, nib, None, None)):
+        with pytest.raises(ValueError, match="x: shape"):
+            ws(Rows(MANY, 64), planes(8, 64)[0])
+    E = 8
+    outs = [Rows(E, dtype=torch.int32), Rows(E), Rows(4)]
+    with pytest.raises(ValueError, match="logits: shape"):
+        moe.moe_router_balance(Rows(MANY, E), 2, *outs, Rows(MANY))
+    with pytest.raises(ValueError, match="logits: shape"):
+        moe.moe_router_balance_grad(Rows(MANY, E), outs[1], outs[2], Rows(MANY), Rows(MANY, E))
+    with pytest.raises(ValueError, match="logits: shape"):
+        moe.moe_router_balance_workspace(Rows(MANY, E))
+
+
+def test_workspace_sizes_of_sizes_past_32_bits():
+    for bad in ((MANY, 8, 64, 0), (2, MANY, 64, 0), (2, 8, (1 << 32) + 64, 0), (2, 8, 64, 1 << 32), (2 - (1 << 33), 8, 64, 0)):
+        assert moe.moe_q4_workspace_bytes(*bad) == -1
+    assert moe.moe_router_balance_workspace_bytes(MANY, 8) == -1
+    assert moe.moe_router_balance_workspace_bytes(2, (1 << 32) + 8) == -1
+
+
+def test_flags_and_picks_past_32_bits_are_refused(monkeypatch):
+    monkeypatch.setattr(moe, "_stream_of", lambda stream, dev: None)
+    ws = Rows(1 << 20, dtype=torch.uint8)
+    E = 8
+    outs = [Rows(E, dtype=torch.int32), Rows(E), Rows(4), Rows(2)]
+    for top_k, flags, what in (((1 << 32) + 2, 0, "top_k"), (2, 1 << 32, "flags"), (2, -(1 << 40), "flags")):
+        with pytest.raises(ValueError, match=what):
+            moe.moe_router_balance(Rows(2, E), top_k, *outs, workspace=ws, flags=flags)
+    with pytest.raises(ValueError, match="flags"):
+        moe.moe_router_balance_grad(Rows(2, E), outs[1], outs[2], outs[3], Rows(2, E), flags=1 << 32)
+    with pytest.raises(ValueError, match="flags"):
+        moe.moe_q4_matmul(Rows(2, 64), *planes(8, 64), Rows(2, 8), workspace=ws, flags=1 << 32)
+
+
+def test_tensors_of_other_dimensions_are_refused():
+    one = Rows(64)
+    with pytest.raises(ValueError, match="nibbles: shape"):
+        moe.moe_q4_matmul(Rows(2, 64), Rows(), Rows(8, 2, dtype=torch.float16), Rows(2, 8))
+    with pytest.raises(ValueError, match="x: shape"):
+        moe.moe_q4_workspace(one, planes(8, 64)[0])
+    with pytest.raises(ValueError, match="nibbles: shape"):
+        moe.moe_q4_workspace(Rows(2, 64), one)
+    with pytest.raises(ValueError, match="logits: shape"):
+        moe.moe_router_balance_workspace(one)
