@@ -539,7 +539,8 @@ MOE_API int64_t moe_q4_workspace_bytes(int32_t n_tokens, int32_t n_out, int32_t 
  *              z term       = z_coef * mean_t lse[t]^2
  * Tokens with valid[t] == 0 (uint8; NULL: none) and tokens whose logits are all
  * -inf are left out of every sum: their lse is -inf. With n = 0 the loads and
- * losses are 0. A NaN or +inf logit makes the losses NaN.
+ * losses are 0. A NaN or +inf logit makes the losses NaN; among the picks a NaN
+ * stands above +inf, or below -inf if its sign bit is set.
  * n_experts 1..4096, top_k 1..min(n_experts, 32). counts
  * int32 [E], load fp32 [E], stats fp32 [4], lse fp32 [n_tokens] are outputs.
  * workspace: moe_router_balance_workspace_bytes bytes of device memory,

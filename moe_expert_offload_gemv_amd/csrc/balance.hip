@@ -257,8 +257,8 @@ __device__ __forceinline__ uint32_t kth_bits(const uint32_t (&b)[NE], int k, int
     for (int i = 0; i < 8; ++i) above += t[i] > m ? 1 : 0;
     return m;
   } else {
-    // a row keeps its place while others of the wave go on; at most k / 8 passes,
-    // for each but the last leaves 8 logits or more behind
+    // a row keeps its place while others of the wave go on; at most ceil(k / 8)
+    // passes, for each but the last leaves 8 logits or more behind
     uint32_t below = ~0u;
     int left = k;  // > 0: the k-th is the left-th of those not above `below`
     m = 0;
@@ -344,6 +344,15 @@ __global__ __launch_bounds__(256, NE <= 32 ? 2 : 1) void balance_rows_kernel(Bal
     const float inv = counted ? 1.0f / sum : 0.f;
     z2 = counted ? fmaf(lse, lse, z2) : z2;
     n += counted ? 1 : 0;
+    if (ZT == MOE_F32 && __ballot(lse != lse)) {
+      // the NaN whose bits are all ones (no 16-bit one has them in fp32) has the order bits of no
+      // expert: one more makes it the lowest of the row's logits instead
+      int gt = gl;
+      asm volatile("" : "+v"(gt));  // as below
+#pragma unroll
+      for (int j = 0; j < NE; ++j)
+        if (run_of<G>(j, gt, E).has(j & 3)) b[j] = max(b[j], 1u);
+    }
     int above;
     const uint32_t m = kth_bits<G, NE, TOP8>(b, k, above);
     // in the set: bits above floor, all ones for a row that does not count

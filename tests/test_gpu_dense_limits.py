@@ -159,3 +159,30 @@ def test_q4_matmul_infinite_scale_of_the_last_block(T, N, K, xt):
     assert (y[:, 3] == float("inf")).all() and (y[:, 5] == float("-inf")).all() and torch.isnan(y[:, 7]).all()
     rest = [n for n in range(N) if n not in (3, 5, 7)]
     assert torch.isfinite(y[:, rest]).all()
+
+
+# ---------------------------------------------------------------------------
+# router balance: NaN of any bits
+
+
+@pytest.mark.parametrize("T,n_e", [(5, 3), (40, 8), (40, 60), (40, 100), (40, 200), (40, 512), (2100, 200), (2100, 500), (9, 1000),
+                                   (9, 1500), (9, 4093)])
+@pytest.mark.parametrize("zt", ["f32", "f16", "bf16"])
+def test_router_balance_counts_its_picks_beside_nan(T, n_e, zt):
+    g = rng_of(42, T, n_e)
+    for k in {min(3, n_e), min(8, n_e), min(9, n_e), min(32, n_e)}:
+        z = torch.from_numpy(g.standard_normal((T, n_e))).to(TYPES[zt])
+        ones = z.view(torch.int32 if zt == "f32" else torch.int16)
+        ones[1] = -1                                     # the lowest NaN there is, in every place
+        ones[2, n_e // 2:] = -1                          # fewer numbers than picks, for few experts
+        ones[3, [0, n_e - 1]] = -1
+        z[4, n_e // 3] = float("nan")
+        want = np.zeros(n_e, np.int64)
+        # the order of moe_forward's picks: a NaN with the sign bit below all numbers, one without above
+        key = z.float().numpy().view(np.uint32).astype(np.int64)
+        key = np.where(key >> 31, 0xFFFFFFFF - key, key | 0x80000000)
+        np.add.at(want, np.argsort(-key, axis=1, kind="stable")[:, :k].ravel(), 1)
+        b = Balance(z, k)
+        b.forward()
+        assert np.array_equal(b.counts.cpu().numpy(), want), k
+        assert torch.isnan(b.stats[:3]).all() and b.stats[3] == T
