@@ -512,7 +512,8 @@ MOE_API int moe_q4_split(int32_t rows, int32_t k, const void* blocks, void* nibb
  * MOE_F16 or MOE_BF16. n_out >= 1, k a multiple of 32, 32..2^20.
  * Weights and activations enter the products unrounded (8-bit codes as whole
  * numbers, their scales times the sums of a block); sums are fp32; y is rounded
- * once. |x| up to 2^115; a token with a value that is not finite has no finite
+ * once. |x| up to 2^115, and bits of an fp32 x below 2^-133 may be cut off (values
+ * from 2^-110 on have none); a token with a value that is not finite has no finite
  * result; a weight scale that is not finite shows in its feature alone, as the
  * formula has it.
  * workspace: moe_q4_workspace_bytes bytes of device memory, 256-byte aligned,

@@ -27,7 +27,8 @@
 // activations' operand. The block's scale is applied to the sum in fp32. Activations enter
 // unrounded: bf16 and fp16 as they are, 8-bit codes as whole numbers whose scale
 // joins the block's, fp32 as three bf16 terms cut from the top, 8 bits each, whose
-// sum is the value.
+// sum is the value (down to bf16's last bit, 2^-133: the third term of a value below
+// 2^-110 loses what lies under it).
 //
 // Operand order: as in grouped_mfma.hip. Lane l covers row/column l % 16 and
 // chunk c = l / 16 of a block, the elements 4c + {0, 2, 1, 3, 16, 18, 17, 19};

@@ -186,3 +186,31 @@ def test_router_balance_counts_its_picks_beside_nan(T, n_e, zt):
         b.forward()
         assert np.array_equal(b.counts.cpu().numpy(), want), k
         assert torch.isnan(b.stats[:3]).all() and b.stats[3] == T
+
+
+# ---------------------------------------------------------------------------
+# dense product: activations near the end of fp32's range
+
+
+@pytest.mark.parametrize("T,N,K", [(1, 40, 256), (20, 40, 256), (200, 4100, 4096), (4100, 4100, 160)])
+@pytest.mark.parametrize("xt", ["f32", "bf16"])
+def test_q4_matmul_tiny_activations(T, N, K, xt):
+    p = Product(T, N, K, xt, seed=3)
+    p.scl *= 2048  # the smallest of them times x is then a normal fp32 number still
+    g = rng_of(43, T, N, K)
+    q = torch.cat([p.nib & 15, p.nib >> 4], dim=2).float() - 8
+    w = (q * p.scl.float().unsqueeze(2)).view(N, K).double()
+    base = torch.from_numpy(g.standard_normal((T, K))).cuda()
+    y = torch.zeros((T, N), device="cuda")
+    for e in (-100, -109, -112, -118, -124, -130, -140):
+        x = (base * 2.0 ** e).to(TYPES[xt])
+        moe.moe_q4_matmul(x, p.nib, p.scl, y)
+        ref = x.double() @ w.t().contiguous()
+        # p.rms as for ordinary values (sums in fp32: a block's from its start, the values below 2^-126 to
+        # 2^-150 each); of an fp32 value the bits below 2^-133, all of one sign
+        cut = (2.0 ** -133 if xt == "f32" else 0.0) * w.abs().sum(dim=1)
+        ends = 2.0 ** -150 * (192 * p.scl.double().abs().sum(dim=1) + 2 * K)
+        off = (y.double() - ref).abs()
+        size = torch.linalg.norm(ref, dim=1, keepdim=True) / N ** 0.5
+        # the largest of N T errors of size p.rms: eight of them
+        assert (off <= 8 * (p.rms + E) * size + (cut + ends) * 1.01).all(), e
