@@ -9,9 +9,10 @@
 //                   registers. Bound by the weights' bytes (1 x 65537 x 4096 bf16, 151 MB, 28 us =
 //                   5.4 TB/s, a streaming read) or, for few rows, by a launch and two trips to memory
 //                   (1 x 2048 x 2048 fp32, 4.0 us).
-//   q4_tile_kernel  up to 2e9 products: 16 tokens a work-group on the matrix cores, one
-//                   launch (32 x 4096 x 1536 fp32, 7.4 us; 201 x 1001 x 1056 fp16, 7.3: rounds of
-//                   load, convert, barrier and product, 1 us each).
+//   q4_tile_kernel  up to 32 tokens or 2e9 products, and where the next would have too few tiles
+//                   (wide_split): 16 tokens a work-group on the matrix cores, one launch (32 x 4096 x
+//                   1536 fp32, 7.4 us; 201 x 1001 x 1056 fp16, 7.3: rounds of load, convert, barrier and
+//                   product, 1 us each).
 //   q4_wide_kernel  more: the activations are brought into operand form once, 64 x 64 tiles
 //                   per wave (4096 x 5120 x 4096 bf16, 172 GFLOP, 267-286 us = 0.62 PFLOP/s, 17 of them the
 //                   operand pass; the library's plain bf16 product of the same sizes would take 153). Per step of
@@ -1122,15 +1123,35 @@ hipError_t launch_operand(const Q4Args& a, const Operand& o, hipStream_t s) {
 // k = 2^20 are 2^25 operand units; 128 row tiles of 2^22 features 2^22 tiles)
 constexpr int64_t kPassTokens = 16384;
 
-// 0: one launch without an operand pass; else the WK of the wide tiles.
-// Below about 2e9 products the one launch wins, whatever their shape (bf16, us on the GPU:
-// 128 x 2048 x 2048, 0.5e9, 10.4 against 16.7 split; 64 x 5120 x 4096, 1.3e9, 21.5 against 24.6;
-// 300 x 1024 x 8192, 2.5e9, 37.8 against 39.6; 128 x 5120 x 4096, 2.7e9, 33.0 against 25.2). Whole
-// 128 x 128 tiles pay from four work-groups per CU on (1024 x 5120 x 4096, 320 tiles, 107 against
-// 80 split; 2048 tokens, 640 tiles, 161 against 153; 4096 tokens, 1280 tiles, 275 against 306).
-int wide_split(int64_t T, int64_t N, int64_t K) {
+// 0: one launch without an operand pass; else the WK of the wide tiles. us on the GPU, one launch /
+// split tiles / whole tiles:
+//                                   bf16              fp32              codes
+//   128 x 2048 x 4096, 1.1e9          16 /  24 /  71    24 /  37 / 111    16 /  29 /  89
+//   1024 x 1024 x 1024, 1.1e9         17 /  15 /  28    27 /  19 /  38    17 /  17 /  32
+// From 2e9 products on the operand pass pays, if every second CU or so has a tile of 64 x 64 to
+// work on: each is one work-group and goes through the whole reduction by itself.
+//   64 x 512 x 65536, 8 tiles         77 / 213 / 935   140 / 407 / 1627   76 / 292 / 1229
+//   300 x 1024 x 8192, 80             35 /  39 / 129    62 /  65 / 210    35 /  48 / 166
+//   64 x 6144 x 8192, 96              37 /  37 / 128    65 /  64 / 209    38 /  48 / 165
+//   64 x 7168 x 8192, 112             47 /  37 / 128    78 /  64 / 209    47 /  48 / 165
+//   512 x 1024 x 4096, 128            26 /  25 /  72    45 /  40 / 112    26 /  30 /  90
+//   128 x 5120 x 4096, 160            32 /  25 /  71    57 /  39 / 111    33 /  30 /  89
+// The pass reads and writes all activations, which a few features do not repay:
+//   8192 x 256 x 1024                 30 /  24 /  33    52 /  46 /  53    30 /  26 /  38
+//   16384 x 128 x 1024                31 /  31 /  40    55 /  64 /  68    30 /  32 /  45
+//   100000 x 64 x 512                 62 / 140 / 196   105 / 227 / 279    58 / 151 / 219
+// (beyond 2^20 tokens the one launch would have too many work-groups for a grid). Whole tiles of
+// 128 x 128: two work-groups a CU, against one of split fp32 tiles, whose three terms fill the LDS.
+//   512 x 5120 x 4096, 160           107 /  51 /  73   188 / 108 / 114   111 /  59 /  90
+//   1024 x 4096 x 4096, 256          159 /  66 /  75   286 / 147 / 120   161 /  75 /  93
+//   2048 x 5120 x 4096, 640          406 / 154 / 172   714 / 361 / 302   393 / 178 / 200
+//   4096 x 4096 x 1024, 1024         199 /  86 /  70   341 / 208 / 119   198 /  98 /  80
+//   48 x 65537 x 1024, 513 (of 48 tokens)  47 / 33 / 50  73 / 61 / 72     42 /  35 /  59
+int wide_split(int64_t T, int64_t N, int64_t K, int32_t x_type) {
   if (T <= 32 || (double)T * (double)N * (double)K <= 2e9) return 0;
-  return ((T + 127) / 128) * ((N + 127) / 128) >= 1024 ? 1 : 4;
+  const int64_t split = ((T + 63) / 64) * ((N + 63) / 64), whole = ((T + 127) / 128) * ((N + 127) / 128);
+  if (split < (x_type == MOE_Q8_32 ? 160 : 112) || (N < 256 && T <= 1 << 20)) return 0;
+  return whole >= (x_type == MOE_F32 && T > 256 ? 256 : 1024) ? 1 : 4;
 }
 
 template <int XT, int WK>
@@ -1156,7 +1177,7 @@ hipError_t launch_wide(const Q4Args& a, hipStream_t s) {
 
 template <int XT>
 hipError_t launch_types(const Q4Args& a, hipStream_t s) {
-  switch (wide_split(a.T, a.N, a.K)) {
+  switch (wide_split(a.T, a.N, a.K, XT)) {
     case 1: return launch_wide<XT, 1>(a, s);
     case 4: return launch_wide<XT, 4>(a, s);
   }
@@ -1167,7 +1188,7 @@ hipError_t launch_types(const Q4Args& a, hipStream_t s) {
 }  // namespace
 
 int64_t q4_workspace_bytes(int64_t T, int64_t N, int64_t K, int32_t x_type) {
-  const int WK = wide_split(T, N, K);
+  const int WK = wide_split(T, N, K, x_type);
   if (!WK) return 0;
   const int terms = x_type == MOE_F32 ? terms_of<MOE_F32>() : 1, runs = x_type == MOE_Q8_32 ? runs_of<MOE_Q8_32>() : 1;
   return Operand::make(nullptr, std::min(T, kPassTokens), K, terms, runs, wide_side(WK)).bytes;

@@ -214,3 +214,71 @@ def test_q4_matmul_tiny_activations(T, N, K, xt):
         size = torch.linalg.norm(ref, dim=1, keepdim=True) / N ** 0.5
         # the largest of N T errors of size p.rms: eight of them
         assert (off <= 8 * (p.rms + E) * size + (cut + ends) * 1.01).all(), e
+
+
+# ---------------------------------------------------------------------------
+# dense product: which form a call takes
+
+
+# (tokens, features, reduction, types with an operand pass): rows too long, tiles too few or features too few for it
+# (one launch), split tiles, and whole tiles (fp32: from fewer of them on)
+FORMS = [(64, 510, 65536, ""), (33, 2050, 31008, ""), (300, 1024, 7008, ""), (17000, 255, 512, ""), (33000, 70, 960, ""),
+         (448, 1000, 4800, "f32 bf16 f16"), (200, 4001, 3936, "f32 bf16 f16 q8"), (260, 2100, 4000, "f32 bf16 f16 q8"),
+         (8200, 257, 992, "f32 bf16 f16 q8"), (1030, 4200, 512, "f32 bf16 f16 q8"), (16500, 258, 512, "f32 bf16 f16 q8")]
+
+
+@pytest.mark.parametrize("T,N,K,passes", FORMS)
+@pytest.mark.parametrize("xt", ["f32", "bf16", "f16", "q8"])
+def test_q4_matmul_forms(T, N, K, passes, xt):
+    p = Product(T, N, K, xt, seed=4)
+    y = torch.zeros((T, N), device="cuda")
+    ws = moe.moe_q4_workspace(p.x, p.nib)
+    assert (ws is not None) == (xt in passes.split())
+    if ws is not None:
+        ws.fill_(255)
+    moe.moe_q4_matmul(p.x, p.nib, p.scl, y, scales=p.scales, workspace=ws)
+    p.check(y, torch.float32)
+    first = y.clone()
+    moe.moe_q4_matmul(p.x, p.nib, p.scl, y, scales=p.scales, workspace=ws)
+    assert torch.equal(first, y)
+    # a token that is not finite shows in its row alone
+    if xt == "q8":
+        p.scales[3, 1] = float("nan")
+    else:
+        p.x[3, 40] = float("inf")
+    moe.moe_q4_matmul(p.x, p.nib, p.scl, y, scales=p.scales, workspace=ws)
+    assert torch.isnan(y[3]).all()
+    assert torch.equal(torch.cat([y[:3], y[4:]]), torch.cat([first[:3], first[4:]]))
+
+
+@pytest.mark.parametrize("xt", ["f32", "bf16", "q8"])
+def test_q4_matmul_split_tiles_at_once_and_captured(xt):
+    T, N, K = 200, 4001, 3936
+    ps = [Product(T, N, K, xt, seed=s) for s in (5, 6)]
+    ys, wss = [torch.zeros((T, N), device="cuda") for _ in ps], [moe.moe_q4_workspace(p.x, p.nib) for p in ps]
+    streams = [torch.cuda.Stream() for _ in ps]
+    assert all(ws is not None for ws in wss)
+    for p, y, ws in zip(ps, ys, wss):
+        moe.moe_q4_matmul(p.x, p.nib, p.scl, y, scales=p.scales, workspace=ws)
+    torch.cuda.synchronize()
+    want = [y.clone() for y in ys]
+    for y in ys:
+        y.zero_()
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for p, y, ws, s in zip(ps, ys, wss, streams):
+            moe.moe_q4_matmul(p.x, p.nib, p.scl, y, scales=p.scales, workspace=ws, stream=s)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(ys, want))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for p, y in zip(ps, ys):
+            moe.moe_q4_matmul(p.x, p.nib, p.scl, y, scales=p.scales, workspace=wss[0])
+    for _ in range(3):
+        for y in ys:
+            y.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(ys, want))
+        moe.moe_q4_matmul(ps[1].x, ps[1].nib, ps[1].scl, ys[0], scales=ps[1].scales, workspace=wss[0])
+        torch.cuda.synchronize()
