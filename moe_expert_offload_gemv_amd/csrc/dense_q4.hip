@@ -906,11 +906,20 @@ struct Turn {
     return t;
   }
   __device__ __forceinline__ void step(const StepWeights& st, int s, int lane, int KB, uint32_t (&w)[4], float (&d)[4]) const {
+    exchange();  // the tile before has been read
     *reinterpret_cast<u32x4_t*>(write_w) = st.w;
     *reinterpret_cast<float*>(write_d) = 4 * s + (lane & 3) < KB ? half_to_float((uint16_t)st.d) : 0.f;
+    exchange();
     const f32x4_t v = *reinterpret_cast<const f32x4_t*>(read_d);
 #pragma unroll
     for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const uint32_t*>(read_w[i]), d[i] = v[i];
+  }
+  // other lanes' words behind this point and before it: an order for the compiler, no
+  // instruction, since a wave's LDS accesses are in order
+  static __device__ __forceinline__ void exchange() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
   }
 };
 
