@@ -589,13 +589,15 @@ struct StepWeights {
   u32x4_t w;
   uint32_t d;
 };
+// vector memory loads of a load_step: the waits of the wide kernel count them
+constexpr int kStepLoads = 2;
 // The products' column of a tile's feature and back: columns 4i + j and
 // features 4j + i.
 __device__ __forceinline__ constexpr int column_of(int f) { return 4 * (f & 3) + (f >> 2); }
 
 // blocks 4s .. of the row whose first block is `row`; past the row: its last
 // block, whose scale counts as 0 in step_ready. Nothing is done to the results
-// here, which would wait for them.
+// here, which would wait for them. kStepLoads loads, one for each member of st.
 __device__ __forceinline__ void load_step(const u32x4_t* nib, const uint16_t* scl, uint32_t row, int s, int lane, int KB,
                                           StepWeights& st) {
   const uint32_t at = row + (uint32_t)min(4 * s + (lane & 3), KB - 1);
@@ -931,6 +933,7 @@ __global__ __launch_bounds__(256, 2) void q4_wide_kernel(Q4Args a, Operand o, in
   constexpr int kSums = WK > 1 ? WK * 16 * 64 * 16 : 0;
   constexpr int kLds = RING * kStage * WK;
   static_assert(RING == 2 || SB == 1, "the ring's waits count blocks");
+  static_assert(sizeof(StepWeights::w) == 16, "a load_step is one load of 16 bytes and one of a scale: kStepLoads");
   __shared__ __attribute__((aligned(1024))) uint8_t s_lds[kLds + 4 * kTurnBytes > kSums ? kLds + 4 * kTurnBytes : kSums];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 15, c = lane >> 4;
@@ -1016,7 +1019,7 @@ __global__ __launch_bounds__(256, 2) void q4_wide_kernel(Q4Args a, Operand o, in
       // back in order: behind it are RING - 2 stages and, if they were issued in between, the step's weights.
       constexpr int kAfter = (RING - 2) * kCopies;
       if (RING > 2 && h >= 1 && h <= RING - 2)
-        __builtin_amdgcn_s_waitcnt(waitcnt_vm(kAfter + 8));
+        __builtin_amdgcn_s_waitcnt(waitcnt_vm(kAfter + 4 * kStepLoads));
       else
         __builtin_amdgcn_s_waitcnt(waitcnt_vm(kAfter));
       if constexpr (WK == 1) __syncthreads();
