@@ -351,6 +351,11 @@ def _dense():
     return _lib or lib()
 
 
+def _fail(rc: int):
+    """Raises what a call without a context left in this thread's message."""
+    raise MoeError(rc, moe_last_error(None))
+
+
 def _stream_of(stream, dev):
     if stream is None:
         return _raw_stream(dev)
@@ -443,7 +448,7 @@ def moe_add_rmsnorm(x, weight, out, residual=None, residual_out=None, scales=Non
     rc = L.moe_add_rmsnorm(dev, _stream_of(stream, dev), T, H, xt, xp, xs, rt, rp, rs, rop, ros, wp, eps, ot, op, os_, sp,
                            ss)
     if rc:
-        _check(None, rc)
+        _fail(rc)
 
 
 def moe_q4_split(blocks):
@@ -452,7 +457,9 @@ def moe_q4_split(blocks):
     if b.ndim != 3 or b.shape[2] != 18:
         raise ValueError(f"blocks of shape [rows][k/32][18] are needed, got {b.shape}")
     nib, scl = np.empty(b.shape[:2] + (16,), np.uint8), np.empty(b.shape[:2], np.float16)
-    _check(None, lib().moe_q4_split(b.shape[0], 32 * b.shape[1], b.ctypes.data, nib.ctypes.data, scl.ctypes.data))
+    rc = lib().moe_q4_split(b.shape[0], 32 * b.shape[1], b.ctypes.data, nib.ctypes.data, scl.ctypes.data)
+    if rc:
+        _fail(rc)
     return nib, scl
 
 
@@ -495,7 +502,7 @@ def moe_q4_matmul(x, nibbles, w_scales, y, scales=None, workspace=None, flags: i
     rc = L.moe_q4_matmul(dev, _stream_of(stream, dev), T, N, K, xt, xp, xs, sp, ss, np_, wp, yt, yp, ys, kp, kn,
                          _number("flags", flags))
     if rc:
-        _check(None, rc)
+        _fail(rc)
 
 
 def moe_router_balance_workspace_bytes(n_tokens: int, n_experts: int) -> int:
@@ -534,7 +541,7 @@ def moe_router_balance(logits, top_k: int, counts, load, stats, lse, valid=None,
     rc = L.moe_router_balance(dev, _stream_of(stream, dev), T, E, _number("top_k", top_k), zt, zp, zs, vp, balance, z, cp, lp,
                               tp, ep, kp, kn, _number("flags", flags))
     if rc:
-        _check(None, rc)
+        _fail(rc)
 
 
 def moe_router_balance_grad(logits, load, stats, lse, dlogits, dloss=None, balance=0.0, z=0.0, flags: int = 0,
@@ -552,4 +559,4 @@ def moe_router_balance_grad(logits, load, stats, lse, dlogits, dloss=None, balan
     rc = L.moe_router_balance_grad(dev, _stream_of(stream, dev), T, E, zt, zp, zs, lp, tp, ep, gp, balance, z, dt, dp, ds,
                                    _number("flags", flags))
     if rc:
-        _check(None, rc)
+        _fail(rc)

@@ -98,3 +98,20 @@ def test_tensors_of_other_dimensions_are_refused():
         moe.moe_q4_workspace(Rows(2, 64), one)
     with pytest.raises(ValueError, match="logits: shape"):
         moe.moe_router_balance_workspace(one)
+
+
+def test_refusals_of_the_library_come_with_their_message(monkeypatch):
+    monkeypatch.setattr(moe, "_stream_of", lambda stream, dev: None)
+    with pytest.raises(moe.MoeError, match="moe_add_rmsnorm: eps -1"):
+        moe.moe_add_rmsnorm(Rows(2, 64), None, Rows(2, 64, dtype=torch.bfloat16), eps=-1.0)
+    with pytest.raises(moe.MoeError, match="moe_q4_matmul: x_scales go with 8-bit x"):
+        moe.moe_q4_matmul(Rows(2, 64, dtype=torch.int8), *planes(8, 64), Rows(2, 8))
+    E = 8
+    outs, ws = [Rows(E, dtype=torch.int32), Rows(E), Rows(4), Rows(2)], Rows(1 << 20, dtype=torch.uint8)
+    with pytest.raises(moe.MoeError, match="moe_router_balance: n_tokens 2, n_experts 8 or top_k 9 out of range"):
+        moe.moe_router_balance(Rows(2, E), 9, *outs, workspace=ws)
+    with pytest.raises(moe.MoeError, match="moe_router_balance_grad: unknown flags"):
+        moe.moe_router_balance_grad(Rows(2, E), *outs[1:], Rows(2, E), flags=4)
+    with pytest.raises(moe.MoeError, match="moe_q4_split: rows 5 or k 0 out of range") as e:
+        moe.moe_q4_split(torch.zeros((5, 0, 18), dtype=torch.uint8).numpy())
+    assert e.value.code == moe.MOE_E_INVAL
