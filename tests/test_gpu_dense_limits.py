@@ -282,3 +282,46 @@ def test_q4_matmul_split_tiles_at_once_and_captured(xt):
         assert all(torch.equal(a, b) for a, b in zip(ys, want))
         moe.moe_q4_matmul(ps[1].x, ps[1].nib, ps[1].scl, ys[0], scales=ps[1].scales, workspace=wss[0])
         torch.cuda.synchronize()
+
+
+# ---------------------------------------------------------------------------
+# workspaces on other streams
+
+
+@pytest.mark.parametrize("xt", ["f32", "bf16", "q8"])
+def test_q4_matmul_workspace_of_the_binding_on_a_side_stream(xt):
+    T, N, K = 200, 4001, 3936
+    p = Product(T, N, K, xt, seed=7)
+    need = moe.moe_q4_workspace(p.x, p.nib)
+    assert need is not None
+    y, side = torch.zeros((T, N), device="cuda"), torch.cuda.Stream()
+    with pytest.raises(ValueError, match="workspace"):  # torch's memory would follow the current stream, the call another
+        moe.moe_q4_matmul(p.x, p.nib, p.scl, y, scales=p.scales, stream=side)
+    with pytest.raises(ValueError, match="workspace"):
+        moe.moe_q4_matmul(p.x, p.nib, p.scl, y, scales=p.scales, stream=side.cuda_stream)
+    with pytest.raises(moe.MoeError, match="workspace"):
+        moe.moe_q4_matmul(p.x, p.nib, p.scl, y, scales=p.scales, workspace=need[:-256])
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        for _ in range(5):
+            y.zero_()
+            moe.moe_q4_matmul(p.x, p.nib, p.scl, y, scales=p.scales)
+            torch.empty_like(need).fill_(255)  # the same memory again, for the stream's next work
+    side.synchronize()
+    p.check(y, torch.float32)
+
+
+def test_router_balance_workspace_of_the_binding_on_a_side_stream():
+    b, side = Balance(torch.randn(500, 96), 6), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        for _ in range(5):
+            moe.moe_router_balance(b.z, 6, b.counts, b.load, b.stats, b.lse, balance=b.a, z=b.b)
+            torch.empty_like(b.ws).fill_(255)
+        d = torch.zeros((500, 96), device="cuda")
+        b.backward(d)
+    side.synchronize()
+    counts, stats, got = b.counts.clone(), b.stats.clone(), d.clone()
+    b.check()
+    b.backward(d)
+    assert torch.equal(counts, b.counts) and torch.equal(stats, b.stats) and torch.equal(got, d)
