@@ -518,7 +518,8 @@ MOE_API int moe_q4_split(int32_t rows, int32_t k, const void* blocks, void* nibb
  * formula has it.
  * workspace: moe_q4_workspace_bytes bytes of device memory, 256-byte aligned,
  * with any content, NULL if 0; calls that may run at once (other streams,
- * graphs replayed side by side) need one each. flags: MOE_ACCUMULATE or 0. */
+ * graphs replayed side by side) need one each. More tokens never need less: the
+ * workspace of the largest batch serves the smaller ones. flags: MOE_ACCUMULATE or 0. */
 MOE_API int moe_q4_matmul(int32_t device, void* stream, int32_t n_tokens, int32_t n_out, int32_t k,
                           int32_t x_type, const void* x, int64_t x_stride, const float* x_scales,
                           int64_t x_scales_stride, const void* nibbles, const void* w_scales,

@@ -596,8 +596,10 @@ int lanes_of(int64_t T, int E) { return E > 512 || (E > 128 && T <= kWaveRows) ?
 
 }  // namespace
 
+// enough for fewer tokens too: up to kWaveRows of them may take more work-groups
 int64_t balance_workspace_bytes(int64_t T, int32_t E) {
-  const int blocks = balance_blocks(T, 4 * 64 / lanes_of(T, E));
+  const int64_t wave = std::min<int64_t>(T, kWaveRows);
+  const int blocks = std::max(balance_blocks(T, 4 * 64 / lanes_of(T, E)), balance_blocks(wave, 4 * 64 / lanes_of(wave, E)));
   return (kOffSums + (int64_t)blocks * 2 * E * 4 + 255) / 256 * 256;
 }
 

@@ -115,3 +115,16 @@ def test_refusals_of_the_library_come_with_their_message(monkeypatch):
     with pytest.raises(moe.MoeError, match="moe_q4_split: rows 5 or k 0 out of range") as e:
         moe.moe_q4_split(torch.zeros((5, 0, 18), dtype=torch.uint8).numpy())
     assert e.value.code == moe.MOE_E_INVAL
+
+
+def test_a_workspace_serves_every_smaller_batch():
+    tokens = sorted({1, 16, 31, 32, 33, 64, 65, 127, 128, 129, 200, 256, 257, 300, 512, 513, 1000, 1024, 2047, 2048, 2049, 2064,
+                     4096, 4097, 8192, 16383, 16384, 16385, 40000, 1 << 20, (1 << 20) + 1, 1 << 24})
+    for n_experts in (1, 8, 64, 65, 128, 129, 200, 256, 257, 512, 513, 1024, 2048, 4096):
+        need = [moe.moe_router_balance_workspace_bytes(t, n_experts) for t in [0] + tokens]
+        assert need == sorted(need), n_experts
+    for x_type in (moe.MOE_F32, moe.MOE_F16, moe.MOE_BF16, moe.MOE_Q8_32):
+        for n_out in (1, 64, 255, 256, 257, 1000, 4096, 5120, 65537, 1 << 22):
+            for k in (32, 96, 256, 2048, 4096, 14336, 65536, 1 << 20):
+                need = [moe.moe_q4_workspace_bytes(t, n_out, k, x_type) for t in tokens]
+                assert need == sorted(need), (x_type, n_out, k)
