@@ -40,12 +40,14 @@
 #include <algorithm>
 
 #include "kernels.h"
+#include "lane_dev.h"
 #include "route_dev.h"
 #include "value_dev.h"
 
 namespace moe {
 namespace {
 
+using namespace lane_dev;
 using namespace value_dev;
 
 typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
@@ -86,11 +88,6 @@ __device__ __forceinline__ f32x4_t mfma(u32x4_t a, u32x4_t b, f32x4_t c) {
   }
 }
 
-// (x & m) | c in one v_bitop3 (truth table of S0 & S1 | S2)
-__device__ __forceinline__ uint32_t and_or(uint32_t x, uint32_t m, uint32_t c) {
-  return __builtin_amdgcn_bitop3_b32(x, m, c, 0xEA);
-}
-
 // the 8 weights 16 + q of a chunk from its dword: the nibble becomes the top
 // four mantissa bits of 16.0 (bf16: bits 3..6, fp16: bits 6..9)
 template <int OP>
@@ -106,23 +103,6 @@ __device__ __forceinline__ uint32_t weights_part(uint32_t w, int i) {
 template <int OP>
 __device__ __forceinline__ u32x4_t weights_of(uint32_t w) {
   return u32x4_t{weights_part<OP>(w, 0), weights_part<OP>(w, 1), weights_part<OP>(w, 2), weights_part<OP>(w, 3)};
-}
-
-// (lane group g, dword d) -> (lane group d, dword g) within each 16-lane
-// column: afterwards dword i of lane group c is the old dword c of group i
-__device__ __forceinline__ void transpose4(u32x4_t& v) {
-  auto a = __builtin_amdgcn_permlane32_swap(v.x, v.z, false, false);
-  auto b = __builtin_amdgcn_permlane32_swap(v.y, v.w, false, false);
-  auto c = __builtin_amdgcn_permlane16_swap(a[0], b[0], false, false);
-  auto d = __builtin_amdgcn_permlane16_swap(a[1], b[1], false, false);
-  v.x = c[0], v.y = c[1], v.z = d[0], v.w = d[1];
-}
-// each lane group's value in every lane of its 16-lane column
-__device__ __forceinline__ void broadcast4(uint32_t x, uint32_t (&out)[4]) {
-  const auto h = __builtin_amdgcn_permlane32_swap(x, x, false, false);
-  const auto lo = __builtin_amdgcn_permlane16_swap(h[0], h[0], false, false);
-  const auto hi = __builtin_amdgcn_permlane16_swap(h[1], h[1], false, false);
-  out[0] = lo[0], out[1] = lo[1], out[2] = hi[0], out[3] = hi[1];
 }
 
 // 4 x 4 transpose within every quad of lanes: register i of lane j and

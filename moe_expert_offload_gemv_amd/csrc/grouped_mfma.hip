@@ -44,11 +44,14 @@
 #include <stdint.h>
 
 #include "kernels.h"
+#include "lane_dev.h"
 #include "split_dev.h"
 
 namespace moe {
 
 namespace {
+
+using namespace lane_dev;
 
 typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
@@ -68,11 +71,6 @@ __device__ __forceinline__ uint32_t as_u32(f16x2_t v) {
   return u;
 }
 
-// (x & m) | c in one v_bitop3 (truth table of S0 & S1 | S2)
-__device__ __forceinline__ uint32_t and_or(uint32_t x, uint32_t m, uint32_t c) {
-  return __builtin_amdgcn_bitop3_b32(x, m, c, 0xEA);
-}
-
 // 8 weights q - 8 (exact fp16) of chunk c of a block from its dword w
 __device__ __forceinline__ f16x8_t dequant_chunk(uint32_t w) {
   constexpr uint32_t M = 0x000F000Fu, MAGIC = 0x64006400u;  // fp16 1024 in both halves
@@ -85,17 +83,6 @@ __device__ __forceinline__ f16x8_t dequant_chunk(uint32_t w) {
   r[0] = p0[0], r[1] = p0[1], r[2] = p1[0], r[3] = p1[1];
   r[4] = p2[0], r[5] = p2[1], r[6] = p3[0], r[7] = p3[1];
   return r;
-}
-
-// (lane group g, dword d) -> (lane group d, dword g) within each 16-lane
-// column of the wave: afterwards dword i of lane group c is the old dword c
-// of lane group i
-__device__ __forceinline__ void transpose4(uint4& v) {
-  auto a = __builtin_amdgcn_permlane32_swap(v.x, v.z, false, false);
-  auto b = __builtin_amdgcn_permlane32_swap(v.y, v.w, false, false);
-  auto c = __builtin_amdgcn_permlane16_swap(a[0], b[0], false, false);
-  auto d = __builtin_amdgcn_permlane16_swap(a[1], b[1], false, false);
-  v.x = c[0], v.y = c[1], v.z = d[0], v.w = d[1];
 }
 
 __device__ __forceinline__ float half_lo(uint32_t u) { return (float)as_h2(u)[0]; }
@@ -138,16 +125,6 @@ __device__ __forceinline__ void stage_run(const uint8_t* src, uint8_t* dst, int6
   uint4* d = reinterpret_cast<uint4*>(dst + off);
   const int64_t n16 = n / 16;
   for (int64_t i = threadIdx.x; i < n16; i += 256) d[i] = s[i];
-}
-
-// Each lane group's value of x in every lane of its 16-lane column: out[g]
-// holds group g's. Two swap rounds: [x0 x1 x2 x3] -> [x0 x1 x0 x1] and
-// [x2 x3 x2 x3] -> [x0 x0 x0 x0], [x1 ...], [x2 ...], [x3 ...].
-__device__ __forceinline__ void broadcast4(uint32_t x, uint32_t (&out)[4]) {
-  const auto h = __builtin_amdgcn_permlane32_swap(x, x, false, false);
-  const auto lo = __builtin_amdgcn_permlane16_swap(h[0], h[0], false, false);
-  const auto hi = __builtin_amdgcn_permlane16_swap(h[1], h[1], false, false);
-  out[0] = lo[0], out[1] = lo[1], out[2] = hi[0], out[3] = hi[1];
 }
 
 typedef __attribute__((address_space(3))) void lds_void_t;
