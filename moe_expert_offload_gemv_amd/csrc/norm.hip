@@ -121,16 +121,19 @@ __device__ __forceinline__ void put_out8(const NormArgs& a, int64_t row, int64_t
 
 // One work-group per row, rows in turn. NV > 0: the row's sums stay in NV
 // chunks of 8 registers per thread; NV = 0: any length, read twice (the sums
-// are formed again, so the residual may be updated in place). 16 waves with a row in
-// registers: two work-groups a CU, at the price of a few spilled scalars (4096 x 8192
-// bf16: 59 us, one work-group 64; fp32 101 and 106).
+// are formed again, so the residual may be updated in place).
 template <int XT, int RT, int THREADS, int NV>
-__global__ __launch_bounds__(THREADS, THREADS == 1024 && NV > 0 ? 8 : 1) void add_rmsnorm_kernel(NormArgs a) {
+__global__ __launch_bounds__(THREADS) void add_rmsnorm_kernel(NormArgs a) {
   constexpr int W = THREADS / 64;
   __shared__ float s_sum[2][W], s_again[W];
   const float least = a.eps < kSmallMean ? kSmallMean * (float)a.H : 0.f;
   int turn = 0;
   for (int64_t row = blockIdx.x; row < a.T; row += gridDim.x, turn ^= 1) {
+    // Offsets within the row are formed anew for each: kept from row to row they would take more
+    // than 64 registers with the values, and a CU then holds one work-group of 16 waves, not two
+    // (4096 x 8192 bf16: 64 us, so 59.5; without residual, fp32 to bf16, 51 and 42).
+    uint32_t tid = threadIdx.x;
+    __asm__ volatile("" : "+v"(tid));
     const char* x = static_cast<const char*>(a.x) + row * a.x_stride * value_size<XT>();
     const char* res = nullptr;
     char* res_out = nullptr;
@@ -143,7 +146,7 @@ __global__ __launch_bounds__(THREADS, THREADS == 1024 && NV > 0 ? 8 : 1) void ad
     if constexpr (NV > 0) {
 #pragma unroll
       for (int c = 0; c < NV; ++c) {
-        const int64_t i = 8 * ((int64_t)c * THREADS + threadIdx.x);
+        const int64_t i = 8 * ((int64_t)c * THREADS + tid);
         if (i < a.H) {
           sum8<XT, RT>(x, res, i, a.H, s[c]);
         } else {
@@ -156,7 +159,7 @@ __global__ __launch_bounds__(THREADS, THREADS == 1024 && NV > 0 ? 8 : 1) void ad
 #pragma unroll
         for (int j = 0; j < 8; ++j) ss = fmaf(s[c][j], s[c][j], ss);
     } else {
-      for (int64_t i = 8 * (int64_t)threadIdx.x; i < a.H; i += 8 * THREADS) {
+      for (int64_t i = 8 * (int64_t)tid; i < a.H; i += 8 * THREADS) {
         sum8<XT, RT>(x, res, i, a.H, s[0]);
 #pragma unroll
         for (int j = 0; j < 8; ++j) ss = fmaf(s[0][j], s[0][j], ss);
@@ -186,7 +189,7 @@ __global__ __launch_bounds__(THREADS, THREADS == 1024 && NV > 0 ? 8 : 1) void ad
 #pragma unroll
           for (int j = 0; j < 8; ++j) add(s[c][j]);
       } else {
-        for (int64_t i = 8 * (int64_t)threadIdx.x; i < a.H; i += 8 * THREADS) {
+        for (int64_t i = 8 * (int64_t)tid; i < a.H; i += 8 * THREADS) {
           sum8<XT, RT>(x, res, i, a.H, s[0]);
 #pragma unroll
           for (int j = 0; j < 8; ++j) add(s[0][j]);
@@ -207,14 +210,14 @@ __global__ __launch_bounds__(THREADS, THREADS == 1024 && NV > 0 ? 8 : 1) void ad
     if constexpr (NV > 0) {
 #pragma unroll
       for (int c = 0; c < NV; ++c) {
-        const int64_t i = 8 * ((int64_t)c * THREADS + threadIdx.x);
+        const int64_t i = 8 * ((int64_t)c * THREADS + tid);
         if (i < a.H) {
           if constexpr (RT != kNoResidual) put8<RT>(res_out, i, a.H, s[c]);
           put_out8(a, row, i, s[c], r, half);
         }
       }
     } else {
-      for (int64_t i = 8 * (int64_t)threadIdx.x; i < a.H; i += 8 * THREADS) {
+      for (int64_t i = 8 * (int64_t)tid; i < a.H; i += 8 * THREADS) {
         sum8<XT, RT>(x, res, i, a.H, s[0]);
         if constexpr (RT != kNoResidual) put8<RT>(res_out, i, a.H, s[0]);
         put_out8(a, row, i, s[0], r, half);
