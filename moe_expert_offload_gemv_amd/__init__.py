@@ -469,14 +469,20 @@ def moe_q4_workspace_bytes(n_tokens: int, n_out: int, k: int, x_type: int) -> in
 
 def moe_q4_workspace(x, nibbles):
     """A workspace tensor for moe_q4_matmul of x with these weights (None if it needs none)."""
-    import torch
-
-    _dense()
+    L = _dense()
     T, K = _dims("x", x, 2)
-    n = moe_q4_workspace_bytes(T, _dims("nibbles", nibbles, 3)[0], K, _types.get(x.dtype, -1))
+    N = _dims("nibbles", nibbles, 3)[0]
+    return _q4_workspace(x, nibbles, L.moe_q4_workspace_bytes(T, N, K, _types.get(x.dtype, -1)))
+
+
+def _q4_workspace(x, nibbles, n):
     if n < 0:
         raise ValueError(f"no product of x {x.dtype} {tuple(x.shape)} with weights {tuple(nibbles.shape)}")
-    return torch.empty(n, dtype=torch.uint8, device=x.device) if n else None
+    if n:
+        import torch
+
+        return torch.empty(n, dtype=torch.uint8, device=x.device)
+    return None
 
 
 def moe_q4_matmul(x, nibbles, w_scales, y, scales=None, workspace=None, flags: int = 0, stream=None) -> None:
@@ -498,7 +504,8 @@ def moe_q4_matmul(x, nibbles, w_scales, y, scales=None, workspace=None, flags: i
         st, sp, ss = _rows("scales", scales, dev, (T, K // 32))
         if st != MOE_F32:
             raise ValueError(f"scales: {scales.dtype}")
-    workspace, kp, kn = _workspace(workspace, dev, stream, lambda: moe_q4_workspace(x, nibbles))
+    workspace, kp, kn = _workspace(workspace, dev, stream,
+                                   lambda: _q4_workspace(x, nibbles, L.moe_q4_workspace_bytes(T, N, K, xt)))
     rc = L.moe_q4_matmul(dev, _stream_of(stream, dev), T, N, K, xt, xp, xs, sp, ss, np_, wp, yt, yp, ys, kp, kn,
                          _number("flags", flags))
     if rc:
