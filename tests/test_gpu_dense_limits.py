@@ -325,3 +325,67 @@ def test_router_balance_workspace_of_the_binding_on_a_side_stream():
     b.check()
     b.backward(d)
     assert torch.equal(counts, b.counts) and torch.equal(stats, b.stats) and torch.equal(got, d)
+
+
+# ---------------------------------------------------------------------------
+# offsets past 32 bits
+
+
+def far_rows(a, dtype, stride):
+    """a [T][n] as rows `stride` values apart, in memory that is otherwise as it comes."""
+    T, n = a.shape
+    v = torch.empty(T * stride, dtype=dtype, device="cuda").view(T, stride)[:, :n]
+    v.copy_(a)
+    return v
+
+
+@pytest.fixture
+def big_memory():
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < 100 << 30:
+        pytest.skip("100 GB of free device memory are needed")
+    yield
+    torch.cuda.empty_cache()
+
+
+def test_rows_further_apart_than_32_bits(big_memory):
+    T, stride = 37, (1 << 27) + 24  # 4.9e9 values
+    g = rng_of(44)
+    near = torch.from_numpy(g.standard_normal((T, 96))).to(torch.bfloat16).cuda()
+    x, r = far_rows(near, torch.bfloat16, stride), near.clone()
+    out, want, res = far_rows(torch.zeros_like(near), torch.bfloat16, stride), torch.zeros_like(near), near.clone()
+    moe.moe_add_rmsnorm(near, None, want, residual=r)
+    moe.moe_add_rmsnorm(x, None, out, residual=res)
+    assert torch.equal(out, want) and torch.equal(res, r)
+    del out
+    for n in (1, 2, 37):  # dots, tiles
+        p = Product(n, 70, 96, "bf16", seed=8)
+        y = [torch.zeros((n, 70), dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+        moe.moe_q4_matmul(near[:n], p.nib, p.scl, y[0])
+        moe.moe_q4_matmul(x[:n], p.nib, p.scl, y[1])
+        assert torch.equal(*y)
+        y[1] = far_rows(torch.zeros_like(y[0]), torch.bfloat16, stride)
+        moe.moe_q4_matmul(near[:n], p.nib, p.scl, y[1])
+        assert torch.equal(*y)
+    b, far = Balance(near, 6), Balance(near, 6)
+    far.z = x
+    d, dfar = torch.zeros_like(near), far_rows(torch.zeros_like(near), torch.bfloat16, stride)
+    b.forward(), far.forward()
+    b.backward(d), far.backward(dfar)
+    assert torch.equal(b.counts, far.counts) and torch.equal(b.stats, far.stats) and torch.equal(b.lse, far.lse)
+    assert torch.equal(d, dfar)
+
+
+@pytest.mark.parametrize("T", [1, 20, 40])
+def test_weights_of_more_than_2_31_blocks(T, big_memory):
+    N, K = 1 << 22, 16416  # the most features, 513 blocks each: dots of rows split over waves, tiles, whole tiles
+    p = Product(T, 64, K, "bf16", seed=9)
+    nib = torch.empty((N, K // 32, 16), dtype=torch.uint8, device="cuda")
+    scl = torch.zeros((N, K // 32), dtype=torch.float16, device="cuda")
+    y = torch.full((T, N), 3.0, device="cuda")
+    at = torch.tensor([i + j for i in (0, 40, (1 << 31) // 513 - 8, N - 16) for j in range(16)], device="cuda")
+    nib[at], scl[at] = p.nib, p.scl
+    moe.moe_q4_matmul(p.x, nib, scl, y)
+    p.check(y[:, at], torch.float32)
+    y[:, at] = 0
+    assert (y == 0).all()  # every other feature's scales are zero
