@@ -470,8 +470,9 @@ MOE_API const char* moe_last_error(moe_ctx* ctx);
  *    call may be captured into a HIP graph. Results depend on the inputs only
  *    (no atomics on values): equal calls give equal bits.
  *  - Rows may be strided: *_stride is the distance of two rows in values, at
- *    least the row length. Values of a row are contiguous and aligned to their
- *    size. What lies between and behind the rows is neither read nor written.
+ *    least the row length and at most 2^36. Values of a row are contiguous and
+ *    aligned to their size. What lies between and behind the rows is neither
+ *    read nor written.
  *  - Outputs may not overlap inputs or each other unless said so.
  *  - n_tokens is 0..2^24 (0: nothing is written but what a call says).
  *  - MOE_E_INVAL on a bad size, type, stride, null pointer, alignment or too
@@ -509,7 +510,7 @@ MOE_API int moe_q4_split(int32_t rows, int32_t k, const void* blocks, void* nibb
  * nibbles and w_scales are the planes of moe_q4_split in device memory,
  * contiguous, 16-byte aligned. x_type MOE_F32, MOE_F16, MOE_BF16, or MOE_Q8_32
  * with x_scales fp32 [n_tokens][k/32] (x = scale * code); y_type MOE_F32,
- * MOE_F16 or MOE_BF16. n_out >= 1, k a multiple of 32, 32..2^20.
+ * MOE_F16 or MOE_BF16. n_out is 1..2^22, k a multiple of 32, 32..2^20.
  * Weights and activations enter the products unrounded (8-bit codes as whole
  * numbers, their scales times the sums of a block); sums are fp32; y is rounded
  * once. |x| up to 2^115, and bits of an fp32 x below 2^-133 may be cut off (values
@@ -538,7 +539,9 @@ MOE_API int64_t moe_q4_workspace_bytes(int32_t n_tokens, int32_t n_out, int32_t 
  *              its tokens: 1 for every expert if balanced
  *   stats    = {balance + z term, balance term, z term, n} with
  *              balance term = balance_coef * sum_e load[e] * mean_t p[t][e]
- *              z term       = z_coef * mean_t lse[t]^2
+ *              z term       = z_coef * mean_t lse[t]^2 (the sum of squares in fp32:
+ *              infinite past 2^128, as for rows of fp32's lowest value alone; 0 if
+ *              z_coef is 0)
  * Tokens with valid[t] == 0 (uint8; NULL: none) and tokens whose logits are all
  * -inf are left out of every sum: their lse is -inf. With n = 0 the loads and
  * losses are 0. A NaN or +inf logit makes the losses NaN; among the picks a NaN

@@ -18,8 +18,9 @@
 //
 // Measured (kernels alone): 32768 x 512 fp32, 8 picks: rows 23-26 us for 67 MB (bound by
 // instructions, 1150 for four rows of a wave: 16 us of them, two waves a SIMD), finishing 5.5, gradient 27.5 for
-// 134 MB = 4.9 TB/s, the rate of a copy. 12288 x 256 bf16: 10.6, 5 and 7.5 us; 999 x 60 fp16:
-// 3.9, 5 and 3.2 us, each a launch and a few dependent trips to memory.
+// 134 MB = 4.9 TB/s, the rate of a copy. 12288 x 256 bf16: 10.7 (3 of them instructions: 768 units of
+// 16 rows leave half of the 512 work-groups idle in their second round), 5 and 7.5 us; 999 x 60
+// fp16: 3.9, 5 and 3.2 us, each a launch and a few dependent trips to memory.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 

@@ -14,7 +14,7 @@
 //                   1536 fp32, 7.4 us; 201 x 1001 x 1056 fp16, 7.3: rounds of load, convert, barrier and
 //                   product, 1 us each).
 //   q4_wide_kernel  more: the activations are brought into operand form once, 64 x 64 tiles
-//                   per wave (4096 x 5120 x 4096 bf16, 172 GFLOP, 267-286 us = 0.62 PFLOP/s, 17 of them the
+//                   per wave (4096 x 5120 x 4096 bf16, 172 GFLOP, 264-300 us = 0.6 PFLOP/s, 17 of them the
 //                   operand pass; the library's plain bf16 product of the same sizes would take 153). Per step of
 //                   four blocks a wave issues 64 products and 460 vector instructions, 256 of them the scale
 //                   FMAs that keep the weights exact; the two do not overlap on a SIMD

@@ -14,9 +14,9 @@
 // of squares is not finite, or whose mean is too small to have kept them all, is summed again
 // scaled by a power of two.
 //
-// Measured (kernel alone): 12287 x 4096, fp32 x, bf16 residual and out, 504 MB, 92-95 us =
-// 5.4 TB/s, the rate of a streaming read (a copy: 4.95); 4096 x 2048 bf16 to codes, 60 MB,
-// 12.4 us = 4.8 TB/s; one row of 2048 values 2.5 us, a launch and two trips to memory.
+// Measured (kernel alone): 12287 x 4096, fp32 x, bf16 residual and out, 504 MB, 89-91 us =
+// 5.6 TB/s, above a streaming read (5.35) and a copy (4.95); 4096 x 2048 bf16 to codes, 60 MB,
+// 12.5-13.1 us = 4.7 TB/s; one row of 2048 values 2.4-2.9 us, a launch and two trips to memory.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
