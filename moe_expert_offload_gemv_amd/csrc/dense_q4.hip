@@ -905,8 +905,9 @@ struct Turn {
   }
 };
 
+// two work-groups a CU, but for split fp32 tiles, whose stages of three terms leave room for one
 template <int XT, int SB, int WK, int RING>
-__global__ __launch_bounds__(256, 2) void q4_wide_kernel(Q4Args a, Operand o, int row_tiles, int col_tiles) {
+__global__ __launch_bounds__(256, WK > 1 && terms_of<XT>() == 3 ? 1 : 2) void q4_wide_kernel(Q4Args a, Operand o, int row_tiles, int col_tiles) {
   constexpr int TERMS = terms_of<XT>(), SIDE = wide_side(WK), MG = SIDE / 16;  // row tiles of 16 in the stages
   constexpr int RUNS = runs_of<XT>(), kBlockBase = 64 * RUNS;
   constexpr int kTermBytes = MG * SB * TERMS * 1024, kBaseBytes = MG * SB * kBlockBase, kStage = kTermBytes + kBaseBytes;
