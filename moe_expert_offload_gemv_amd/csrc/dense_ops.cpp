@@ -42,7 +42,6 @@ int device_ok(int32_t device, const char* what) {
 
 int launched(hipError_t e, const char* what) {
   if (e == hipSuccess) return MOE_OK;
-  (void)hipGetLastError();
   return moe_thread_fail(MOE_E_HIP, "%s: launch failed: %s", what, hipGetErrorString(e));
 }
 

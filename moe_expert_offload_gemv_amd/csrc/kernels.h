@@ -106,11 +106,12 @@ hipError_t launch_route(const RouteArgs& a, const Launch& l);
 
 // Launch on l.stream; timed by the dispatch itself when l carries events. The
 // status is this launch's own: hipGetLastError would also tell of an error that
-// some other call left with the thread, though the kernel runs.
+// some other call left with the thread, though the kernel runs. A failure is
+// reported here alone and not left with the thread for the caller's next check.
 template <typename... Args, typename... P>
 inline hipError_t launch(void (*kern)(Args...), dim3 grid, dim3 block, const Launch& l, P... params) {
   std::tuple<Args...> values(params...);
-  return std::apply(
+  const hipError_t e = std::apply(
       [&](Args&... v) {
         void* args[] = {const_cast<void*>(static_cast<const void*>(&v))...};
         const void* f = reinterpret_cast<const void*>(kern);
@@ -118,6 +119,8 @@ inline hipError_t launch(void (*kern)(Args...), dim3 grid, dim3 block, const Lau
                        : hipLaunchKernel(f, grid, block, args, l.lds, l.stream);
       },
       values);
+  if (e != hipSuccess) (void)hipGetLastError();
+  return e;
 }
 
 struct GemvArgs {
