@@ -529,6 +529,132 @@ MOE_API int moe_q4_matmul(int32_t device, void* stream, int32_t n_tokens, int32_
 /* Bytes of its workspace, -1 on a bad size or type. */
 MOE_API int64_t moe_q4_workspace_bytes(int32_t n_tokens, int32_t n_out, int32_t k, int32_t x_type);
 
+/* The same product with what follows it in one pass:
+ *   y[t][n] = act(sum_k W[n][k] x[t][k] + bias[n]) * mul[t][n] + residual[t][n]
+ * with the product as moe_q4_matmul's (types, limits, forms and workspace too) and
+ * the rest in fp32 on the unrounded sum; y is rounded once. act:
+ *   MOE_ACT_NONE        v
+ *   MOE_ACT_RELU        max(v, 0)
+ *   MOE_ACT_SILU        v / (1 + e^-v)
+ *   MOE_ACT_GELU        v / 2 * (1 + erf(v / sqrt 2))
+ *   MOE_ACT_GELU_TANH   v / 2 * (1 + tanh(sqrt(2 / pi) * (v + 0.044715 v^3)))
+ * bias fp32 [n_out], mul and residual [n_tokens][n_out] of MOE_F32, MOE_F16 or
+ * MOE_BF16, each NULL if left out (its type and stride are then not looked at). A
+ * SwiGLU expert is three calls: up; gate with MOE_ACT_SILU and mul = up; down with
+ * residual = the stream. y may be mul or residual (in place) when type and stride
+ * are the same. */
+enum {
+  MOE_ACT_NONE = 0,
+  MOE_ACT_RELU = 1,
+  MOE_ACT_SILU = 2,
+  MOE_ACT_GELU = 3,
+  MOE_ACT_GELU_TANH = 4
+};
+MOE_API int moe_q4_linear(int32_t device, void* stream, int32_t n_tokens, int32_t n_out, int32_t k,
+                          int32_t x_type, const void* x, int64_t x_stride, const float* x_scales,
+                          int64_t x_scales_stride, const void* nibbles, const void* w_scales,
+                          const float* bias, int32_t act, int32_t mul_type, const void* mul, int64_t mul_stride,
+                          int32_t res_type, const void* residual, int64_t res_stride,
+                          int32_t y_type, void* y, int64_t y_stride, void* workspace, int64_t workspace_bytes);
+
+/* RMS norm of every query and key head and the rotation by its position, the step
+ * between the query/key/value product and attention. For each token t and head:
+ *   v = x * weight / sqrt(mean(x^2) + eps)     over the head_dim values of the head
+ *   (v_a, v_b) -> (v_a cos w - v_b sin w, v_b cos w + v_a sin w),
+ *       w = positions[axis(i)][t] * inv_freq[i],  for the pairs i < rotary_dim / 2
+ * Pair i is values i and i + rotary_dim / 2 of the head, or with MOE_ROPE_PAIRS
+ * 2i and 2i + 1; values from rotary_dim on are not turned. Positions may be of
+ * several axes (n_axes 1..8: time, height, width of a video, say): axis(i) =
+ * pair_axis[i] (uint8 [rotary_dim / 2] on the device, NULL: 0 for all; a pair whose
+ * axis is n_axes or more is not turned). positions int32 [n_axes][n_tokens], rows
+ * pos_stride apart, any sign; inv_freq fp32 [rotary_dim / 2]. The angle is formed
+ * in 64 bits, so it is exact for every position. rotary_dim is even, 0..head_dim;
+ * 0: the norm alone, with inv_freq and positions NULL. MOE_NO_NORM: the rotation
+ * alone, with both weights NULL.
+ * A tensor of heads [n_tokens][heads][head_dim] has its values contiguous, tokens
+ * *_stride and heads *_head_stride values apart, the heads of a token after each
+ * other (*_head_stride >= head_dim, *_stride past the last of them) or the tokens of
+ * a head (the other way round); neither above 2^36. head_dim is even, 2..512,
+ * q_heads 1..1024, k_heads 0..1024 (0: k, k_out and k_weight are not looked at).
+ * q_weight and k_weight fp32 [head_dim], NULL: ones. x_type and out_type MOE_F32,
+ * MOE_F16 or MOE_BF16. All in fp32, rounded once. q_out may be q, and k_out k, when
+ * type and strides are the same. Any finite head has its norm, however large or
+ * small its squares; one of zeros with eps = 0 gives NaN.
+ * flags: MOE_ROPE_PAIRS, MOE_NO_NORM. */
+#define MOE_ROPE_PAIRS 2u
+#define MOE_NO_NORM 4u
+MOE_API int moe_qk_norm_rope(int32_t device, void* stream, int32_t n_tokens, int32_t q_heads, int32_t k_heads,
+                             int32_t head_dim, int32_t x_type, const void* q, int64_t q_stride, int64_t q_head_stride,
+                             const void* k, int64_t k_stride, int64_t k_head_stride,
+                             const float* q_weight, const float* k_weight, float eps,
+                             int32_t rotary_dim, const float* inv_freq, const int32_t* positions, int64_t pos_stride,
+                             int32_t n_axes, const uint8_t* pair_axis,
+                             int32_t out_type, void* q_out, int64_t q_out_stride, int64_t q_out_head_stride,
+                             void* k_out, int64_t k_out_stride, int64_t k_out_head_stride, uint32_t flags);
+
+/* Its gradient: gq and gk (g_type) are the gradients of q_out and k_out; q, k and the
+ * rest are those of the call. dq and dk (d_type) are the gradients of q and k,
+ * dq_weight and dk_weight (fp32 [head_dim], NULL: not asked for) those of the
+ * weights, sums over tokens and heads (with MOE_ACCUMULATE added to what is there; 0 for
+ * no tokens). A weight left out counts as ones and may have its gradient all the same.
+ * dq may be gq or q, and dk gk or k, when type and strides are the same. With
+ * MOE_NO_NORM q and k are not looked at and may be NULL, and so have to be
+ * dq_weight and dk_weight. workspace:
+ * moe_qk_norm_rope_grad_workspace_bytes bytes of device memory, 256-byte aligned,
+ * as moe_q4_matmul's; not needed (NULL) without dq_weight and dk_weight.
+ * flags: those of the call, MOE_ACCUMULATE. */
+MOE_API int moe_qk_norm_rope_grad(int32_t device, void* stream, int32_t n_tokens, int32_t q_heads, int32_t k_heads,
+                             int32_t head_dim, int32_t x_type, const void* q, int64_t q_stride, int64_t q_head_stride,
+                             const void* k, int64_t k_stride, int64_t k_head_stride,
+                             const float* q_weight, const float* k_weight, float eps,
+                             int32_t rotary_dim, const float* inv_freq, const int32_t* positions, int64_t pos_stride,
+                             int32_t n_axes, const uint8_t* pair_axis,
+                             int32_t g_type, const void* gq, int64_t gq_stride, int64_t gq_head_stride,
+                             const void* gk, int64_t gk_stride, int64_t gk_head_stride,
+                             int32_t d_type, void* dq, int64_t dq_stride, int64_t dq_head_stride,
+                             void* dk, int64_t dk_stride, int64_t dk_head_stride,
+                             float* dq_weight, float* dk_weight, void* workspace, int64_t workspace_bytes, uint32_t flags);
+MOE_API int64_t moe_qk_norm_rope_grad_workspace_bytes(int32_t n_tokens, int32_t q_heads, int32_t k_heads, int32_t head_dim);
+
+/* What the output head says of each token. For logits [n_tokens][n_vocab] (MOE_F32,
+ * MOE_F16 or MOE_BF16), z = scale * logits (an inverse temperature, > 0 and finite):
+ *   p[t] = softmax(z[t]), lse[t] = log sum exp(z[t])
+ *   logp[t]    = log p[t][targets[t]]     (0 where the target is not in 0..n_vocab-1)
+ *   entropy[t] = -sum_j p[t][j] log p[t][j]
+ *   top_ids[t], top_logp[t] = the top_n largest logits above -inf, in descending
+ *                order, ties to the lower id, and their log p; where there are
+ *                fewer, ids -1 and log p -inf
+ * all in one read of the logits. lse is fp32 [n_tokens][2], a value and what its
+ * rounding left out, for the gradient. Logits of -inf (words that a grammar leaves
+ * out) have p = 0; a row of nothing else has lse and logp -inf, entropy 0 and no
+ * top ids, and so has a row whose z are all below fp32's range. A row with a NaN or
+ * +inf (z past fp32's range) has NaN for all of them, and ids -1.
+ * targets int32 [n_tokens] and logp fp32 [n_tokens] go together; entropy fp32
+ * [n_tokens], lse: each NULL if not asked for. top_n is 0..min(n_vocab, 32); top_ids
+ * int32 and top_logp fp32 [n_tokens][top_n] are NULL with 0. n_vocab is 1..2^22.
+ * workspace: moe_token_logprobs_workspace_bytes bytes of device memory, 256-byte
+ * aligned, as moe_q4_matmul's. */
+MOE_API int moe_token_logprobs(int32_t device, void* stream, int32_t n_tokens, int32_t n_vocab, int32_t z_type,
+                               const void* logits, int64_t z_stride, const int32_t* targets, float scale, float* logp,
+                               float* entropy, float* lse, int32_t top_n, int32_t* top_ids, float* top_logp,
+                               void* workspace, int64_t workspace_bytes);
+MOE_API int64_t moe_token_logprobs_workspace_bytes(int32_t n_tokens, int32_t n_vocab, int32_t top_n);
+
+/* Gradient of sum_t dlogp[t] logp[t] + dentropy[t] entropy[t] to the logits:
+ *   dlogits[t][j] (=|+=) scale * (dlogp[t] * ((j == targets[t]) - p[t][j])
+ *                                 - dentropy[t] * p[t][j] * (log p[t][j] + entropy[t]))
+ * A cross entropy's is dlogp = -1 / n. logits, targets, scale, lse and entropy are
+ * those of the moe_token_logprobs call; dlogp fp32 [n_tokens] needs targets,
+ * dentropy fp32 [n_tokens] needs entropy, each NULL if left out (not both). A token whose
+ * target is not in 0..n_vocab-1 has no part of dlogp; one with nothing of either (0),
+ * or with lse -inf, has gradient 0, whatever its logits. d_type is MOE_F32,
+ * MOE_F16 or MOE_BF16; dlogits may be logits when type and stride are the same (not
+ * with MOE_ACCUMULATE). flags: MOE_ACCUMULATE or 0. */
+MOE_API int moe_token_logprobs_grad(int32_t device, void* stream, int32_t n_tokens, int32_t n_vocab, int32_t z_type,
+                                    const void* logits, int64_t z_stride, const int32_t* targets, float scale,
+                                    const float* lse, const float* entropy, const float* dlogp, const float* dentropy,
+                                    int32_t d_type, void* dlogits, int64_t d_stride, uint32_t flags);
+
 /* The router's load over a batch of tokens, and its losses. For logits
  * [n_tokens][n_experts] (MOE_F32, MOE_F16 or MOE_BF16):
  *   p[t] = softmax(logits[t]), lse[t] = log sum exp(logits[t])

@@ -26,6 +26,13 @@ MOE_E_CAPTURING = -5
 MOE_E_RANGE = -6
 MOE_Q4_32_F16 = 1
 MOE_ACCUMULATE = 1
+MOE_ROPE_PAIRS = 2
+MOE_NO_NORM = 4
+MOE_ACT_NONE = 0
+MOE_ACT_RELU = 1
+MOE_ACT_SILU = 2
+MOE_ACT_GELU = 3
+MOE_ACT_GELU_TANH = 4
 MOE_F32 = 0
 MOE_F16 = 1
 MOE_BF16 = 2
@@ -46,6 +53,8 @@ EXPORTED = [
     "moe_forward_static_scratch",
     "moe_add_rmsnorm", "moe_q4_split", "moe_q4_matmul", "moe_q4_workspace_bytes", "moe_router_balance",
     "moe_router_balance_workspace_bytes", "moe_router_balance_grad",
+    "moe_q4_linear", "moe_qk_norm_rope", "moe_qk_norm_rope_grad", "moe_qk_norm_rope_grad_workspace_bytes",
+    "moe_token_logprobs", "moe_token_logprobs_workspace_bytes", "moe_token_logprobs_grad",
 ]
 
 
@@ -140,6 +149,18 @@ def lib():
             "moe_router_balance_workspace_bytes": (i64, [i32, i32]),
             "moe_router_balance_grad": (C.c_int, [i32, vp, i32, i32, i32, vp, i64, vp, vp, vp, vp, f32, f32, i32, vp,
                                                   i64, u32]),
+            "moe_q4_linear": (C.c_int, [i32, vp, i32, i32, i32, i32, vp, i64, vp, i64, vp, vp, vp, i32, i32, vp, i64, i32,
+                                        vp, i64, i32, vp, i64, vp, i64]),
+            "moe_qk_norm_rope": (C.c_int, [i32, vp, i32, i32, i32, i32, i32, vp, i64, i64, vp, i64, i64, vp, vp, f32, i32, vp,
+                                           vp, i64, i32, vp, i32, vp, i64, i64, vp, i64, i64, u32]),
+            "moe_qk_norm_rope_grad": (C.c_int, [i32, vp, i32, i32, i32, i32, i32, vp, i64, i64, vp, i64, i64, vp, vp, f32, i32,
+                                                vp, vp, i64, i32, vp, i32, vp, i64, i64, vp, i64, i64, i32, vp, i64, i64, vp,
+                                                i64, i64, vp, vp, vp, i64, u32]),
+            "moe_qk_norm_rope_grad_workspace_bytes": (i64, [i32, i32, i32, i32]),
+            "moe_token_logprobs": (C.c_int, [i32, vp, i32, i32, i32, vp, i64, vp, f32, vp, vp, vp, i32, vp, vp, vp, i64]),
+            "moe_token_logprobs_workspace_bytes": (i64, [i32, i32, i32]),
+            "moe_token_logprobs_grad": (C.c_int, [i32, vp, i32, i32, i32, vp, i64, vp, f32, vp, vp, vp, vp, i32, vp, i64,
+                                                  u32]),
         }
         for name, (res, args) in sig.items():
             f = getattr(L, name)
@@ -508,6 +529,234 @@ def moe_q4_matmul(x, nibbles, w_scales, y, scales=None, workspace=None, flags: i
                                    lambda: _q4_workspace(x, nibbles, L.moe_q4_workspace_bytes(T, N, K, xt)))
     rc = L.moe_q4_matmul(dev, _stream_of(stream, dev), T, N, K, xt, xp, xs, sp, ss, np_, wp, yt, yp, ys, kp, kn,
                          _number("flags", flags))
+    if rc:
+        _fail(rc)
+
+
+def moe_q4_linear(x, nibbles, w_scales, y, bias=None, act: int = MOE_ACT_NONE, mul=None, residual=None, scales=None,
+                  workspace=None, stream=None) -> None:
+    """y = act(x W^T + bias) * mul + residual, each of the three left out if None (see moe_offload.h).
+
+    x, nibbles, w_scales, scales and workspace as in moe_q4_matmul (moe_q4_workspace serves both); bias fp32 [N];
+    mul and residual [T][N] fp32, fp16 or bf16, either of which may be y.
+    """
+    L = _dense()
+    shape, dev = _dims("x", x, 2), x.get_device()
+    T, K = shape
+    N = _dims("nibbles", nibbles, 3)[0]
+    xt, xp, xs = _rows("x", x, dev, shape)
+    np_ = _flat("nibbles", nibbles, dev, (N, K // 32, 16), "torch.uint8")
+    wp = _flat("w_scales", w_scales, dev, (N, K // 32), "torch.float16")
+    bp = _flat("bias", bias, dev, (N,), "torch.float32")
+    yt, yp, ys = _rows("y", y, dev, (T, N))
+    mt, mp, ms = (MOE_F32, None, 0) if mul is None else _rows("mul", mul, dev, (T, N))
+    rt, rp, rs = (MOE_F32, None, 0) if residual is None else _rows("residual", residual, dev, (T, N))
+    sp, ss = None, 0
+    if scales is not None:
+        st, sp, ss = _rows("scales", scales, dev, (T, K // 32))
+        if st != MOE_F32:
+            raise ValueError(f"scales: {scales.dtype}")
+    workspace, kp, kn = _workspace(workspace, dev, stream,
+                                   lambda: _q4_workspace(x, nibbles, L.moe_q4_workspace_bytes(T, N, K, xt)))
+    rc = L.moe_q4_linear(dev, _stream_of(stream, dev), T, N, K, xt, xp, xs, sp, ss, np_, wp, bp, _number("act", act), mt, mp,
+                         ms, rt, rp, rs, yt, yp, ys, kp, kn)
+    if rc:
+        _fail(rc)
+
+
+def _heads(name, t, dev, shape):
+    """(type code, address, stride of tokens, stride of heads) of a tensor [T][heads][head_dim]."""
+    if t.shape != shape or t.get_device() != dev or dev < 0 or t.dtype not in _types:
+        raise ValueError(f"{name}: {t.dtype} {tuple(t.shape)} on {t.device}; fp32, fp16 or bf16 of shape "
+                         f"{tuple(shape)} on cuda device {max(dev, 0)} is needed")
+    stride, head, step = t.stride()
+    T, H, D = shape
+    if step != 1:
+        raise ValueError(f"{name}: the values of a head must be contiguous, strides {t.stride()}")
+    # a stride that is never taken may be anything in torch
+    return _types[t.dtype], t.data_ptr(), stride if T > 1 else max(stride, D), head if H > 1 else D
+
+
+_NO_HEADS = (MOE_F32, None, 0, 0)
+
+
+def _rope(T, D, dev, inv_freq, positions, pair_axis):
+    """rotary_dim, inv_freq, positions, their stride, axes and pair_axis as the library takes them."""
+    if inv_freq is None:
+        if positions is not None or pair_axis is not None:
+            raise ValueError("positions: there is no inv_freq")
+        return 0, None, None, 0, 0, None
+    n = inv_freq.numel()
+    if 2 * n > D or n < 1:
+        raise ValueError(f"inv_freq: {n} frequencies for heads of {D}")
+    fp = _flat("inv_freq", inv_freq, dev, (n,), "torch.float32")
+    if positions is None or positions.dim() not in (1, 2):
+        raise ValueError("positions: an int32 tensor [tokens] or [axes][tokens] is needed")
+    axes = 1 if positions.dim() == 1 else positions.shape[0]
+    if (positions.shape[-1] != T or positions.get_device() != dev or positions.dtype is not _dtypes["torch.int32"]
+            or not 1 <= axes <= 8 or (positions.stride(-1) != 1 and T > 1)):
+        raise ValueError(f"positions: {positions.dtype} {tuple(positions.shape)} on {positions.device}; int32 [tokens] or "
+                         f"[axes][tokens], {T} tokens in a row, on cuda device {max(dev, 0)} is needed")
+    return (2 * n, fp, positions.data_ptr(), max(positions.stride(0), T) if axes > 1 else T, axes,
+            _flat("pair_axis", pair_axis, dev, (n,), "torch.uint8"))
+
+
+def moe_qk_norm_rope(q, k, q_out, k_out, q_weight=None, k_weight=None, eps=1e-6, inv_freq=None, positions=None,
+                     pair_axis=None, flags: int = 0, stream=None) -> None:
+    """q_out, k_out = RMS norm of each head of q and k times its weight, turned by its position (see moe_offload.h).
+
+    q [T][q_heads][D] and k [T][k_heads][D] (both k and k_out may be None) fp32, fp16 or bf16; q_out and k_out of those
+    shapes, of one type, q and k themselves if need be; weights fp32 [D] or None. inv_freq fp32 [rotary_dim / 2]; positions
+    int32 [T], or [axes][T] with pair_axis uint8 [rotary_dim / 2]. Without inv_freq the norm alone; flags: MOE_ROPE_PAIRS
+    (values 2i and 2i + 1 turn together), MOE_NO_NORM (the rotation alone).
+    """
+    L = _dense()
+    shape, dev = _dims("q", q, 3), q.get_device()
+    T, Hq, D = shape
+    R, fp, pp, ps, axes, ap = _rope(T, D, dev, inv_freq, positions, pair_axis)
+    xt, qp, qs, qh = _heads("q", q, dev, shape)
+    ot, qop, qos, qoh = _heads("q_out", q_out, dev, shape)
+    Hk, kp, ks, kh, kop, kos, koh = 0, None, 0, 0, None, 0, 0
+    if k is not None or k_out is not None:
+        if k is None or k_out is None:
+            raise ValueError("k and k_out go together")
+        Hk = _dims("k", k, 3)[1]
+        kt, kp, ks, kh = _heads("k", k, dev, (T, Hk, D))
+        kot, kop, kos, koh = _heads("k_out", k_out, dev, (T, Hk, D))
+        if kt != xt or kot != ot:
+            raise ValueError(f"k: {k.dtype} to {k_out.dtype}, but q: {q.dtype} to {q_out.dtype}")
+    qw = _flat("q_weight", q_weight, dev, (D,), "torch.float32")
+    kw = _flat("k_weight", k_weight, dev, (D,), "torch.float32")
+    rc = L.moe_qk_norm_rope(dev, _stream_of(stream, dev), T, Hq, Hk, _number("head_dim", D), xt, qp, qs, qh, kp, ks, kh, qw, kw,
+                            eps, R, fp, pp, ps, axes, ap, ot, qop, qos, qoh, kop, kos, koh, _number("flags", flags))
+    if rc:
+        _fail(rc)
+
+
+def moe_qk_norm_rope_grad_workspace_bytes(n_tokens: int, q_heads: int, k_heads: int, head_dim: int) -> int:
+    if not _fits(n_tokens, q_heads, k_heads, head_dim):
+        return -1
+    return int(lib().moe_qk_norm_rope_grad_workspace_bytes(n_tokens, q_heads, k_heads, head_dim))
+
+
+def moe_qk_norm_rope_workspace(q, k=None):
+    """A workspace tensor for moe_qk_norm_rope_grad of these heads (None if it needs none)."""
+    T, Hq, D = _dims("q", q, 3)
+    n = moe_qk_norm_rope_grad_workspace_bytes(T, Hq, 0 if k is None else _dims("k", k, 3)[1], D)
+    if n < 0:
+        raise ValueError(f"no norm of heads {tuple(q.shape)}")
+    if n:
+        import torch
+
+        return torch.empty(n, dtype=torch.uint8, device=q.device)
+    return None
+
+
+def moe_qk_norm_rope_grad(q, k, gq, gk, dq, dk, q_weight=None, k_weight=None, dq_weight=None, dk_weight=None, eps=1e-6,
+                          inv_freq=None, positions=None, pair_axis=None, workspace=None, flags: int = 0, stream=None) -> None:
+    """dq, dk = gradients of q and k, dq_weight, dk_weight (fp32 [D], None: not asked for) those of the weights, from gq and
+    gk, the gradients of moe_qk_norm_rope's outputs; the rest as in that call.
+
+    dq may be gq or q, and dk gk or k. MOE_ACCUMULATE adds to the weights' gradients. With MOE_NO_NORM the values of q
+    and k are not read. Without a workspace a call that needs one allocates it from torch.
+    """
+    L = _dense()
+    shape, dev = _dims("q", q, 3), q.get_device()
+    T, Hq, D = shape
+    R, fp, pp, ps, axes, ap = _rope(T, D, dev, inv_freq, positions, pair_axis)
+    xt, qp, qs, qh = _heads("q", q, dev, shape)
+    gt, gqp, gqs, gqh = _heads("gq", gq, dev, shape)
+    dt, dqp, dqs, dqh = _heads("dq", dq, dev, shape)
+    Hk, kp, ks, kh, gkp, gks, gkh, dkp, dks, dkh = 0, None, 0, 0, None, 0, 0, None, 0, 0
+    if k is not None or gk is not None or dk is not None:
+        if k is None or gk is None or dk is None:
+            raise ValueError("k, gk and dk go together")
+        Hk = _dims("k", k, 3)[1]
+        kt, kp, ks, kh = _heads("k", k, dev, (T, Hk, D))
+        gkt, gkp, gks, gkh = _heads("gk", gk, dev, (T, Hk, D))
+        dkt, dkp, dks, dkh = _heads("dk", dk, dev, (T, Hk, D))
+        if (kt, gkt, dkt) != (xt, gt, dt):
+            raise ValueError(f"k, gk, dk: {k.dtype}, {gk.dtype}, {dk.dtype}, but q, gq, dq: {q.dtype}, {gq.dtype}, {dq.dtype}")
+    elif dk_weight is not None:
+        raise ValueError("dk_weight: there is no k")
+    qw = _flat("q_weight", q_weight, dev, (D,), "torch.float32")
+    kw = _flat("k_weight", k_weight, dev, (D,), "torch.float32")
+    dqw = _flat("dq_weight", dq_weight, dev, (D,), "torch.float32")
+    dkw = _flat("dk_weight", dk_weight, dev, (D,), "torch.float32")
+    workspace, wp, wn = _workspace(workspace, dev, stream, lambda: moe_qk_norm_rope_workspace(q, k)) if (
+        workspace is not None or dqw or dkw) else (None, None, 0)
+    rc = L.moe_qk_norm_rope_grad(dev, _stream_of(stream, dev), T, Hq, Hk, _number("head_dim", D), xt, qp, qs, qh, kp, ks, kh, qw,
+                                 kw, eps, R, fp, pp, ps, axes, ap, gt, gqp, gqs, gqh, gkp, gks, gkh, dt, dqp, dqs, dqh, dkp,
+                                 dks, dkh, dqw, dkw, wp, wn, _number("flags", flags))
+    if rc:
+        _fail(rc)
+
+
+def moe_token_logprobs_workspace_bytes(n_tokens: int, n_vocab: int, top_n: int = 0) -> int:
+    if not _fits(n_tokens, n_vocab, top_n):
+        return -1
+    return int(lib().moe_token_logprobs_workspace_bytes(n_tokens, n_vocab, top_n))
+
+
+def moe_token_logprobs_workspace(logits, top_n: int = 0):
+    """A workspace tensor for moe_token_logprobs of these logits with top_n alternatives (None if it needs none)."""
+    n = moe_token_logprobs_workspace_bytes(*_dims("logits", logits, 2), top_n)
+    if n < 0:
+        raise ValueError(f"no log probabilities of logits {tuple(logits.shape)} with {top_n} alternatives")
+    if n:
+        import torch
+
+        return torch.empty(n, dtype=torch.uint8, device=logits.device)
+    return None
+
+
+def moe_token_logprobs(logits, targets=None, logp=None, entropy=None, lse=None, top_ids=None, top_logp=None, scale=1.0,
+                       workspace=None, stream=None) -> None:
+    """Of softmax(scale * logits), logits [T][V] fp32, fp16 or bf16: the log probability of targets (int32 [T]) into logp,
+    the entropy, the log of the sum of exponentials (lse, fp32 [T][2]), and the n most likely tokens of each row into top_ids
+    (int32 [T][n]) and top_logp (see moe_offload.h). What is None is not formed; logp, entropy and top_logp are fp32 [T], [T],
+    [T][n]. Without a workspace a call that needs one allocates it from torch.
+    """
+    L = _dense()
+    shape, dev = _dims("logits", logits, 2), logits.get_device()
+    T, V = shape
+    zt, zp, zs = _rows("logits", logits, dev, shape)
+    yp = _flat("targets", targets, dev, (T,), "torch.int32")
+    lp = _flat("logp", logp, dev, (T,), "torch.float32")
+    ep = _flat("entropy", entropy, dev, (T,), "torch.float32")
+    sp = _flat("lse", lse, dev, (T, 2), "torch.float32")
+    n, ip, tp = 0, None, None
+    if top_ids is not None or top_logp is not None:
+        if top_ids is None or top_logp is None:
+            raise ValueError("top_ids and top_logp go together")
+        n = _dims("top_ids", top_ids, 2)[1]
+        ip = _flat("top_ids", top_ids, dev, (T, n), "torch.int32")
+        tp = _flat("top_logp", top_logp, dev, (T, n), "torch.float32")
+        if n == 0:
+            ip = tp = None
+    workspace, kp, kn = _workspace(workspace, dev, stream, lambda: moe_token_logprobs_workspace(logits, n))
+    rc = L.moe_token_logprobs(dev, _stream_of(stream, dev), T, V, zt, zp, zs, yp, scale, lp, ep, sp, n, ip, tp, kp, kn)
+    if rc:
+        _fail(rc)
+
+
+def moe_token_logprobs_grad(logits, lse, dlogits, targets=None, dlogp=None, entropy=None, dentropy=None, scale=1.0,
+                            flags: int = 0, stream=None) -> None:
+    """dlogits [T][V] = gradient of sum(dlogp * logp) + sum(dentropy * entropy) to the logits, fp32 [T] each; logits, lse,
+    targets, entropy and scale are those of the moe_token_logprobs call (a cross entropy: dlogp = -1 / n).
+    """
+    L = _dense()
+    shape, dev = _dims("logits", logits, 2), logits.get_device()
+    T, V = shape
+    zt, zp, zs = _rows("logits", logits, dev, shape)
+    sp = _flat("lse", lse, dev, (T, 2), "torch.float32")
+    yp = _flat("targets", targets, dev, (T,), "torch.int32")
+    gp = _flat("dlogp", dlogp, dev, (T,), "torch.float32")
+    ep = _flat("entropy", entropy, dev, (T,), "torch.float32")
+    hp = _flat("dentropy", dentropy, dev, (T,), "torch.float32")
+    dt, dp, ds = _rows("dlogits", dlogits, dev, shape)
+    rc = L.moe_token_logprobs_grad(dev, _stream_of(stream, dev), T, V, zt, zp, zs, yp, scale, sp, ep, gp, hp, dt, dp, ds,
+                                   _number("flags", flags))
     if rc:
         _fail(rc)
 

@@ -18,7 +18,7 @@ OBJDIR = os.path.join(ROOT, "_build", "moe_offload")
 ARCH = os.environ.get("MOE_OFFLOAD_ARCH", "gfx950")
 
 SOURCES = ["route.hip", "decode.hip", "decode_layer.hip", "prefill_kernels.hip", "measure.hip", "step_copy.hip", "scratch.hip", "grouped_mfma.hip",
-           "norm.hip", "dense_q4.hip", "balance.hip",
+           "norm.hip", "dense_q4.hip", "dense_q4_linear.hip", "balance.hip", "heads.hip", "heads_grad.hip", "logprobs.hip",
            "runtime.cpp", "prefill.cpp", "dense_ops.cpp", "host_experts.cpp"]
 # plain C++ with no HIP in it (x86 vector code chosen at run time), built by the host compiler
 HOST_ONLY = {"host_experts.cpp"}
@@ -39,7 +39,7 @@ FLAGS = [
 # per-file code generation options: the grouped and dense MFMA kernels scale each MFMA
 # result in VALU right away, so their results go to VGPRs (the AGPR form
 # would add a v_accvgpr_read per result element)
-EXTRA_FLAGS = {f: ["-mllvm", "-amdgpu-mfma-vgpr-form"] for f in ("grouped_mfma.hip", "dense_q4.hip")}
+EXTRA_FLAGS = {f: ["-mllvm", "-amdgpu-mfma-vgpr-form"] for f in ("grouped_mfma.hip", "dense_q4.hip", "dense_q4_linear.hip")}
 
 
 def _compile(src: str) -> str:

@@ -308,7 +308,78 @@ struct NormArgs {
 };
 hipError_t launch_add_rmsnorm(const NormArgs& a, hipStream_t s);
 
-// dense_q4.hip
+// heads.hip, heads_grad.hip
+constexpr int kHeadRows = 4;  // rows per row group of a work-group, loaded at once
+struct HeadsPart {     // queries, or keys
+  const void* x;
+  const void* g;       // gradient of the output (moe_qk_norm_rope_grad)
+  void* out;
+  const float* weight; // nullptr: ones
+  float* dweight;      // nullptr: not asked for
+  float* sums;         // [blocks][D] the work-groups' shares of dweight
+  int64_t x_stride, x_head, g_stride, g_head, out_stride, out_head;
+  int32_t H, rows, blocks;  // heads; rows of a work-group, work-groups
+  uint32_t magic;           // of H, see quotient
+};
+struct HeadsArgs {
+  HeadsPart q, k;
+  const float* inv_freq;
+  const int32_t* pos;    // [axes][T]
+  const uint8_t* axis;   // [R / 2] or nullptr
+  int64_t T, pos_stride;
+  int32_t D, R, axes, x_type, g_type, out_type, pairs, norm, accumulate;
+  int32_t lanes, lanes_log;
+  uint32_t slot_magic;   // of D / 2
+  float eps;
+};
+struct HeadsShape {
+  int run, lanes_log;    // slots of a run, log2 of the lanes of a head
+};
+HeadsShape heads_shape(int D, int R, bool pairs);
+void heads_split(HeadsPart& p, const HeadsArgs& a, int max_rows, int64_t max_blocks);
+uint32_t heads_lds(const HeadsArgs& a);  // bytes of a work-group's angles
+hipError_t launch_heads(HeadsArgs a, hipStream_t s);
+int64_t heads_grad_workspace_bytes(int64_t T, int32_t Hq, int32_t Hk, int32_t D);
+hipError_t launch_heads_grad(HeadsArgs a, uint8_t* ws, hipStream_t s);
+
+// logprobs.hip
+constexpr int kMaxTop = 32;
+struct LogprobArgs {
+  const void* logits;
+  const int32_t* targets;  // nullptr: none
+  float *logp, *entropy, *lse;  // [T], [T], [T][2]; nullptr: not asked for
+  int32_t* top_ids;        // [T][top_n]
+  float* top_logp;
+  uint8_t* ws;
+  int64_t z_stride, T, V;
+  int32_t z_type, top_n;
+  float scale;
+  // of the launch: slices of a row, values of a slice, iterations of a noted maximum
+  int32_t slices, per_note;
+  int64_t slice;
+  float *sums, *slice_values;  // [T][slices][4], [T][slices][top_n]
+  int32_t* slice_ids;
+};
+int64_t logprob_workspace_bytes(int64_t T, int64_t V, int top_n);
+hipError_t launch_logprobs(const LogprobArgs& a, hipStream_t s);
+struct LogprobGradArgs {
+  const void* logits;
+  const int32_t* targets;
+  const float *lse, *entropy, *dlogp, *dentropy;
+  void* dlogits;
+  int64_t z_stride, d_stride, T, V;
+  int32_t z_type, d_type, accumulate;
+  float scale;
+};
+hipError_t launch_logprobs_grad(const LogprobGradArgs& a, hipStream_t s);
+
+// dense_q4.hip, dense_q4_linear.hip
+struct Q4Epilogue {           // y = act(product + bias) * mul + res; nullptr: left out
+  const float* bias;          // [N]
+  const void *mul, *res;
+  int64_t mul_stride, res_stride;
+  int32_t mul_type, res_type, act;
+};
 struct Q4Args {
   const void* x;
   const float* x_scales;      // 8-bit x
@@ -319,9 +390,11 @@ struct Q4Args {
   int64_t x_stride, x_scales_stride, y_stride;
   int64_t T, N, K;
   int32_t x_type, y_type, accumulate;
+  Q4Epilogue epi;             // moe_q4_linear
 };
 int64_t q4_workspace_bytes(int64_t T, int64_t N, int64_t K, int32_t x_type);
 hipError_t launch_q4_matmul(const Q4Args& a, hipStream_t s);
+hipError_t launch_q4_linear(const Q4Args& a, hipStream_t s);
 
 // balance.hip
 struct BalanceArgs {

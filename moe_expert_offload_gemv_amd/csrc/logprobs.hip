@@ -1,0 +1,521 @@
+// logprobs.hip - what a row of an output head's logits says: the log probability
+// of a given token, the entropy, the most likely tokens (moe_token_logprobs), and the
+// gradient of the first two to the logits (moe_token_logprobs_grad).
+//
+//   logprob_rows_kernel    a row, or a slice of it, once: maximum, sum of e^(z - max), sum of
+//                          e^(z - max) (z - max), and the top_n largest of it
+//   logprob_finish_kernel  the slices of a row put together (few rows: they are cut into slices)
+//   logprob_grad_kernel    logits once more: dlogits
+//
+// Bound by traffic, one read of the logits: a thread keeps a running maximum and both sums
+// over 32 values at a time, in powers of two.
+//
+// The top_n largest come out of the same read. A thread also notes the largest of each 32 values in LDS.
+// The top_n-th largest of the threads' maxima is a bound that top_n values reach at least (taken in
+// each wave, and the best wave's); the few runs of 32 whose largest reaches it are read again, from
+// cache, and what reaches it in them, about two or three times top_n values, is ranked by counting. Equal
+// values: a token's rank counts equal ones of lower id, so ties go to the lower id whatever
+// the order in which the values were found.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <algorithm>
+
+#include "kernels.h"
+#include "route_dev.h"
+#include "value_dev.h"
+
+namespace moe {
+namespace {
+
+using namespace value_dev;
+
+constexpr float kLog2e = 1.44269504089f;
+constexpr float kLowest = -3.4028234664e38f, kMinusInf = -__builtin_inff();
+// powers below this are 0 in fp32; a finite floor keeps 0 * (z - max) a zero where z is -inf
+constexpr float kFloor = -200.0f;
+constexpr int kU = 4;              // runs of 8 values of a thread, loaded at once
+constexpr int kNotes = 16;         // noted maxima of a thread
+constexpr int kSliceStep = 2048;   // slices are whole multiples
+constexpr int kMaxSlices = 64;
+constexpr int kSliceTarget = 2048; // rows times slices aimed at: eight work-groups a CU
+constexpr int kWaveRow = 2048;     // rows up to this long have one wave
+
+// maximum, sum of 2^((x - max) c) and of the same times (x - max) c
+struct Sums {
+  float m, s, u;
+};
+// the sums of `a` referred to the maximum m >= a.m
+__device__ __forceinline__ void refer(Sums& a, float m, float c) {
+  const float d = fmaxf((a.m - m) * c, kFloor), f = __builtin_amdgcn_exp2f(d);
+  a.u = f * fmaf(a.s, d, a.u);
+  a.s *= f;
+  a.m = m;
+}
+
+__device__ __forceinline__ uint32_t key_of(float v) { return route_dev::order_bits(v); }
+
+// The logits i .. i + 7 of those before `end`, in one load: where fewer are left, the last 8, with -inf
+// in the place of those before i. v[j] is logit base + j; returns base.
+template <int ZT>
+__device__ __forceinline__ int64_t load_logits(const char* row, int64_t i, int64_t end, float (&v)[8]) {
+  if (end < 8) {  // the same for the work-group
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = i + j < end ? load1<ZT>(row, i + j) : kMinusInf;
+    return i;
+  }
+  const int64_t base = std::min(i, end - 8);
+  const int skip = (int)std::min<int64_t>(i - base, 8);
+  unpack8<ZT>(load8<ZT>(row, base), v);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] = j >= skip ? v[j] : kMinusInf;
+  return base;
+}
+
+// what a row's sums say of it
+struct RowResult {
+  float m, log_sum;
+  bool none, bad;  // every logit -inf; a NaN, or a logit of +inf
+};
+__device__ __forceinline__ RowResult row_result(const Sums& t, float most, float scale) {
+  RowResult r;
+  const float z = t.m * scale;
+  r.bad = !(t.s == t.s) || z == __builtin_inff();
+  r.none = !r.bad && (most == kMinusInf || z == kMinusInf);
+  r.m = t.m;
+  r.log_sum = logf(t.s);
+  return r;
+}
+constexpr uint32_t kNan = 0x7FC00000u;
+
+// A row's outputs, by one thread: in 64 bits, for the gradient's p are e^(z - lse), and a
+// rounding of lse would scale them all. lse is handed on in two floats.
+template <int ZT>
+__device__ __forceinline__ void put_row(const LogprobArgs& a, int64_t row, const Sums& t, const RowResult& r) {
+  const double log_sum = log((double)t.s), scale = a.scale, lse = t.m * scale + log_sum;
+  const float nan = __uint_as_float(kNan);
+  if (a.logp) {
+    const int64_t y = a.targets[row];
+    float v = 0.f;
+    if (y >= 0 && y < a.V) {
+      const float x = load1<ZT>(static_cast<const char*>(a.logits) + row * a.z_stride * value_size<ZT>(), y);
+      v = r.bad ? nan : r.none ? kMinusInf : (float)(((double)x - t.m) * scale - log_sum);
+    }
+    a.logp[row] = v;
+  }
+  if (a.entropy) {
+    const float h = (float)(log_sum - (double)t.u / t.s * 0.69314718055994530942);
+    a.entropy[row] = r.bad ? nan : r.none ? 0.f : fmaxf(h, 0.f);
+  }
+  if (a.lse) {
+    const float hi = r.bad ? nan : r.none ? kMinusInf : (float)lse;
+    a.lse[2 * row] = hi;
+    a.lse[2 * row + 1] = r.bad || r.none ? 0.f : (float)(lse - hi);
+  }
+}
+// log probability of a row's value above -inf; not by way of (x - max) c, which passes fp32's range first
+__device__ __forceinline__ float row_logp(const RowResult& r, float x, float scale) { return fmaf(x - r.m, scale, -r.log_sum); }
+
+// Ranks `count` candidates (value, id) and hands each with its rank to f; every thread of the
+// work-group comes here. The order of the candidates has no part in the ranks.
+struct Candidate {
+  uint32_t key;
+  int id;
+};
+template <int THREADS, typename F>
+__device__ __forceinline__ void rank_candidates(const Candidate* s_c, int count, F f) {
+  for (int i = threadIdx.x; i < count; i += THREADS) {
+    const Candidate me = s_c[i];
+    int rank = 0;
+#pragma unroll 4
+    for (int j = 0; j < count; ++j) {
+      const Candidate o = s_c[j];
+      rank += o.key > me.key || (o.key == me.key && o.id < me.id);
+    }
+    f(me, rank);
+  }
+}
+
+// The top_n largest values above -inf of a slice, [begin, end) of a row, whose threads' maxima are `most` and
+// whose noted maxima lie in s_note: into s_c, unordered, at most kCand of them; returns how many.
+template <int THREADS>
+struct Top {
+  static constexpr int kCand = THREADS * 4 > 512 ? 1024 : 512;
+  float note[kNotes][THREADS];
+  uint16_t list[kNotes * THREADS];
+  Candidate c[kCand];
+  int n_list, n_c;
+  uint32_t bound[THREADS / 64];
+  int before[THREADS / 64 + 1];
+};
+template <int ZT, int THREADS>
+__device__ int find_top(Top<THREADS>& s, const char* row, int64_t begin, int64_t end, float most, int top_n, int iters, int per_note) {
+  constexpr int W = THREADS / 64;
+  constexpr uint32_t kNothing = 0x007FFFFFu;  // key_of(-inf)
+  const int tid = threadIdx.x, wave = tid >> 6;
+  // the largest bound that top_n of the wave's lanes reach
+  uint32_t bound = 0;
+  const uint32_t key = key_of(most);
+#pragma unroll 1
+  for (int b = 31; b >= 0; --b) {
+    const uint32_t next = bound | 1u << b;
+    if (__popcll(__ballot(key >= next)) >= top_n) bound = next;
+  }
+  if ((tid & 63) == 0) s.bound[wave] = bound;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < W; ++w) bound = max(bound, s.bound[w]);
+  const int notes = (iters + per_note - 1) / per_note;
+  const int64_t iter_values = (int64_t)THREADS * 8 * kU;
+  // all values of keys >= t, as many as there is room for; returns how many there are
+  auto gather = [&](uint32_t t) {
+    __syncthreads();
+    if (tid == 0) s.n_list = s.n_c = 0;
+    __syncthreads();
+    for (int i = 0; i < notes; ++i)
+      if (key_of(s.note[i][tid]) >= t) s.list[atomicAdd(&s.n_list, 1)] = (uint16_t)(i * THREADS + tid);
+    __syncthreads();
+    const int runs = per_note * kU, items = s.n_list * runs;
+    for (int e = tid; e < items; e += THREADS) {
+      const int note = s.list[e / runs], r = e % runs, it = note / THREADS * per_note + r / kU;
+      const int64_t i = begin + it * iter_values + ((int64_t)(r % kU) * THREADS + note % THREADS) * 8;
+      if (i >= end) continue;
+      float v[8];
+      const int first = (int)load_logits<ZT>(row, i, end, v);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const uint32_t k = key_of(v[j]);
+        if (k < t) continue;
+        const int at = atomicAdd(&s.n_c, 1);
+        if (at < Top<THREADS>::kCand) s.c[at] = Candidate{k, first + j};
+      }
+    }
+    __syncthreads();
+    return s.n_c;
+  };
+  uint32_t t = max(bound, kNothing + 1);
+  int count;
+  for (;;) {
+    count = gather(t);
+    if (count <= Top<THREADS>::kCand) return count;
+    // More than there is room for. Without the values equal to the bound (a mask's lowest value, say)?
+    count = gather(t + 1);
+    if (count <= Top<THREADS>::kCand) break;
+    // still: the top_n-th largest of those that found room is a higher bound
+    rank_candidates<THREADS>(s.c, Top<THREADS>::kCand, [&](const Candidate& me, int rank) {
+      if (rank == top_n - 1) s.bound[0] = me.key;
+    });
+    __syncthreads();
+    t = s.bound[0];
+  }
+  // those above the bound, and of those equal to it the first ones, in order
+  for (int it = 0; it < iters && count < top_n; ++it) {
+    if (!__syncthreads_or(key_of(s.note[it / per_note][tid]) >= t)) continue;
+    for (int r = 0; r < kU && count < top_n; ++r) {
+      const int64_t i = begin + it * iter_values + ((int64_t)r * THREADS + tid) * 8;
+      float v[8];
+      const int first = (int)load_logits<ZT>(row, i, end, v);
+      int mine = 0;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) mine += key_of(v[j]) == t;
+      int upto = mine;  // over the lanes up to this one
+#pragma unroll
+      for (int o = 1; o < 64; o <<= 1) {
+        const int other = __shfl_up(upto, o, 64);
+        upto += (tid & 63) >= o ? other : 0;
+      }
+      __syncthreads();
+      if ((tid & 63) == 63) s.before[wave] = upto;
+      __syncthreads();
+      int all = 0, at = count + upto - mine;
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+        if (w < wave) at += s.before[w];
+        all += s.before[w];
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (key_of(v[j]) == t) {
+          if (at < top_n) s.c[at] = Candidate{t, first + j};
+          ++at;
+        }
+      count = min(count + all, top_n);
+    }
+  }
+  __syncthreads();
+  return count;
+}
+
+// One work-group per row or slice, in turn. TOP: the largest are asked for.
+template <int ZT, int THREADS, bool TOP>
+__global__ __launch_bounds__(THREADS) void logprob_rows_kernel(LogprobArgs a) {
+  constexpr int W = THREADS / 64;
+  constexpr int64_t kIter = (int64_t)THREADS * 8 * kU;
+  __shared__ Top<TOP ? THREADS : 64> s_top;
+  __shared__ Sums s_sum[W];
+  __shared__ float s_most[W];
+  const int tid = threadIdx.x;
+  const float c = a.scale * kLog2e;
+  for (int64_t item = blockIdx.x; item < a.T * a.slices; item += gridDim.x) {
+    const int64_t row = item / a.slices;
+    const int slice = (int)(item - row * a.slices);
+    const char* z = static_cast<const char*>(a.logits) + row * a.z_stride * value_size<ZT>();
+    const int64_t begin = slice * a.slice, end = std::min<int64_t>(begin + a.slice, a.V);
+    const int iters = (int)((end - begin + kIter - 1) / kIter);
+    Sums t{kLowest, 0.f, 0.f};
+    float most = kMinusInf, noted = kMinusInf;
+    for (int it = 0; it < iters; ++it) {
+      const int64_t at = begin + it * kIter + tid * 8;
+      float v[kU][8];
+      if (begin + (it + 1) * kIter <= end) {
+        Raw8<ZT> raw[kU];
+#pragma unroll
+        for (int r = 0; r < kU; ++r) raw[r] = load8<ZT>(z, at + r * THREADS * 8);
+#pragma unroll
+        for (int r = 0; r < kU; ++r) unpack8<ZT>(raw[r], v[r]);
+      } else {
+#pragma unroll
+        for (int r = 0; r < kU; ++r) load_logits<ZT>(z, at + r * THREADS * 8, end, v[r]);
+      }
+      float m = kMinusInf;
+#pragma unroll
+      for (int r = 0; r < kU; ++r)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) m = fmaxf(m, v[r][j]);
+      if constexpr (TOP) {
+        most = fmaxf(most, m);
+        noted = fmaxf(noted, m);
+        if ((it + 1) % a.per_note == 0 || it + 1 == iters) s_top.note[it / a.per_note][tid] = noted, noted = kMinusInf;
+      } else {
+        most = fmaxf(most, m);
+      }
+      refer(t, fmaxf(t.m, m), c);
+#pragma unroll
+      for (int r = 0; r < kU; ++r)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float d = (v[r][j] - t.m) * c, e = __builtin_amdgcn_exp2f(d);
+          t.s += e;
+          t.u = fmaf(e, fmaxf(d, kFloor), t.u);
+        }
+    }
+    // over the lanes, then the waves in their order
+    float m = t.m;
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor(m, o, 64));
+    refer(t, m, c);
+    t.s = route_dev::wave_sum(t.s);
+    t.u = route_dev::wave_sum(t.u);
+    float wave_most = most;
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) wave_most = fmaxf(wave_most, __shfl_xor(wave_most, o, 64));
+    if constexpr (W > 1) {
+      __syncthreads();  // the item before has been read
+      if ((tid & 63) == 0) s_sum[tid >> 6] = t, s_most[tid >> 6] = wave_most;
+      __syncthreads();
+#pragma unroll
+      for (int w = 0; w < W; ++w) m = fmaxf(m, s_sum[w].m), wave_most = fmaxf(wave_most, s_most[w]);
+      Sums all{m, 0.f, 0.f};
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+        Sums o = s_sum[w];
+        refer(o, m, c);
+        all.s += o.s, all.u += o.u;
+      }
+      t = all;
+    }
+    const RowResult r = row_result(t, wave_most, a.scale);
+    if (a.slices == 1) {
+      if (tid == 0) put_row<ZT>(a, row, t, r);
+    } else if (tid == 0) {
+      float* p = a.sums + 4 * item;
+      p[0] = t.m, p[1] = t.s, p[2] = t.u, p[3] = wave_most;
+    }
+    if constexpr (TOP) {
+      int* ids = a.slices == 1 ? a.top_ids + row * a.top_n : a.slice_ids + item * a.top_n;
+      float* out = a.slices == 1 ? a.top_logp + row * a.top_n : a.slice_values + item * a.top_n;
+      // the same for the whole work-group
+      const bool none = r.bad || (a.slices == 1 && r.none);
+      const int count = none ? 0 : find_top<ZT, THREADS>(s_top, z, begin, end, most, a.top_n, iters, a.per_note);
+      rank_candidates<THREADS>(s_top.c, count, [&](const Candidate& me, int rank) {
+        if (rank >= a.top_n) return;
+        const float x = route_dev::order_logit(me.key);
+        ids[rank] = me.id;
+        out[rank] = a.slices == 1 ? row_logp(r, x, a.scale) : x;
+      });
+      for (int i = count + tid; i < a.top_n; i += THREADS) ids[i] = -1, out[i] = r.bad ? __uint_as_float(kNan) : kMinusInf;
+      __syncthreads();  // s_top is written again by the next item
+    }
+  }
+}
+
+// The slices of a row: their sums referred to the row's maximum, added in order; the best of their top_n.
+constexpr int kFinish = 256;
+template <int ZT>
+__global__ __launch_bounds__(kFinish) void logprob_finish_kernel(LogprobArgs a) {
+  constexpr int kCand = kMaxSlices * kMaxTop;
+  __shared__ Candidate s_c[kCand];
+  __shared__ int s_n;
+  const int64_t row = blockIdx.x;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const float c = a.scale * kLog2e;
+  // every wave forms the row's sums: a lane per slice
+  static_assert(kMaxSlices == 64, "a lane per slice");
+  const float* p = a.sums + 4 * (row * a.slices + std::min(lane, a.slices - 1));
+  const bool in = lane < a.slices;
+  Sums t{p[0], in ? p[1] : 0.f, in ? p[2] : 0.f};
+  float most = p[3], m = t.m;
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor(m, o, 64)), most = fmaxf(most, __shfl_xor(most, o, 64));
+  refer(t, m, c);
+  t.s = route_dev::wave_sum(t.s);
+  t.u = route_dev::wave_sum(t.u);
+  const RowResult r = row_result(t, most, a.scale);
+  if (tid == 0) put_row<ZT>(a, row, t, r);
+  if (!a.top_n) return;
+  if (tid == 0) s_n = 0;
+  __syncthreads();
+  const int n = r.bad || r.none ? 0 : a.slices * a.top_n;
+  for (int i = tid; i < n; i += kFinish) {
+    const int id = a.slice_ids[row * a.slices * a.top_n + i];
+    if (id >= 0) s_c[atomicAdd(&s_n, 1)] = Candidate{key_of(a.slice_values[row * a.slices * a.top_n + i]), id};
+  }
+  __syncthreads();
+  const int count = s_n;
+  rank_candidates<kFinish>(s_c, count, [&](const Candidate& me, int rank) {
+    if (rank >= a.top_n) return;
+    a.top_ids[row * a.top_n + rank] = me.id;
+    a.top_logp[row * a.top_n + rank] = row_logp(r, route_dev::order_logit(me.key), a.scale);
+  });
+  for (int i = count + tid; i < a.top_n; i += kFinish) {
+    a.top_ids[row * a.top_n + i] = -1;
+    a.top_logp[row * a.top_n + i] = r.bad ? __uint_as_float(kNan) : kMinusInf;
+  }
+}
+
+// dz_j = scale (a (j == y) - p_j (a + b (log p_j + entropy))); 32 values of a thread at once
+template <int ZT, int THREADS>
+__global__ __launch_bounds__(THREADS) void logprob_grad_kernel(LogprobGradArgs a, int pieces) {
+  constexpr int64_t kPiece = (int64_t)THREADS * 8 * kU;
+  for (int64_t item = blockIdx.x; item < a.T * pieces; item += gridDim.x) {
+    const int64_t row = item / pieces, at = (item - row * pieces) * kPiece + threadIdx.x * 8;
+    const int64_t y = a.targets ? a.targets[row] : -1;
+    const bool given = y >= 0 && y < a.V;
+    const float ga = given && a.dlogp ? a.dlogp[row] : 0.f, gb = a.dentropy ? a.dentropy[row] : 0.f;
+    const float hi = a.lse[2 * row], lo = a.lse[2 * row + 1], entropy = a.dentropy ? a.entropy[row] : 0.f;
+    // nothing is asked of the row, or it has no tokens: zeros, whatever its logits
+    const bool zero = (ga == 0.f && gb == 0.f) || hi == kMinusInf;
+    if (zero && a.accumulate) continue;
+    const char* z = static_cast<const char*>(a.logits) + row * a.z_stride * value_size<ZT>();
+    char* out = static_cast<char*>(a.dlogits) + row * a.d_stride * (a.d_type == MOE_F32 ? 4 : 2);
+    const float sa = a.scale * ga, sb = a.scale * gb;
+    auto grad = [&](float x, int64_t j) __attribute__((always_inline)) {
+      const float lp = fmaf(x, a.scale, -hi) - lo, q = __builtin_amdgcn_exp2f(lp * kLog2e);
+      const float g = -q * fmaf(sb, fmaxf(lp, kFloor) + entropy, sa);
+      return zero ? 0.f : j == y && given ? g + sa : g;
+    };
+    auto finish = [&](auto type, int64_t i, float (&v)[8]) __attribute__((always_inline)) {
+      constexpr int DT = decltype(type)::value;
+      if (a.accumulate) {
+        float old[8];
+        if (i + 8 <= a.V)
+          unpack8<DT>(load8<DT>(out, i), old);
+        else
+          load8_tail<DT>(out, i, a.V, old);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] += old[j];
+      }
+      if (i + 8 <= a.V)
+        store8<DT>(out, i, v);
+      else
+        store8_tail<DT>(out, i, a.V, v);
+    };
+    float v[kU][8];
+    if (!zero) {
+#pragma unroll
+      for (int r = 0; r < kU; ++r) {
+        const int64_t i = at + r * THREADS * 8;
+        if (i + 8 <= a.V)
+          unpack8<ZT>(load8<ZT>(z, i), v[r]);
+        else  // a row's last values: the others of the load that the sums take would be written twice
+          load8_tail<ZT>(z, i, a.V, v[r]);
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < kU; ++r) {
+      const int64_t i = at + r * THREADS * 8;
+      if (i >= a.V) break;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[r][j] = grad(v[r][j], i + j);
+      if (a.d_type == MOE_F32)
+        finish(std::integral_constant<int, MOE_F32>{}, i, v[r]);
+      else if (a.d_type == MOE_F16)
+        finish(std::integral_constant<int, MOE_F16>{}, i, v[r]);
+      else
+        finish(std::integral_constant<int, MOE_BF16>{}, i, v[r]);
+    }
+  }
+}
+
+int slices_of(int64_t T, int64_t V) {
+  if (V <= kWaveRow || T >= kSliceTarget || T < 1) return 1;
+  const int64_t want = std::min<int64_t>((kSliceTarget + T - 1) / T, kMaxSlices);
+  const int64_t slice = ((V + want - 1) / want + kSliceStep - 1) / kSliceStep * kSliceStep;
+  return (int)((V + slice - 1) / slice);
+}
+
+template <int ZT, int THREADS>
+hipError_t launch_rows(const LogprobArgs& a, dim3 grid, hipStream_t s) {
+  return a.top_n ? launch(logprob_rows_kernel<ZT, THREADS, true>, grid, dim3(THREADS), Launch{s}, a)
+                 : launch(logprob_rows_kernel<ZT, THREADS, false>, grid, dim3(THREADS), Launch{s}, a);
+}
+template <int ZT>
+hipError_t launch_types(LogprobArgs a, hipStream_t s) {
+  const int threads = a.V <= kWaveRow ? 64 : 256;
+  a.slices = slices_of(a.T, a.V);
+  a.slice = a.slices == 1 ? a.V : ((a.V + a.slices - 1) / a.slices + kSliceStep - 1) / kSliceStep * kSliceStep;
+  const int64_t per_iter = (int64_t)threads * 8 * kU, iters = (a.slice + per_iter - 1) / per_iter;
+  a.per_note = (int)((iters + kNotes - 1) / kNotes);
+  if (a.slices > 1) {
+    const int64_t items = a.T * a.slices;
+    a.sums = reinterpret_cast<float*>(a.ws);
+    a.slice_values = a.sums + 4 * items;
+    a.slice_ids = reinterpret_cast<int*>(a.slice_values + items * a.top_n);
+  }
+  // rows beyond the grid are taken in turn by the same work-groups
+  const dim3 grid((unsigned)std::min<int64_t>(a.T * a.slices, 1 << 20));
+  const hipError_t e = threads == 64 ? launch_rows<ZT, 64>(a, grid, s) : launch_rows<ZT, 256>(a, grid, s);
+  if (e != hipSuccess || a.slices == 1) return e;
+  return launch(logprob_finish_kernel<ZT>, dim3((unsigned)a.T), dim3(kFinish), Launch{s}, a);
+}
+template <int ZT>
+hipError_t launch_grad_types(const LogprobGradArgs& a, hipStream_t s) {
+  const int threads = a.V <= kWaveRow ? 64 : 256;
+  const int64_t piece = (int64_t)threads * 8 * kU;
+  const int pieces = (int)((a.V + piece - 1) / piece);
+  const dim3 grid((unsigned)std::min<int64_t>(a.T * pieces, 1 << 22));
+  return threads == 64 ? launch(logprob_grad_kernel<ZT, 64>, grid, dim3(64), Launch{s}, a, pieces)
+                       : launch(logprob_grad_kernel<ZT, 256>, grid, dim3(256), Launch{s}, a, pieces);
+}
+
+}  // namespace
+
+// Rows are cut into slices below kSliceTarget of them: at most twice that many slices in all. Never less for more rows.
+int64_t logprob_workspace_bytes(int64_t T, int64_t V, int top_n) {
+  if (V <= kWaveRow || T < 1) return 0;
+  const int64_t items = std::min<int64_t>(T * kMaxSlices, 2 * kSliceTarget);
+  return items * (16 + 8 * (int64_t)top_n);
+}
+
+hipError_t launch_logprobs(const LogprobArgs& a, hipStream_t s) {
+  if (a.z_type == MOE_F32) return launch_types<MOE_F32>(a, s);
+  if (a.z_type == MOE_F16) return launch_types<MOE_F16>(a, s);
+  return launch_types<MOE_BF16>(a, s);
+}
+hipError_t launch_logprobs_grad(const LogprobGradArgs& a, hipStream_t s) {
+  if (a.z_type == MOE_F32) return launch_grad_types<MOE_F32>(a, s);
+  if (a.z_type == MOE_F16) return launch_grad_types<MOE_F16>(a, s);
+  return launch_grad_types<MOE_BF16>(a, s);
+}
+
+}  // namespace moe
