@@ -929,13 +929,94 @@ struct Turn {
   }
 };
 
+// A wave's tile of results on its way through the epilogue, [64 tokens][kTileRow]: the four lane groups write rows 4
+// apart, 16 banks from each other
+constexpr int kTileRow = 68;
+
+// 4 values at i, of those before n
+__device__ __forceinline__ f32x4_t load_values4(const void* p, int type, int64_t i, int n) {
+  f32x4_t v = {0.f, 0.f, 0.f, 0.f};
+  if (n >= 4 && type == MOE_F32) {
+    __builtin_memcpy(&v, static_cast<const float*>(p) + i, 16);
+  } else if (n >= 4) {
+    uint32_t h[2];
+    __builtin_memcpy(h, static_cast<const uint16_t*>(p) + i, 8);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint16_t b = (uint16_t)(h[j >> 1] >> (16 * (j & 1)));
+      v[j] = type == MOE_F16 ? half_to_float(b) : bf16_to_float(b);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (j < n) v[j] = load_value(p, type, i + j);
+  }
+  return v;
+}
+__device__ __forceinline__ void store_values4(void* p, int type, int64_t i, int n, f32x4_t v) {
+  if (n >= 4 && type == MOE_F32) {
+    __builtin_memcpy(static_cast<float*>(p) + i, &v, 16);
+  } else if (n >= 4) {
+    uint16_t h[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) h[j] = type == MOE_F16 ? float_to_half(v[j]) : float_to_bf16(v[j]);
+    __builtin_memcpy(static_cast<uint16_t*>(p) + i, h, 8);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (j < n) {
+        if (type == MOE_F32)
+          store1<MOE_F32>(p, i + j, v[j]);
+        else if (type == MOE_F16)
+          store1<MOE_F16>(p, i + j, v[j]);
+        else
+          store1<MOE_BF16>(p, i + j, v[j]);
+      }
+  }
+}
+// The results of one wave's tile, tokens t0 .. t0 + 63 and features f0 .. f0 + 63, through the epilogue: four
+// tokens at a time, a lane 4 features of one; the operands of the next four are on their way meanwhile
+__device__ __forceinline__ void put_tile(const Q4Args& a, const float* s_y, int64_t t0, int f0, int lane) {
+  const Q4Epilogue& e = a.epi;
+  const int f = f0 + 4 * (lane & 15), n = (int)std::min<int64_t>(a.N - f, 4);
+  if (n <= 0) return;
+  const f32x4_t zero = {0.f, 0.f, 0.f, 0.f};
+  const f32x4_t bias = e.bias ? load_values4(e.bias, MOE_F32, f, n) : zero;
+  f32x4_t mul[2] = {zero, zero}, res[2] = {zero, zero};
+  auto fetch = [&](int i, int to) __attribute__((always_inline)) {
+    const int64_t t = t0 + 4 * i + (lane >> 4);
+    if (t >= a.T) return;
+    if (e.mul) mul[to] = load_values4(e.mul, e.mul_type, t * e.mul_stride + f, n);
+    if (e.res) res[to] = load_values4(e.res, e.res_type, t * e.res_stride + f, n);
+  };
+  auto put4 = [&](int i, int from) __attribute__((always_inline)) {
+    const int64_t t = t0 + 4 * i + (lane >> 4);
+    f32x4_t v = *reinterpret_cast<const f32x4_t*>(s_y + (4 * i + (lane >> 4)) * kTileRow + 4 * (lane & 15));
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      v[j] = activate(e.act, v[j] + bias[j]);
+      if (e.mul) v[j] *= mul[from][j];
+      if (e.res) v[j] += res[from][j];
+    }
+    if (t < a.T) store_values4(a.y, a.y_type, t * a.y_stride + f, n, v);
+  };
+  fetch(0, 0);
+#pragma unroll 1
+  for (int i = 0; i < 16; i += 2) {
+    fetch(i + 1, 1);
+    put4(i, 0);
+    if (i + 2 < 16) fetch(i + 2, 0);
+    put4(i + 1, 1);
+  }
+}
+
 // two work-groups a CU, but for split fp32 tiles, whose stages of three terms leave room for one
 template <int XT, int SB, int WK, int RING>
 __global__ __launch_bounds__(256, WK > 1 && terms_of<XT>() == 3 ? 1 : 2) void q4_wide_kernel(Q4Args a, Operand o, int row_tiles, int col_tiles) {
   constexpr int TERMS = terms_of<XT>(), SIDE = wide_side(WK), MG = SIDE / 16;  // row tiles of 16 in the stages
   constexpr int RUNS = runs_of<XT>(), kBlockBase = 64 * RUNS;
   constexpr int kTermBytes = MG * SB * TERMS * 1024, kBaseBytes = MG * SB * kBlockBase, kStage = kTermBytes + kBaseBytes;
-  constexpr int kSums = WK > 1 ? WK * 16 * 64 * 16 : 0;
+  constexpr int kSums = WK > 1 ? WK * 16 * 64 * 16 : kEpilogue ? 4 * 64 * kTileRow * 4 : 0;
   constexpr int kLds = RING * kStage * WK;
   static_assert(RING == 2 || SB == 1, "the ring's waits count blocks");
   static_assert(sizeof(StepWeights::w) == 16, "a load_step is one load of 16 bytes and one of a scale: kStepLoads");
@@ -1091,7 +1172,24 @@ __global__ __launch_bounds__(256, WK > 1 && terms_of<XT>() == 3 ? 1 : 2) void q4
       for (int m = 0; m < 4; ++m) scale(4 * SB - 1, m);
     }
   }
-  if constexpr (WK == 1) {
+  if constexpr (WK == 1 && kEpilogue) {
+    // Through LDS: the epilogue reads its operands and writes y in whole lines, 64 features of a token by
+    // 16 lanes, in a loop (4096 x 4096 x 4096 bf16 with all of it: 260 us; 340 in the
+    // lanes' own order, 2-byte accesses by 16 lanes).
+    // Every wave is done with the stages and the copies behind the last one have landed; a wave's
+    // 64 x 64 results are then its own.
+    __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
+    __syncthreads();
+    float* s_y = reinterpret_cast<float*>(s_lds) + wave * (64 * kTileRow);
+#pragma unroll
+    for (int m = 0; m < 4; ++m)
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) s_y[(16 * m + 4 * c + r) * kTileRow + 16 * t + col] = acc[m][t][r];
+    Turn::exchange();
+    put_tile(a, s_y, (int64_t)rt * SIDE + 16 * m0, f0, lane);
+  } else if constexpr (WK == 1) {
     // lane (column, c) holds tokens 4c + r of its features
 #pragma unroll
     for (int m = 0; m < 4; ++m)

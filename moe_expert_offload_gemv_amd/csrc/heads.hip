@@ -6,9 +6,14 @@
 //   (a, b) -> (a cos - b sin, b cos + a sin)        for each of the R / 2 pairs
 //
 // Bound by traffic: every value is read and written once. A row is a head of a token,
-// in the registers of G lanes (heads_dev.h); a work-group takes up to 4 rows per row
-// group, all loads before the first use, and forms the angles of its tokens once in LDS
-// meanwhile. Queries and keys are two ranges of work-groups of one launch.
+// in the registers of G lanes (heads_dev.h); a work-group takes up to 8 rows per row
+// group, the next one's loads on their way behind each, and forms the angles of all their tokens
+// once in LDS beforehand. Queries and keys are two ranges of work-groups of one launch.
+//
+// Measured (as nodes of a graph): 4096 x 36 heads of 128 bf16, 75 MB, 14.6-15 us = 5.1 TB/s, a copy's rate
+// (2 rows a group and no loads ahead 16.7, 4 rows at once 18.4); 12287 x 16 heads of 80 fp16, three axes, 63 MB,
+// 17.4 = 3.6 TB/s (10 of 16 lanes have values, and 2.3e5 instructions a SIMD are 15 of it); one token,
+// 18 heads of 128 fp32, 3.2: a launch, two trips to memory and the angles between.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -22,14 +27,27 @@ namespace {
 
 using namespace heads_dev;
 
+constexpr int kHeadSteps = 8;   // rows per row group whose angles are formed together
+constexpr int kHeadAim = 1536;  // work-groups of queries, and of keys
+
+// what a lane has of a row: its values as loaded, and where they go
+template <int XT, int RUN, int NG>
+struct HeadRow {
+  RawRun<XT, RUN> x[NG][2];
+  int64_t out;
+  int token;
+};
+
 template <int XT, int RUN, int NG, bool PAIRS>
 __global__ __launch_bounds__(kThreads) void heads_kernel(HeadsArgs a) {
-  constexpr int U = kHeadRows;
+  using Row = HeadRow<XT, RUN, NG>;
   extern __shared__ __attribute__((aligned(16))) float2 s_turn[];
   const bool is_k = (int)blockIdx.x >= a.q.blocks;
   const HeadsPart p = is_k ? a.k : a.q;
   const int G = a.lanes, l = threadIdx.x & (G - 1), mine = threadIdx.x >> a.lanes_log;
   const int at_once = kThreads >> a.lanes_log, S = a.D / 2;
+  const bool some_still = a.R < a.D || a.axis;
+  const float inv_D = 1.0f / (float)a.D;
   Place place[NG];
   float wa[NG][RUN], wb[NG][RUN];
 #pragma unroll
@@ -50,72 +68,75 @@ __global__ __launch_bounds__(kThreads) void heads_kernel(HeadsArgs a) {
     if (r0 >= a.T * p.H) break;
     const int64_t t0 = r0 / p.H;
     const int h0 = (int)(r0 - t0 * p.H), n = (int)std::min<int64_t>(p.rows, a.T * p.H - r0);
-    RawRun<XT, RUN> raw[U][NG][2];
-    int token[U];
-    int64_t out[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (u * at_once >= n) break;
-      const int i = h0 + min(u * at_once + mine, n - 1);  // past the last row: it again, never stored
-      token[u] = quotient(i, p.magic);
-      const int h = i - token[u] * p.H;
-      const char* x = static_cast<const char*>(p.x) + ((t0 + token[u]) * p.x_stride + h * p.x_head) * value_size<XT>();
-      out[u] = (t0 + token[u]) * p.out_stride + h * p.out_head;
+    // a row group's row of step u; past the last row: it again, never stored
+    auto fetch = [&](int u, Row& to) __attribute__((always_inline)) {
+      const int i = h0 + min(u * at_once + mine, n - 1);
+      to.token = quotient(i, p.magic);
+      const int h = i - to.token * p.H;
+      const int64_t t = t0 + to.token;
+      const char* x = static_cast<const char*>(p.x) + (t * p.x_stride + h * p.x_head) * value_size<XT>();
+      to.out = t * p.out_stride + h * p.out_head;
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
-        raw[u][g][0] = load_run<XT, RUN>(x + place[g].a * value_size<XT>());
-        raw[u][g][1] = load_run<XT, RUN>(x + place[g].b * value_size<XT>());
+        to.x[g][0] = load_run<XT, RUN>(x + place[g].a * value_size<XT>());
+        to.x[g][1] = load_run<XT, RUN>(x + place[g].b * value_size<XT>());
       }
-    }
+    };
+    const int steps = (n + at_once - 1) / at_once;
+    Row next;
+    fetch(0, next);
     if (a.R) {
       __syncthreads();  // every wave is done with the rows before
       fill_turns(a, t0, quotient(h0 + n - 1, p.magic) + 1, s_turn);
       __syncthreads();
     }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (u * at_once >= n) break;
+    auto step = [&](int u, Row& now) __attribute__((always_inline)) {
       float va[NG][RUN], vb[NG][RUN], ss = 0.f;
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
-        unpack_slots<XT, PAIRS, RUN>(raw[u][g], va[g], vb[g]);
+        unpack_slots<XT, PAIRS, RUN>(now.x[g], va[g], vb[g]);
+        float part = 0.f;
 #pragma unroll
         for (int j = 0; j < RUN; ++j) {
-          va[g][j] = place[g].in ? va[g][j] : 0.f;
-          vb[g][j] = place[g].in ? vb[g][j] : 0.f;
-          ss = fmaf(va[g][j], va[g][j], ss);
-          ss = fmaf(vb[g][j], vb[g][j], ss);
+          part = fmaf(va[g][j], va[g][j], part);
+          part = fmaf(vb[g][j], vb[g][j], part);
         }
+        ss += place[g].in ? part : 0.f;
       }
-      Inverse inv{1.0f, 1.0f};
+      float r = 1.0f;
       if (a.norm)
-        inv = inverse_rms(lanes_sum(ss, G), (float)a.D, a.eps, [&](float k) {
-          float s2 = 0.f;
+        r = inverse_rms(lanes_sum(ss, G), inv_D, (float)a.D, a.eps, [&](float k, float rest) {
+              float s2 = 0.f;
 #pragma unroll
-          for (int g = 0; g < NG; ++g)
+              for (int g = 0; g < NG; ++g)
 #pragma unroll
-            for (int j = 0; j < RUN; ++j) {
-              const float x = va[g][j] * k, y = vb[g][j] * k;
-              s2 = fmaf(x, x, s2);
-              s2 = fmaf(y, y, s2);
-            }
-          return lanes_sum(s2, G);
-        });
-      if (u * at_once + mine >= n) continue;
-      char* row = static_cast<char*>(p.out) + out[u] * (a.out_type == MOE_F32 ? 4 : 2);
+                for (int j = 0; j < RUN; ++j) {
+                  va[g][j] *= k, vb[g][j] *= k;
+                  const float x = place[g].in ? va[g][j] * rest : 0.f, y = place[g].in ? vb[g][j] * rest : 0.f;
+                  s2 = fmaf(x, x, s2);
+                  s2 = fmaf(y, y, s2);
+                }
+              return lanes_sum(s2, G);
+            }).r;
+      const int token = now.token;
+      char* row = static_cast<char*>(p.out) + now.out * (a.out_type == MOE_F32 ? 4 : 2);
+      if (u + 1 < steps) fetch(u + 1, now);
+      if (u * at_once + mine >= n) return;
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
         if (!place[g].in) continue;
-        const float2* angles = s_turn + token[u] * S + RUN * (l + G * g);
-        float ya[RUN], yb[RUN];
 #pragma unroll
-        for (int j = 0; j < RUN; ++j) {
-          const float x = va[g][j] * inv.half * inv.r * wa[g][j], y = vb[g][j] * inv.half * inv.r * wb[g][j];
-          turn(x, y, a.R ? angles[j] : make_float2(1.0f, 0.0f), ya[j], yb[j]);
+        for (int j = 0; j < RUN; ++j) va[g][j] = va[g][j] * r * wa[g][j], vb[g][j] = vb[g][j] * r * wb[g][j];
+        if (a.R) {
+          float2 angles[RUN];
+          load_turns<RUN>(s_turn + token * S + RUN * (l + G * g), angles);
+          turn<false, RUN>(va[g], vb[g], angles, some_still);
         }
-        store_slots<PAIRS, RUN>(a.out_type, row, place[g], ya, yb);
+        store_slots<PAIRS, RUN>(a.out_type, row, place[g], va[g], vb[g]);
       }
-    }
+    };
+#pragma unroll 1
+    for (int u = 0; u < steps; ++u) step(u, next);
   }
 }
 
@@ -128,7 +149,7 @@ hipError_t launch_types(const HeadsArgs& a, const Launch& l, dim3 grid) {
 template <bool PAIRS>
 hipError_t launch_run(const HeadsArgs& a, int run, const Launch& l, dim3 grid) {
   switch (run) {
-    case 8: return launch_types<8, 1, PAIRS>(a, l, grid);
+    case 6: return launch_types<6, 1, PAIRS>(a, l, grid);
     case 4: return launch_types<4, 1, PAIRS>(a, l, grid);
     case 2: return launch_types<2, 2, PAIRS>(a, l, grid);
     default: return launch_types<1, 4, PAIRS>(a, l, grid);
@@ -137,29 +158,41 @@ hipError_t launch_run(const HeadsArgs& a, int run, const Launch& l, dim3 grid) {
 
 }  // namespace
 
-HeadsShape heads_shape(int D, int R, bool pairs) {
-  HeadsShape s;
-  // a run lies on one side of every boundary: that of the values that turn, and the middle of either side
-  for (s.run = 8; s.run > 1; s.run /= 2)
-    if (pairs ? D % (2 * s.run) == 0 : R / 2 % s.run == 0 && (D - R) / 2 % s.run == 0) break;
-  const int groups = D / 2 / s.run, per_lane = s.run >= 4 ? 1 : s.run == 2 ? 2 : 4;
-  for (s.lanes_log = 0; (per_lane << s.lanes_log) < groups; ++s.lanes_log) {
+// The slots of a run and the lanes of a head. A run lies on one side of every boundary: that of the values that
+// turn, and the middle of either side. Of the runs that do, the one that leaves the fewest lanes without
+// values, 4 before others (us: 12287 x 10 heads of 192 bf16, 6 slots 24.5, 4 slots 27.3; gradient of 4096 x 32 heads of 72
+// and 80, 6 and 5 slots 17.4 and 19.5, 4 slots 23.3 and 23.2; forward, 5 slots of 80 are slower than 4, 21.5 and 19.7;
+// 8 slots, half as many lanes and twice the registers, lose at 4096 x 36 of 128: 17.7 and 16.7, gradient 41.5 and 34.4).
+HeadsShape heads_shape(int D, int R, bool pairs, bool grad) {
+  HeadsShape best{1, 0};
+  int most = 0;
+  for (int run : {4, 6, 5, 2, 1}) {
+    if (run == 5 && !grad) continue;
+    if (pairs ? D % (2 * run) : R / 2 % run || (D - R) / 2 % run) continue;
+    const int groups = D / 2 / run, per_lane = run >= 4 ? 1 : run == 2 ? 2 : 4;
+    if (run < 4 && most) break;  // narrower accesses only where nothing else fits
+    int log = 0;
+    while ((per_lane << log) < groups) ++log;
+    const int filled = 64 * groups / (per_lane << log);
+    if (log <= 6 && filled > most) best = HeadsShape{run, log}, most = filled;
   }
-  return s;
+  return best;
 }
 
-// Rows of a work-group: as many as its loads in flight hold, fewer while that leaves CUs without one,
-// and no more than the LDS has angles for (32 KB: five work-groups a CU).
-void heads_split(HeadsPart& p, const HeadsArgs& a, int max_rows, int64_t max_blocks) {
+// Rows of a work-group and work-groups: as many of these as are aimed at, up to max_rows rows per row group each and no
+// more rows than the LDS has angles for (32 KB: five work-groups a CU). Beyond max_blocks they take rows in turn,
+// all of them about as often.
+void heads_split(HeadsPart& p, const HeadsArgs& a, int64_t aim, int max_rows, int64_t max_blocks) {
   const int at_once = kThreads >> a.lanes_log;
-  const int64_t rows = a.T * p.H, want = (rows + 512 * at_once - 1) / (512 * at_once);
+  const int64_t rows = a.T * p.H, want = (rows + aim * at_once - 1) / (aim * at_once);
   p.rows = at_once * (int)std::max<int64_t>(1, std::min<int64_t>(want, max_rows));
   if (a.R) {
     const int tokens = 32768 / (a.D / 2 * 8);
     p.rows = std::min(p.rows, p.H == 1 ? tokens : (tokens - 2) * p.H);
   }
   p.magic = (uint32_t)(((1ll << 31) + p.H - 1) / std::max(p.H, 1));
-  p.blocks = (int)std::min<int64_t>((rows + p.rows - 1) / p.rows, max_blocks);
+  const int64_t chunks = (rows + p.rows - 1) / p.rows, turns = (chunks + max_blocks - 1) / max_blocks;
+  p.blocks = turns ? (int)((chunks + turns - 1) / turns) : 0;
 }
 uint32_t heads_lds(const HeadsArgs& a) {
   if (!a.R) return 0;
@@ -170,12 +203,12 @@ uint32_t heads_lds(const HeadsArgs& a) {
 }
 
 hipError_t launch_heads(HeadsArgs a, hipStream_t s) {
-  const HeadsShape shape = heads_shape(a.D, a.R, a.pairs);
+  const HeadsShape shape = heads_shape(a.D, a.R, a.pairs, false);
   a.lanes_log = shape.lanes_log, a.lanes = 1 << shape.lanes_log;
   a.slot_magic = (uint32_t)(((1ll << 31) + a.D / 2 - 1) / (a.D / 2));
   // rows beyond the grid are taken in turn by the same work-groups
   for (HeadsPart* p : {&a.q, &a.k})
-    if (p->H) heads_split(*p, a, kHeadRows, 1 << 20);
+    if (p->H) heads_split(*p, a, kHeadAim, kHeadSteps, 1 << 20);
   const Launch l{s, nullptr, nullptr, heads_lds(a)};
   const dim3 grid((unsigned)(a.q.blocks + a.k.blocks));
   return a.pairs ? launch_run<true>(a, shape.run, l, grid) : launch_run<false>(a, shape.run, l, grid);

@@ -104,32 +104,39 @@ __device__ __forceinline__ void unpack_slots(const RawRun<TYPE, RUN> (&r)[2], fl
     for (int j = 0; j < RUN; ++j) x[i][j] = run_value<TYPE, RUN>(r[i], j);
   to_slots<PAIRS, RUN>(x, a, b);
 }
-template <bool PAIRS, int RUN>
-__device__ __forceinline__ void store_slots(int type, char* row, const Place& p, const float (&a)[RUN], const float (&b)[RUN]) {
+template <int TYPE, bool PAIRS, int RUN>
+__device__ __forceinline__ void store_slots_as(char* row, const Place& p, const float (&a)[RUN], const float (&b)[RUN]) {
   float x[2][RUN];
   from_slots<PAIRS, RUN>(a, b, x);
+  store_run<TYPE, RUN>(row + value_size<TYPE>() * p.a, x[0]);
+  store_run<TYPE, RUN>(row + value_size<TYPE>() * p.b, x[1]);
+}
+template <bool PAIRS, int RUN>
+__device__ __forceinline__ void store_slots(int type, char* row, const Place& p, const float (&a)[RUN], const float (&b)[RUN]) {
   if (type == MOE_F32)
-    store_run<MOE_F32, RUN>(row + 4 * p.a, x[0]), store_run<MOE_F32, RUN>(row + 4 * p.b, x[1]);
+    store_slots_as<MOE_F32, PAIRS, RUN>(row, p, a, b);
   else if (type == MOE_F16)
-    store_run<MOE_F16, RUN>(row + 2 * p.a, x[0]), store_run<MOE_F16, RUN>(row + 2 * p.b, x[1]);
+    store_slots_as<MOE_F16, PAIRS, RUN>(row, p, a, b);
   else
-    store_run<MOE_BF16, RUN>(row + 2 * p.a, x[0]), store_run<MOE_BF16, RUN>(row + 2 * p.b, x[1]);
+    store_slots_as<MOE_BF16, PAIRS, RUN>(row, p, a, b);
 }
 
-// sum over the G lanes of a row (a power of two), in every one of them
+// sum over the G lanes of a row (a power of two), in every one of them; selects, not branches, within 16 lanes
 __device__ __forceinline__ float lanes_sum(float v, int G) {
   using namespace route_dev;
-  if (G > 1) v += __uint_as_float(dpp32<kDppQuadXor1>(__float_as_uint(v)));
-  if (G > 2) v += __uint_as_float(dpp32<kDppQuadXor2>(__float_as_uint(v)));
-  if (G > 4) v += __uint_as_float(dpp32<kDppRowHalfMirror>(__float_as_uint(v)));
-  if (G > 8) v += __uint_as_float(dpp32<kDppRowMirror>(__float_as_uint(v)));
+  float w = v + __uint_as_float(dpp32<kDppQuadXor1>(__float_as_uint(v)));
+  v = G > 1 ? w : v;
+  w = v + __uint_as_float(dpp32<kDppQuadXor2>(__float_as_uint(v)));
+  v = G > 2 ? w : v;
+  w = v + __uint_as_float(dpp32<kDppRowHalfMirror>(__float_as_uint(v)));
+  v = G > 4 ? w : v;
+  w = v + __uint_as_float(dpp32<kDppRowMirror>(__float_as_uint(v)));
+  v = G > 8 ? w : v;
   if (G > 16) {
     const auto s = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
     v = __uint_as_float(s[0]) + __uint_as_float(s[1]);
-  }
-  if (G > 32) {
-    const auto s = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-    v = __uint_as_float(s[0]) + __uint_as_float(s[1]);
+    const auto t = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = G > 32 ? __uint_as_float(t[0]) + __uint_as_float(t[1]) : v;
   }
   return v;
 }
@@ -163,12 +170,35 @@ __device__ __forceinline__ float2 turn_of(int position, float inv_freq) {
   return r;
 }
 
-// (a, b) turned by (cos, sin). Without a sine neither sees the other: what does not turn is not
-// spoilt by a neighbour that is not finite.
-__device__ __forceinline__ void turn(float a, float b, float2 cs, float& ya, float& yb) {
-  const float pa = b * cs.y, pb = a * cs.y;
-  ya = fmaf(a, cs.x, cs.y != 0.f ? -pa : 0.f);
-  yb = fmaf(b, cs.x, cs.y != 0.f ? pb : 0.f);
+// The slots (a, b) turned by their (cos, sin), by minus the angle with BACK. some_still: there are slots that do not
+// turn, whose sine is 0; without a sine neither value sees the other, so that they are not spoilt
+// by a neighbour that is not finite.
+template <bool BACK, int RUN>
+__device__ __forceinline__ void turn(float (&a)[RUN], float (&b)[RUN], const float2 (&cs)[RUN], bool some_still) {
+  float pa[RUN], pb[RUN];
+#pragma unroll
+  for (int j = 0; j < RUN; ++j) pa[j] = (BACK ? b[j] : -b[j]) * cs[j].y, pb[j] = (BACK ? -a[j] : a[j]) * cs[j].y;
+  if (some_still) {
+#pragma unroll
+    for (int j = 0; j < RUN; ++j) pa[j] = cs[j].y != 0.f ? pa[j] : 0.f, pb[j] = cs[j].y != 0.f ? pb[j] : 0.f;
+  }
+#pragma unroll
+  for (int j = 0; j < RUN; ++j) a[j] = fmaf(a[j], cs[j].x, pa[j]), b[j] = fmaf(b[j], cs[j].x, pb[j]);
+}
+
+// the angles of a group of slots, in the widest reads that its place allows
+template <int RUN>
+__device__ __forceinline__ void load_turns(const float2* p, float2 (&cs)[RUN]) {
+  if constexpr (RUN % 2 == 0) {
+#pragma unroll
+    for (int j = 0; j < RUN; j += 2) {
+      const f32x4_t v = *reinterpret_cast<const f32x4_t*>(p + j);  // whole groups: 16-byte aligned
+      cs[j] = make_float2(v[0], v[1]), cs[j + 1] = make_float2(v[2], v[3]);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < RUN; ++j) cs[j] = p[j];
+  }
 }
 
 // The (cos, sin) of tokens t0 .. t0 + n - 1, every slot, once per work-group and not per head: [token][D / 2]
@@ -185,27 +215,30 @@ __device__ __forceinline__ void fill_turns(const HeadsArgs& a, int64_t t0, int n
   }
 }
 
-// 1 / sqrt(mean + eps) = r * half of a row whose squares sum to ss; again(k): the same sum of the values
-// times k. Squares leave fp32's range long before the values do, as in the norm of whole rows: such a
-// row is summed a second time, scaled by a power of two. Every lane of the wave comes here.
+// 1 / sqrt(mean + eps) of a row whose squares sum to ss, D values, to the last bit of the device's reciprocal
+// root. Squares leave fp32's range long before the values do, as in the norm of whole rows: such a row is
+// summed a second time, scaled by a power of two. scaled(k) multiplies the row's values by k
+// and returns the same sum of them times k; afterwards the values are those of the row times `left`,
+// and the result belongs to them. Every lane of the wave comes here.
 struct Inverse {
-  float r, half;
+  float r, left;
 };
 template <typename F>
-__device__ __forceinline__ Inverse inverse_rms(float ss, float D, float eps, F again) {
+__device__ __forceinline__ Inverse inverse_rms(float ss, float inv_D, float D, float eps, F scaled) {
   // a square rounded below fp32's normal range is off by at most 2^-150: beside a mean of 2^-100, or an
   // eps of it, that is nothing
   const float least = eps < 0x1p-100f ? 0x1p-100f * D : 0.f;
-  Inverse i{1.0f / sqrtf(ss / D + eps), 1.0f};
+  Inverse i{__builtin_amdgcn_rsqf(fmaf(ss, inv_D, eps)), 1.0f};
   const bool fine = ss >= least && ss < __builtin_inff();
   if (__builtin_expect(__any(!fine), 0)) {
+    // 2^-80 as 2^-40 now and 2^-40 in the result (2^100 as 2^34 and 2^66), so that neither leaves the normal
+    // range before the normed value does
     const bool large = !(ss < __builtin_inff());
-    const float k = large ? 0x1p-80f : 0x1p100f;
-    const float s2 = again(k);
-    if (!fine) {
-      i.r = 1.0f / sqrtf(s2 / D + eps * k * k) * (large ? 0x1p-40f : 0x1p66f);
-      i.half = large ? 0x1p-40f : 0x1p34f;
-    }
+    const float k = fine ? 1.0f : large ? 0x1p-40f : 0x1p34f, rest = fine ? 1.0f : large ? 0x1p-40f : 0x1p66f;
+    const float s2 = scaled(k, rest);
+    i.left = k;
+    // eps times (k rest)^2 in this order: the square alone may leave the range
+    i.r = __builtin_amdgcn_rsqf(fmaf(s2, inv_D, eps * k * rest * k * rest)) * rest;
   }
   return i;
 }

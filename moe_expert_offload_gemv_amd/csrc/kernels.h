@@ -309,7 +309,6 @@ struct NormArgs {
 hipError_t launch_add_rmsnorm(const NormArgs& a, hipStream_t s);
 
 // heads.hip, heads_grad.hip
-constexpr int kHeadRows = 4;  // rows per row group of a work-group, loaded at once
 struct HeadsPart {     // queries, or keys
   const void* x;
   const void* g;       // gradient of the output (moe_qk_norm_rope_grad)
@@ -335,8 +334,8 @@ struct HeadsArgs {
 struct HeadsShape {
   int run, lanes_log;    // slots of a run, log2 of the lanes of a head
 };
-HeadsShape heads_shape(int D, int R, bool pairs);
-void heads_split(HeadsPart& p, const HeadsArgs& a, int max_rows, int64_t max_blocks);
+HeadsShape heads_shape(int D, int R, bool pairs, bool grad);
+void heads_split(HeadsPart& p, const HeadsArgs& a, int64_t aim, int max_rows, int64_t max_blocks);
 uint32_t heads_lds(const HeadsArgs& a);  // bytes of a work-group's angles
 hipError_t launch_heads(HeadsArgs a, hipStream_t s);
 int64_t heads_grad_workspace_bytes(int64_t T, int32_t Hq, int32_t Hk, int32_t D);

@@ -117,23 +117,43 @@ __device__ __forceinline__ void put_row(const LogprobArgs& a, int64_t row, const
 __device__ __forceinline__ float row_logp(const RowResult& r, float x, float scale) { return fmaf(x - r.m, scale, -r.log_sum); }
 
 // Ranks `count` candidates (value, id) and hands each with its rank to f; every thread of the
-// work-group comes here. The order of the candidates has no part in the ranks.
+// work-group comes here. The order of the candidates has no part in the ranks. Four lanes share a
+// candidate and compare it with every fourth, four at a time (the array holds whole sixteens).
 struct Candidate {
   uint32_t key;
   int id;
 };
 template <int THREADS, typename F>
 __device__ __forceinline__ void rank_candidates(const Candidate* s_c, int count, F f) {
-  for (int i = threadIdx.x; i < count; i += THREADS) {
-    const Candidate me = s_c[i];
-    int rank = 0;
-#pragma unroll 4
-    for (int j = 0; j < count; ++j) {
-      const Candidate o = s_c[j];
-      rank += o.key > me.key || (o.key == me.key && o.id < me.id);
+  const int whole_waves = (4 * count + 63) & ~63;
+  for (int e = threadIdx.x; e < whole_waves; e += THREADS) {
+    const int i = e >> 2;
+    const Candidate me = s_c[min(i, count - 1)];
+    uint32_t rank = 0;
+#pragma unroll 1
+    for (int j0 = e & 3; j0 < count; j0 += 16) {
+      Candidate o[4];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) o[r] = s_c[j0 + 4 * r];
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        rank += j0 + 4 * r < count && (o[r].key > me.key || (o[r].key == me.key && o[r].id < me.id));
     }
-    f(me, rank);
+    rank += route_dev::dpp32<route_dev::kDppQuadXor1>(rank);
+    rank += route_dev::dpp32<route_dev::kDppQuadXor2>(rank);
+    if ((e & 3) == 0 && i < count) f(me, (int)rank);
   }
+}
+
+// the largest key that at least n of the wave's lanes reach
+__device__ __forceinline__ uint32_t nth_of_lanes(uint32_t key, int n) {
+  uint32_t bound = 0;
+#pragma unroll 1
+  for (int b = 31; b >= 0; --b) {
+    const uint32_t next = bound | 1u << b;
+    if (__popcll(__ballot(key >= next)) >= n) bound = next;
+  }
+  return bound;
 }
 
 // The top_n largest values above -inf of a slice, [begin, end) of a row, whose threads' maxima are `most` and
@@ -153,14 +173,7 @@ __device__ int find_top(Top<THREADS>& s, const char* row, int64_t begin, int64_t
   constexpr int W = THREADS / 64;
   constexpr uint32_t kNothing = 0x007FFFFFu;  // key_of(-inf)
   const int tid = threadIdx.x, wave = tid >> 6;
-  // the largest bound that top_n of the wave's lanes reach
-  uint32_t bound = 0;
-  const uint32_t key = key_of(most);
-#pragma unroll 1
-  for (int b = 31; b >= 0; --b) {
-    const uint32_t next = bound | 1u << b;
-    if (__popcll(__ballot(key >= next)) >= top_n) bound = next;
-  }
+  uint32_t bound = nth_of_lanes(key_of(most), top_n);
   if ((tid & 63) == 0) s.bound[wave] = bound;
   __syncthreads();
 #pragma unroll
@@ -375,10 +388,16 @@ __global__ __launch_bounds__(kFinish) void logprob_finish_kernel(LogprobArgs a) 
   if (!a.top_n) return;
   if (tid == 0) s_n = 0;
   __syncthreads();
+  // The slices' lists are in order. With `deep` = top_n / slices, rounded up: where top_n / deep slices, rounded up,
+  // have their deep-th value at a bound or above it, top_n values reach it.
+  const int64_t lists = row * a.slices * a.top_n;
+  const int deep = (a.top_n + a.slices - 1) / a.slices;
+  const uint32_t bound = nth_of_lanes(in ? key_of(a.slice_values[lists + lane * a.top_n + deep - 1]) : 0u, (a.top_n + deep - 1) / deep);
   const int n = r.bad || r.none ? 0 : a.slices * a.top_n;
   for (int i = tid; i < n; i += kFinish) {
-    const int id = a.slice_ids[row * a.slices * a.top_n + i];
-    if (id >= 0) s_c[atomicAdd(&s_n, 1)] = Candidate{key_of(a.slice_values[row * a.slices * a.top_n + i]), id};
+    const int id = a.slice_ids[lists + i];
+    const uint32_t key = key_of(a.slice_values[lists + i]);
+    if (id >= 0 && key >= bound) s_c[atomicAdd(&s_n, 1)] = Candidate{key, id};
   }
   __syncthreads();
   const int count = s_n;
