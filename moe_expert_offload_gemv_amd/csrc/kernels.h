@@ -353,8 +353,8 @@ struct LogprobArgs {
   int64_t z_stride, T, V;
   int32_t z_type, top_n;
   float scale;
-  // of the launch: slices of a row, values of a slice, iterations of a noted maximum
-  int32_t slices, per_note;
+  // of the launch: slices of a row, values of a slice, log2 of the iterations of a noted maximum
+  int32_t slices, note_log;
   int64_t slice;
   float *sums, *slice_values;  // [T][slices][4], [T][slices][top_n]
   int32_t* slice_ids;

@@ -8,14 +8,21 @@
 //   logprob_grad_kernel    logits once more: dlogits
 //
 // Bound by traffic, one read of the logits: a thread keeps a running maximum and both sums
-// over 32 values at a time, in powers of two.
+// over 16 values at a time, the next 16 on their way, in powers of two; 12 issue slots a value of which the
+// power takes four, so that 16-bit logits are nearly as long in the vector unit as on their way. Rows are cut
+// into slices while all of them fit on the chip at once.
 //
-// The top_n largest come out of the same read. A thread also notes the largest of each 32 values in LDS.
+// The top_n largest come out of the same read. A thread also notes the largest of its values in LDS.
 // The top_n-th largest of the threads' maxima is a bound that top_n values reach at least (taken in
-// each wave, and the best wave's); the few runs of 32 whose largest reaches it are read again, from
+// each wave, and the best wave's); the few runs whose largest reaches it are read again, from
 // cache, and what reaches it in them, about two or three times top_n values, is ranked by counting. Equal
 // values: a token's rank counts equal ones of lower id, so ties go to the lower id whatever
 // the order in which the values were found.
+//
+// Measured (as nodes of a graph): 4096 x 65537 bf16, 537 MB, 124 us = 4.3 TB/s, its gradient, 1074 MB, 212 = 5.1 TB/s, the
+// rate of a copy; 4096 x 32000 fp32 91 = 5.8 TB/s; 301 x 131072 bf16 with 8 alternatives 26 (floor 15: finding
+// them takes 5, the finishing launch 5); 1 x 65537 fp32 with 20, 13.7: two launches of a few dependent
+// trips to memory and LDS each, 3.6 and 2.4 without alternatives.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -34,11 +41,11 @@ constexpr float kLog2e = 1.44269504089f;
 constexpr float kLowest = -3.4028234664e38f, kMinusInf = -__builtin_inff();
 // powers below this are 0 in fp32; a finite floor keeps 0 * (z - max) a zero where z is -inf
 constexpr float kFloor = -200.0f;
-constexpr int kU = 4;              // runs of 8 values of a thread, loaded at once
-constexpr int kNotes = 16;         // noted maxima of a thread
+constexpr int kULog = 1, kU = 1 << kULog;  // runs of 8 values of a thread, loaded at once
+constexpr int kNotes = 8;          // noted maxima of a thread
 constexpr int kSliceStep = 2048;   // slices are whole multiples
 constexpr int kMaxSlices = 64;
-constexpr int kSliceTarget = 2048; // rows times slices aimed at: eight work-groups a CU
+constexpr int kSliceTarget = 1024; // rows times slices at most: four work-groups a CU, all of them at once
 constexpr int kWaveRow = 2048;     // rows up to this long have one wave
 
 // maximum, sum of 2^((x - max) c) and of the same times (x - max) c
@@ -55,18 +62,22 @@ __device__ __forceinline__ void refer(Sums& a, float m, float c) {
 
 __device__ __forceinline__ uint32_t key_of(float v) { return route_dev::order_bits(v); }
 
+// 8 logits from logit i of a row on (below 2^22 of them): a 32-bit offset from the row's address
+template <int ZT>
+__device__ __forceinline__ Raw8<ZT> load_run(const char* row, int i) {
+  return load8<ZT>(row + (uint32_t)i * (uint32_t)value_size<ZT>(), 0);
+}
 // The logits i .. i + 7 of those before `end`, in one load: where fewer are left, the last 8, with -inf
 // in the place of those before i. v[j] is logit base + j; returns base.
 template <int ZT>
-__device__ __forceinline__ int64_t load_logits(const char* row, int64_t i, int64_t end, float (&v)[8]) {
+__device__ __forceinline__ int load_logits(const char* row, int i, int end, float (&v)[8]) {
   if (end < 8) {  // the same for the work-group
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] = i + j < end ? load1<ZT>(row, i + j) : kMinusInf;
     return i;
   }
-  const int64_t base = std::min(i, end - 8);
-  const int skip = (int)std::min<int64_t>(i - base, 8);
-  unpack8<ZT>(load8<ZT>(row, base), v);
+  const int base = min(i, end - 8), skip = i - base;
+  unpack8<ZT>(load_run<ZT>(row, base), v);
 #pragma unroll
   for (int j = 0; j < 8; ++j) v[j] = j >= skip ? v[j] : kMinusInf;
   return base;
@@ -126,6 +137,7 @@ struct Candidate {
 template <int THREADS, typename F>
 __device__ __forceinline__ void rank_candidates(const Candidate* s_c, int count, F f) {
   const int whole_waves = (4 * count + 63) & ~63;
+#pragma unroll 1
   for (int e = threadIdx.x; e < whole_waves; e += THREADS) {
     const int i = e >> 2;
     const Candidate me = s_c[min(i, count - 1)];
@@ -145,15 +157,59 @@ __device__ __forceinline__ void rank_candidates(const Candidate* s_c, int count,
   }
 }
 
-// the largest key that at least n of the wave's lanes reach
+// A key that at least n of the wave's lanes reach: the largest such one but for its last 12 bits
 __device__ __forceinline__ uint32_t nth_of_lanes(uint32_t key, int n) {
   uint32_t bound = 0;
 #pragma unroll 1
-  for (int b = 31; b >= 0; --b) {
-    const uint32_t next = bound | 1u << b;
-    if (__popcll(__ballot(key >= next)) >= n) bound = next;
+  for (uint32_t bit = 1u << 31; bit >= 1u << 12; bit >>= 1)
+    if (__popcll(__ballot(key >= (bound | bit))) >= n) bound |= bit;
+  return bound;
+}
+
+// The same over the candidates, PER of them in a lane: every wave finds it for itself
+template <int PER>
+__device__ __forceinline__ uint32_t nth_of_candidates(const Candidate* s_c, int count, int n) {
+  uint32_t key[PER], bound = 0;
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) key[i] = lane + 64 * i < count ? s_c[lane + 64 * i].key : 0u;
+#pragma unroll 1
+  for (uint32_t bit = 1u << 31; bit >= 1u << 12; bit >>= 1) {
+    int many = 0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) many += __popcll(__ballot(key[i] >= (bound | bit)));
+    if (many >= n) bound |= bit;
   }
   return bound;
+}
+// The top_n best of `count` candidates, ranked. Counting takes their number squared: more than a few are
+// first cut to those that reach the top_n-th key (64 x 131072 with 32 alternatives, slices of 8192: 21.5 us
+// and 15.4).
+constexpr int kFew = 64;
+struct Few {
+  Candidate c[kFew];
+  int n;
+};
+template <int THREADS, typename F>
+__device__ __forceinline__ void rank_top(const Candidate* s_c, int count, int top_n, Few& s_few, F f) {
+  if (count > kFew) {
+    const uint32_t bound = count <= 256 ? nth_of_candidates<4>(s_c, count, top_n) : 0u;
+    if (threadIdx.x == 0) s_few.n = 0;
+    __syncthreads();
+#pragma unroll 1
+    for (int i = threadIdx.x; i < count; i += THREADS) {
+      const Candidate me = s_c[i];
+      if (me.key < bound) continue;
+      const int at = atomicAdd(&s_few.n, 1);
+      if (at < kFew) s_few.c[at] = me;
+    }
+    __syncthreads();
+    if (s_few.n <= kFew) {
+      rank_candidates<THREADS>(s_few.c, s_few.n, f);
+      return;
+    }
+  }
+  rank_candidates<THREADS>(s_c, count, f);
 }
 
 // The top_n largest values above -inf of a slice, [begin, end) of a row, whose threads' maxima are `most` and
@@ -165,11 +221,12 @@ struct Top {
   uint16_t list[kNotes * THREADS];
   Candidate c[kCand];
   int n_list, n_c;
+  Few few;
   uint32_t bound[THREADS / 64];
   int before[THREADS / 64 + 1];
 };
 template <int ZT, int THREADS>
-__device__ int find_top(Top<THREADS>& s, const char* row, int64_t begin, int64_t end, float most, int top_n, int iters, int per_note) {
+__device__ int find_top(Top<THREADS>& s, const char* row, int begin, int end, float most, int top_n, int iters, int note_log) {
   constexpr int W = THREADS / 64;
   constexpr uint32_t kNothing = 0x007FFFFFu;  // key_of(-inf)
   const int tid = threadIdx.x, wave = tid >> 6;
@@ -178,29 +235,41 @@ __device__ int find_top(Top<THREADS>& s, const char* row, int64_t begin, int64_t
   __syncthreads();
 #pragma unroll
   for (int w = 0; w < W; ++w) bound = max(bound, s.bound[w]);
-  const int notes = (iters + per_note - 1) / per_note;
-  const int64_t iter_values = (int64_t)THREADS * 8 * kU;
+  const int notes = (iters + (1 << note_log) - 1) >> note_log;
+  constexpr int kIter = THREADS * 8 * kU;
+  auto push = [&](uint32_t t, int i) __attribute__((always_inline)) {
+    float v[8];
+    const int first = load_logits<ZT>(row, i, end, v);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const uint32_t k = key_of(v[j]);
+      if (k < t) continue;
+      const int at = atomicAdd(&s.n_c, 1);
+      if (at < Top<THREADS>::kCand) s.c[at] = Candidate{k, first + j};
+    }
+  };
   // all values of keys >= t, as many as there is room for; returns how many there are
   auto gather = [&](uint32_t t) {
     __syncthreads();
     if (tid == 0) s.n_list = s.n_c = 0;
     __syncthreads();
-    for (int i = 0; i < notes; ++i)
-      if (key_of(s.note[i][tid]) >= t) s.list[atomicAdd(&s.n_list, 1)] = (uint16_t)(i * THREADS + tid);
-    __syncthreads();
-    const int runs = per_note * kU, items = s.n_list * runs;
-    for (int e = tid; e < items; e += THREADS) {
-      const int note = s.list[e / runs], r = e % runs, it = note / THREADS * per_note + r / kU;
-      const int64_t i = begin + it * iter_values + ((int64_t)(r % kU) * THREADS + note % THREADS) * 8;
-      if (i >= end) continue;
-      float v[8];
-      const int first = (int)load_logits<ZT>(row, i, end, v);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const uint32_t k = key_of(v[j]);
-        if (k < t) continue;
-        const int at = atomicAdd(&s.n_c, 1);
-        if (at < Top<THREADS>::kCand) s.c[at] = Candidate{k, first + j};
+    if (iters == 1) {
+      // a thread's values are still in its CU's cache
+      if (key_of(most) >= t) {
+#pragma unroll 1
+        for (int i = begin + tid * 8; i < end; i += THREADS * 8) push(t, i);
+      }
+    } else {
+#pragma unroll 1
+      for (int i = 0; i < notes; ++i)
+        if (key_of(s.note[i][tid]) >= t) s.list[atomicAdd(&s.n_list, 1)] = (uint16_t)(i * THREADS + tid);
+      __syncthreads();
+      const int log = note_log + kULog, items = s.n_list << log;
+#pragma unroll 1
+      for (int e = tid; e < items; e += THREADS) {
+        const int note = s.list[e >> log], r = e & ((1 << log) - 1), it = (note / THREADS << note_log) + r / kU;
+        const int i = begin + it * kIter + ((r % kU) * THREADS + note % THREADS) * 8;
+        if (i < end) push(t, i);
       }
     }
     __syncthreads();
@@ -208,26 +277,32 @@ __device__ int find_top(Top<THREADS>& s, const char* row, int64_t begin, int64_t
   };
   uint32_t t = max(bound, kNothing + 1);
   int count;
+  bool above = false;  // without the values equal to the bound
   for (;;) {
-    count = gather(t);
-    if (count <= Top<THREADS>::kCand) return count;
-    // More than there is room for. Without the values equal to the bound (a mask's lowest value, say)?
-    count = gather(t + 1);
+    count = gather(t + above);
     if (count <= Top<THREADS>::kCand) break;
+    // More than there is room for. Without the values equal to the bound (a mask's lowest value, say)?
+    if (!above) {
+      above = true;
+      continue;
+    }
     // still: the top_n-th largest of those that found room is a higher bound
     rank_candidates<THREADS>(s.c, Top<THREADS>::kCand, [&](const Candidate& me, int rank) {
       if (rank == top_n - 1) s.bound[0] = me.key;
     });
     __syncthreads();
     t = s.bound[0];
+    above = false;
   }
+  if (!above) return count;
   // those above the bound, and of those equal to it the first ones, in order
   for (int it = 0; it < iters && count < top_n; ++it) {
-    if (!__syncthreads_or(key_of(s.note[it / per_note][tid]) >= t)) continue;
+    if (!__syncthreads_or(key_of(iters == 1 ? most : s.note[it >> note_log][tid]) >= t)) continue;
+#pragma unroll 1
     for (int r = 0; r < kU && count < top_n; ++r) {
-      const int64_t i = begin + it * iter_values + ((int64_t)r * THREADS + tid) * 8;
+      const int i = begin + it * kIter + (r * THREADS + tid) * 8;
       float v[8];
-      const int first = (int)load_logits<ZT>(row, i, end, v);
+      const int first = load_logits<ZT>(row, i, end, v);
       int mine = 0;
 #pragma unroll
       for (int j = 0; j < 8; ++j) mine += key_of(v[j]) == t;
@@ -261,9 +336,9 @@ __device__ int find_top(Top<THREADS>& s, const char* row, int64_t begin, int64_t
 
 // One work-group per row or slice, in turn. TOP: the largest are asked for.
 template <int ZT, int THREADS, bool TOP>
-__global__ __launch_bounds__(THREADS) void logprob_rows_kernel(LogprobArgs a) {
+__global__ __launch_bounds__(THREADS, TOP ? 4 : ZT == MOE_F32 ? 6 : 8) void logprob_rows_kernel(LogprobArgs a) {
   constexpr int W = THREADS / 64;
-  constexpr int64_t kIter = (int64_t)THREADS * 8 * kU;
+  constexpr int kIter = THREADS * 8 * kU;
   __shared__ Top<TOP ? THREADS : 64> s_top;
   __shared__ Sums s_sum[W];
   __shared__ float s_most[W];
@@ -273,44 +348,65 @@ __global__ __launch_bounds__(THREADS) void logprob_rows_kernel(LogprobArgs a) {
     const int64_t row = item / a.slices;
     const int slice = (int)(item - row * a.slices);
     const char* z = static_cast<const char*>(a.logits) + row * a.z_stride * value_size<ZT>();
-    const int64_t begin = slice * a.slice, end = std::min<int64_t>(begin + a.slice, a.V);
-    const int iters = (int)((end - begin + kIter - 1) / kIter);
+    const int begin = slice * (int)a.slice, end = min(begin + (int)a.slice, (int)a.V);
+    const int iters = (end - begin + kIter - 1) / kIter;
     Sums t{kLowest, 0.f, 0.f};
     float most = kMinusInf, noted = kMinusInf;
-    for (int it = 0; it < iters; ++it) {
-      const int64_t at = begin + it * kIter + tid * 8;
-      float v[kU][8];
-      if (begin + (it + 1) * kIter <= end) {
-        Raw8<ZT> raw[kU];
+    Raw8<ZT> raw[kU];
+    auto fetch = [&](int at) __attribute__((always_inline)) {
 #pragma unroll
-        for (int r = 0; r < kU; ++r) raw[r] = load8<ZT>(z, at + r * THREADS * 8);
-#pragma unroll
-        for (int r = 0; r < kU; ++r) unpack8<ZT>(raw[r], v[r]);
-      } else {
-#pragma unroll
-        for (int r = 0; r < kU; ++r) load_logits<ZT>(z, at + r * THREADS * 8, end, v[r]);
-      }
+      for (int r = 0; r < kU; ++r) raw[r] = load_run<ZT>(z, at + r * THREADS * 8);
+    };
+    // maximum and sums of the first `runs` runs of v
+    auto add = [&](const float (&v)[kU][8], int runs) __attribute__((always_inline)) {
       float m = kMinusInf;
 #pragma unroll
-      for (int r = 0; r < kU; ++r)
+      for (int r = 0; r < kU; ++r) {
+        if (r >= runs) break;
 #pragma unroll
         for (int j = 0; j < 8; ++j) m = fmaxf(m, v[r][j]);
-      if constexpr (TOP) {
-        most = fmaxf(most, m);
-        noted = fmaxf(noted, m);
-        if ((it + 1) % a.per_note == 0 || it + 1 == iters) s_top.note[it / a.per_note][tid] = noted, noted = kMinusInf;
-      } else {
-        most = fmaxf(most, m);
       }
+      most = fmaxf(most, m);
+      noted = fmaxf(noted, m);
       refer(t, fmaxf(t.m, m), c);
 #pragma unroll
-      for (int r = 0; r < kU; ++r)
+      for (int r = 0; r < kU; ++r) {
+        if (r >= runs) break;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           const float d = (v[r][j] - t.m) * c, e = __builtin_amdgcn_exp2f(d);
           t.s += e;
           t.u = fmaf(e, fmaxf(d, kFloor), t.u);
         }
+      }
+    };
+    auto note = [&](int it) __attribute__((always_inline)) {
+      if constexpr (TOP)
+        if (((it + 1) & ((1 << a.note_log) - 1)) == 0 || it + 1 == iters) {
+          s_top.note[it >> a.note_log][tid] = noted;
+          noted = kMinusInf;
+        }
+    };
+    const int whole = (end - begin) / kIter;
+    if (whole) fetch(begin + tid * 8);
+    int it = 0;
+#pragma unroll 1
+    for (; it < whole; ++it) {
+      float v[kU][8];
+#pragma unroll
+      for (int r = 0; r < kU; ++r) unpack8<ZT>(raw[r], v[r]);
+      // the next values on their way, those of the last ones again behind them
+      fetch(begin + min(it + 1, whole - 1) * kIter + tid * 8);
+      add(v, kU);
+      note(it);
+    }
+    if (it < iters) {
+      float v[kU][8];
+      const int at = begin + it * kIter;
+#pragma unroll
+      for (int r = 0; r < kU; ++r) load_logits<ZT>(z, at + (r * THREADS + tid) * 8, end, v[r]);
+      add(v, (end - at + THREADS * 8 - 1) / (THREADS * 8));
+      note(it);
     }
     // over the lanes, then the waves in their order
     float m = t.m;
@@ -349,8 +445,8 @@ __global__ __launch_bounds__(THREADS) void logprob_rows_kernel(LogprobArgs a) {
       float* out = a.slices == 1 ? a.top_logp + row * a.top_n : a.slice_values + item * a.top_n;
       // the same for the whole work-group
       const bool none = r.bad || (a.slices == 1 && r.none);
-      const int count = none ? 0 : find_top<ZT, THREADS>(s_top, z, begin, end, most, a.top_n, iters, a.per_note);
-      rank_candidates<THREADS>(s_top.c, count, [&](const Candidate& me, int rank) {
+      const int count = none ? 0 : find_top<ZT, THREADS>(s_top, z, begin, end, most, a.top_n, iters, a.note_log);
+      rank_top<THREADS>(s_top.c, count, a.top_n, s_top.few, [&](const Candidate& me, int rank) {
         if (rank >= a.top_n) return;
         const float x = route_dev::order_logit(me.key);
         ids[rank] = me.id;
@@ -368,6 +464,7 @@ template <int ZT>
 __global__ __launch_bounds__(kFinish) void logprob_finish_kernel(LogprobArgs a) {
   constexpr int kCand = kMaxSlices * kMaxTop;
   __shared__ Candidate s_c[kCand];
+  __shared__ Few s_few;
   __shared__ int s_n;
   const int64_t row = blockIdx.x;
   const int tid = threadIdx.x, lane = tid & 63;
@@ -388,20 +485,33 @@ __global__ __launch_bounds__(kFinish) void logprob_finish_kernel(LogprobArgs a) 
   if (!a.top_n) return;
   if (tid == 0) s_n = 0;
   __syncthreads();
-  // The slices' lists are in order. With `deep` = top_n / slices, rounded up: where top_n / deep slices, rounded up,
-  // have their deep-th value at a bound or above it, top_n values reach it.
+  // The slices' lists are in order: where top_n / deep slices, rounded up, have their deep-th value at a bound or
+  // above it, top_n values reach it. The first depth at which half of the slices are enough, for the best of
+  // few values would be a bound of none.
   const int64_t lists = row * a.slices * a.top_n;
-  const int deep = (a.top_n + a.slices - 1) / a.slices;
-  const uint32_t bound = nth_of_lanes(in ? key_of(a.slice_values[lists + lane * a.top_n + deep - 1]) : 0u, (a.top_n + deep - 1) / deep);
+  int deep = 1;
+  while (deep < a.top_n && 2 * ((a.top_n + deep - 1) / deep) > a.slices) deep *= 2;
+  deep = min(deep, a.top_n);
+  const uint32_t mine = in ? key_of(a.slice_values[lists + lane * a.top_n + deep - 1]) : 0u;
   const int n = r.bad || r.none ? 0 : a.slices * a.top_n;
-  for (int i = tid; i < n; i += kFinish) {
-    const int id = a.slice_ids[lists + i];
-    const uint32_t key = key_of(a.slice_values[lists + i]);
-    if (id >= 0 && key >= bound) s_c[atomicAdd(&s_n, 1)] = Candidate{key, id};
+  constexpr int kMine = kCand / kFinish;
+  float value[kMine];
+  int id[kMine];
+#pragma unroll
+  for (int i = 0; i < kMine; ++i) {
+    const int e = tid + kFinish * i;
+    if (kFinish * i < n) value[i] = a.slice_values[lists + min(e, n - 1)], id[i] = a.slice_ids[lists + min(e, n - 1)];
+  }
+  const uint32_t bound = nth_of_lanes(mine, (a.top_n + deep - 1) / deep);
+#pragma unroll
+  for (int i = 0; i < kMine; ++i) {
+    if (kFinish * i >= n) break;
+    const uint32_t key = key_of(value[i]);
+    if (tid + kFinish * i < n && id[i] >= 0 && key >= bound) s_c[atomicAdd(&s_n, 1)] = Candidate{key, id[i]};
   }
   __syncthreads();
   const int count = s_n;
-  rank_candidates<kFinish>(s_c, count, [&](const Candidate& me, int rank) {
+  rank_top<kFinish>(s_c, count, a.top_n, s_few, [&](const Candidate& me, int rank) {
     if (rank >= a.top_n) return;
     a.top_ids[row * a.top_n + rank] = me.id;
     a.top_logp[row * a.top_n + rank] = row_logp(r, route_dev::order_logit(me.key), a.scale);
@@ -477,8 +587,8 @@ __global__ __launch_bounds__(THREADS) void logprob_grad_kernel(LogprobGradArgs a
 }
 
 int slices_of(int64_t T, int64_t V) {
-  if (V <= kWaveRow || T >= kSliceTarget || T < 1) return 1;
-  const int64_t want = std::min<int64_t>((kSliceTarget + T - 1) / T, kMaxSlices);
+  if (V <= kWaveRow || T < 1) return 1;
+  const int64_t want = std::max<int64_t>(1, std::min<int64_t>(kSliceTarget / T, kMaxSlices));
   const int64_t slice = ((V + want - 1) / want + kSliceStep - 1) / kSliceStep * kSliceStep;
   return (int)((V + slice - 1) / slice);
 }
@@ -494,7 +604,8 @@ hipError_t launch_types(LogprobArgs a, hipStream_t s) {
   a.slices = slices_of(a.T, a.V);
   a.slice = a.slices == 1 ? a.V : ((a.V + a.slices - 1) / a.slices + kSliceStep - 1) / kSliceStep * kSliceStep;
   const int64_t per_iter = (int64_t)threads * 8 * kU, iters = (a.slice + per_iter - 1) / per_iter;
-  a.per_note = (int)((iters + kNotes - 1) / kNotes);
+  for (a.note_log = 0; iters > (int64_t)kNotes << a.note_log; ++a.note_log) {
+  }
   if (a.slices > 1) {
     const int64_t items = a.T * a.slices;
     a.sums = reinterpret_cast<float*>(a.ws);
@@ -519,10 +630,10 @@ hipError_t launch_grad_types(const LogprobGradArgs& a, hipStream_t s) {
 
 }  // namespace
 
-// Rows are cut into slices below kSliceTarget of them: at most twice that many slices in all. Never less for more rows.
+// Never less for more rows: up to kSliceTarget slices in all
 int64_t logprob_workspace_bytes(int64_t T, int64_t V, int top_n) {
   if (V <= kWaveRow || T < 1) return 0;
-  const int64_t items = std::min<int64_t>(T * kMaxSlices, 2 * kSliceTarget);
+  const int64_t items = std::min<int64_t>(T * kMaxSlices, kSliceTarget);
   return items * (16 + 8 * (int64_t)top_n);
 }
 
