@@ -368,9 +368,10 @@ struct LogprobGradArgs {
   void* dlogits;
   int64_t z_stride, d_stride, T, V;
   int32_t z_type, d_type, accumulate;
+  int32_t past;  // of the launch: dlogits past the caches
   float scale;
 };
-hipError_t launch_logprobs_grad(const LogprobGradArgs& a, hipStream_t s);
+hipError_t launch_logprobs_grad(LogprobGradArgs a, hipStream_t s);
 
 // dense_q4.hip, dense_q4_linear.hip
 struct Q4Epilogue {           // y = act(product + bias) * mul + res; nullptr: left out

@@ -86,8 +86,10 @@ __device__ __forceinline__ void unpack8(const Raw8<TYPE>& r, float (&v)[8]) {
     }
   }
 }
-template <int TYPE>
+// PAST: past the caches, for outputs that they cannot hold anyway
+template <int TYPE, bool PAST = false>
 __device__ __forceinline__ void store8(void* p, int64_t i, const float (&v)[8]) {
+  typedef uint32_t loose_t __attribute__((ext_vector_type(4), aligned(2)));
   char* q = static_cast<char*>(p) + i * value_size<TYPE>();
   u32x4_t a, b;
 #pragma unroll
@@ -100,6 +102,11 @@ __device__ __forceinline__ void store8(void* p, int64_t i, const float (&v)[8]) 
       const uint32_t hi = TYPE == MOE_F16 ? float_to_half(v[2 * j + 1]) : float_to_bf16(v[2 * j + 1]);
       a[j] = lo | hi << 16;
     }
+  }
+  if constexpr (PAST) {
+    __builtin_nontemporal_store(loose_t(a), reinterpret_cast<loose_t*>(q));
+    if constexpr (TYPE == MOE_F32) __builtin_nontemporal_store(loose_t(b), reinterpret_cast<loose_t*>(q + 16));
+    return;
   }
   __builtin_memcpy(q, &a, 16);
   if constexpr (TYPE == MOE_F32) __builtin_memcpy(q + 16, &b, 16);

@@ -272,6 +272,42 @@ def test_token_logprobs_grad(T, V, zt, dt, parts, banned, scale):
         assert torch.equal(z, first)
 
 
+@pytest.mark.parametrize("T,V,zt,dt", [(520, 65537, "bf16", "bf16"), (270, 65537, "f32", "f32"), (40, 500000, "f16", "f32")])
+def test_gradient_larger_than_the_caches(T, V, zt, dt):
+    """64 MB and more of dlogits, rows that begin anywhere: against the formula row by row, into its own memory, onto
+    what is there, and in place."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(T)
+    z = (3 * torch.randn((T, V), generator=g, device="cuda")).to(TYPES[zt])
+    targets = torch.randint(0, V, (T,), generator=g, device="cuda", dtype=torch.int32)
+    targets[:3] = torch.tensor([0, V - 1, -1], dtype=torch.int32)
+    a, b = torch.randn(T, generator=g, device="cuda"), torch.randn(T, generator=g, device="cuda")
+    H, lse = torch.empty(T, device="cuda"), torch.empty((T, 2), device="cuda")
+    moe.moe_token_logprobs(z, entropy=H, lse=lse)
+    d = torch.full((T, V + 1), 7.0, dtype=TYPES[dt], device="cuda")[:, :V]
+    kw = dict(targets=targets, dlogp=a, entropy=H, dentropy=b)
+    moe.moe_token_logprobs_grad(z, lse, d, **kw)
+    more = torch.ones((T, V), dtype=TYPES[dt], device="cuda")
+    moe.moe_token_logprobs_grad(z, lse, more, flags=moe.MOE_ACCUMULATE, **kw)
+    for t in range(0, T, 37):
+        lp = torch.log_softmax(z[t].double(), dim=0)
+        p, h = lp.exp(), -(lp.exp() * lp).sum()
+        at = a[t].double() if targets[t] >= 0 else torch.zeros((), dtype=torch.float64, device="cuda")
+        want = -p * (at + b[t].double() * (lp + h))
+        if targets[t] >= 0:
+            want[targets[t]] += at
+        s, hb = bounds(lp[None], V)
+        mag = p * (at.abs() + b[t].double().abs() * (lp.abs() + h))
+        tol = mag * (s + E * (3 * lp.abs() + 12)) + p * b[t].double().abs() * (s + hb + 4 * E * h) + 3 * E * at.abs() * (want.abs() > 0)
+        tol = (tol + u(TYPES[dt]) * want.abs()) * 1.01 + smallest(TYPES[dt])
+        assert ((d[t].double() - want).abs() <= tol).all()
+        assert ((more[t].double() - (want + 1)).abs() <= tol + (u(TYPES[dt]) + E) * 1.01 * ((want + 1).abs() + tol)).all()
+    assert (d.as_strided((T,), (V + 1,), V) == 7).all()
+    if zt == dt:
+        moe.moe_token_logprobs_grad(z, lse, z, **kw)
+        assert torch.equal(z, d)
+
+
 def test_gradient_against_differences():
     """Central differences of the forward call, step 2^-6: h^2 / 6 times third derivatives below 1, roundings over the step."""
     g = rng_of(46)
