@@ -567,7 +567,7 @@ MOE_API int moe_q4_linear(int32_t device, void* stream, int32_t n_tokens, int32_
  * several axes (n_axes 1..8: time, height, width of a video, say): axis(i) =
  * pair_axis[i] (uint8 [rotary_dim / 2] on the device, NULL: 0 for all; a pair whose
  * axis is n_axes or more is not turned). positions int32 [n_axes][n_tokens], rows
- * pos_stride apart, any sign; inv_freq fp32 [rotary_dim / 2]. The angle is formed
+ * pos_stride apart (0: one row for all), any sign; inv_freq fp32 [rotary_dim / 2]. The angle is formed
  * in 64 bits, so it is exact for every position. rotary_dim is even, 0..head_dim;
  * 0: the norm alone, with inv_freq and positions NULL. MOE_NO_NORM: the rotation
  * alone, with both weights NULL.
@@ -617,7 +617,7 @@ MOE_API int moe_qk_norm_rope_grad(int32_t device, void* stream, int32_t n_tokens
 MOE_API int64_t moe_qk_norm_rope_grad_workspace_bytes(int32_t n_tokens, int32_t q_heads, int32_t k_heads, int32_t head_dim);
 
 /* What the output head says of each token. For logits [n_tokens][n_vocab] (MOE_F32,
- * MOE_F16 or MOE_BF16), z = scale * logits (an inverse temperature, > 0 and finite):
+ * MOE_F16 or MOE_BF16), z = scale * logits (an inverse temperature, 2^-64..2^64):
  *   p[t] = softmax(z[t]), lse[t] = log sum exp(z[t])
  *   logp[t]    = log p[t][targets[t]]     (0 where the target is not in 0..n_vocab-1)
  *   entropy[t] = -sum_j p[t][j] log p[t][j]

@@ -385,7 +385,8 @@ def _stream_of(stream, dev):
 
 def _rows(name, t, dev, shape):
     """(type code, address, row stride) of a 2-d tensor whose rows are contiguous runs of values."""
-    if t.shape != shape or t.get_device() != dev or dev < 0 or t.dtype not in _types:
+    code = _types.get(t.dtype)
+    if code is None or t.shape != shape or t.get_device() != dev or dev < 0:
         raise ValueError(f"{name}: {t.dtype} {tuple(t.shape)} on {t.device}; fp32, fp16, bf16 or int8 of shape "
                          f"{tuple(shape)} on cuda device {max(dev, 0)} is needed")
     stride, step = t.stride()
@@ -394,7 +395,7 @@ def _rows(name, t, dev, shape):
         if (step != 1 and width > 1) or (stride < width and shape[0] > 1):
             raise ValueError(f"{name}: rows must be contiguous and must not overlap, strides {t.stride()}")
         stride = max(stride, width)
-    return _types[t.dtype], t.data_ptr(), stride
+    return code, t.data_ptr(), stride
 
 
 def _flat(name, t, dev, shape, dtype):
@@ -566,7 +567,8 @@ def moe_q4_linear(x, nibbles, w_scales, y, bias=None, act: int = MOE_ACT_NONE, m
 
 def _heads(name, t, dev, shape):
     """(type code, address, stride of tokens, stride of heads) of a tensor [T][heads][head_dim]."""
-    if t.shape != shape or t.get_device() != dev or dev < 0 or t.dtype not in _types:
+    code = _types.get(t.dtype)
+    if code is None or t.shape != shape or t.get_device() != dev or dev < 0:
         raise ValueError(f"{name}: {t.dtype} {tuple(t.shape)} on {t.device}; fp32, fp16 or bf16 of shape "
                          f"{tuple(shape)} on cuda device {max(dev, 0)} is needed")
     stride, head, step = t.stride()
@@ -574,7 +576,7 @@ def _heads(name, t, dev, shape):
     if step != 1:
         raise ValueError(f"{name}: the values of a head must be contiguous, strides {t.stride()}")
     # a stride that is never taken may be anything in torch
-    return _types[t.dtype], t.data_ptr(), stride if T > 1 else max(stride, D), head if H > 1 else D
+    return code, t.data_ptr(), stride if T > 1 else max(stride, D), head if H > 1 else D
 
 
 _NO_HEADS = (MOE_F32, None, 0, 0)
@@ -597,7 +599,7 @@ def _rope(T, D, dev, inv_freq, positions, pair_axis):
             or not 1 <= axes <= 8 or (positions.stride(-1) != 1 and T > 1)):
         raise ValueError(f"positions: {positions.dtype} {tuple(positions.shape)} on {positions.device}; int32 [tokens] or "
                          f"[axes][tokens], {T} tokens in a row, on cuda device {max(dev, 0)} is needed")
-    return (2 * n, fp, positions.data_ptr(), max(positions.stride(0), T) if axes > 1 else T, axes,
+    return (2 * n, fp, positions.data_ptr(), positions.stride(0) if axes > 1 else T, axes,
             _flat("pair_axis", pair_axis, dev, (n,), "torch.uint8"))
 
 

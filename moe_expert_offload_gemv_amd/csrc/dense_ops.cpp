@@ -216,8 +216,9 @@ int heads_common(const char* me, int32_t n_tokens, int32_t q_heads, int32_t k_he
   REFUSE(rotary_dim == 0 && (inv_freq || positions || pair_axis), "%s: positions or inv_freq without rotary_dim", me);
   REFUSE(rotary_dim && (n_axes < 1 || n_axes > 8), "%s: n_axes %d", me, n_axes);
   REFUSE(rotary_dim && (!inv_freq || !aligned(inv_freq, 4)), "%s: inv_freq null or unaligned", me);
-  REFUSE(rotary_dim && n_tokens > 0 && (!rows_ok(positions, MOE_F32, n_tokens, pos_stride)),
-         "%s: positions null, unaligned or their stride below n_tokens", me);
+  // rows of positions are read alone: they may be one and the same
+  REFUSE(rotary_dim && n_tokens > 0 && (!positions || !aligned(positions, 4)), "%s: positions null or unaligned", me);
+  REFUSE(rotary_dim && n_axes > 1 && (pos_stride < 0 || pos_stride > (int64_t)1 << 36), "%s: stride of positions", me);
   REFUSE(!aligned(q_weight, 4) || (k_heads && !aligned(k_weight, 4)), "%s: weights unaligned", me);
   REFUSE(!value_type(x_type), "%s: bad type of q and k", me);
   a->q.weight = q_weight, a->k.weight = k_weight, a->q.H = q_heads, a->k.H = k_heads;
@@ -343,7 +344,7 @@ extern "C" int moe_token_logprobs(int32_t device, void* stream, int32_t n_tokens
   const int64_t need = moe_token_logprobs_workspace_bytes(n_tokens, n_vocab, top_n);
   REFUSE(need < 0, "%s: n_tokens %d, n_vocab %d or top_n %d out of range", me, n_tokens, n_vocab, top_n);
   REFUSE(!value_type(z_type), "%s: bad type of the logits", me);
-  REFUSE(!(scale > 0.f && scale <= 3.4028235e38f), "%s: scale %g", me, scale);
+  REFUSE(!(scale >= 0x1p-64f && scale <= 0x1p64f), "%s: scale %g out of range", me, scale);
   if (n_tokens > 0) {
     REFUSE(!rows_ok(logits, z_type, n_vocab, z_stride), "%s: logits null, unaligned or their stride below n_vocab", me);
     REFUSE((targets == nullptr) != (logp == nullptr), "%s: targets and logp go together", me);
@@ -373,7 +374,7 @@ extern "C" int moe_token_logprobs_grad(int32_t device, void* stream, int32_t n_t
   REFUSE(n_tokens < 0 || n_tokens > kMaxTokens || n_vocab < 1 || n_vocab > kMaxOut, "%s: n_tokens %d or n_vocab %d out of range",
          me, n_tokens, n_vocab);
   REFUSE(!value_type(z_type) || !value_type(d_type), "%s: bad type of the logits or dlogits", me);
-  REFUSE(!(scale > 0.f && scale <= 3.4028235e38f), "%s: scale %g", me, scale);
+  REFUSE(!(scale >= 0x1p-64f && scale <= 0x1p64f), "%s: scale %g out of range", me, scale);
   REFUSE(flags & ~MOE_ACCUMULATE, "%s: unknown flags", me);
   if (n_tokens > 0) {
     REFUSE(!rows_ok(logits, z_type, n_vocab, z_stride), "%s: logits null, unaligned or their stride below n_vocab", me);

@@ -166,6 +166,23 @@ def test_far_positions():
     assert ((y.double() - ref).abs() <= 2 * (TURN + 2.0 ** -22 * (pos.double().abs() > 2 ** 25)[:, None, None])).all()
 
 
+def test_one_row_of_positions_for_all_axes():
+    """Positions of text in a model with several axes: one row, expanded (stride 0), or rows of a wider table."""
+    T, D = 7, 24
+    g = rng_of(50)
+    x, _ = head_tensor(g, T, 2, D, torch.float32, "own")
+    pos = torch.from_numpy(g.integers(0, 1000, T)).int().cuda()
+    inv = torch.from_numpy(100.0 ** (-np.arange(0, D, 2) / D)).float().cuda()
+    axis = torch.from_numpy(g.integers(0, 3, D // 2)).to(torch.uint8).cuda()
+    want, y = torch.empty_like(x), torch.empty_like(x)
+    moe.moe_qk_norm_rope(x, None, want, None, inv_freq=inv, positions=pos)
+    wide = torch.full((3, 50), 1 << 30, dtype=torch.int32, device="cuda")
+    wide[:, 5:5 + T] = pos
+    for p in (pos.expand(3, T), wide[:, 5:5 + T], pos[None]):
+        moe.moe_qk_norm_rope(x, None, y, None, inv_freq=inv, positions=p, pair_axis=axis if len(p) > 1 else None)
+        assert torch.equal(y, want)
+
+
 def test_axes_that_do_not_exist_are_not_turned():
     T, D = 4, 16
     g = rng_of(34)

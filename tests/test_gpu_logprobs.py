@@ -218,6 +218,24 @@ def test_logits_far_from_zero(scale):
     assert ((ds[0] - ds[1]).abs() <= scale * lp.exp() * (8 + 4 * lp.abs()) * E + scale * 2 * E).all()
 
 
+@pytest.mark.parametrize("power", [64, -64])
+@pytest.mark.parametrize("T,V", [(3, 900), (2, 30000)])
+def test_scales_at_their_limits(power, T, V):
+    """Powers of two: exact, so logits times 2^-power say the same with a scale of 2^power."""
+    g = rng_of(49, V)
+    z = torch.from_numpy(logits_of(g, T, V)).float().cuda()
+    far = z * 2.0 ** -power
+    targets = torch.zeros(T, dtype=torch.int32, device="cuda")
+    outs = []
+    for x, scale in ((z, 1.0), (far, 2.0 ** power)):
+        o = Out(T, V, 9, z)
+        moe.moe_token_logprobs(x, targets=targets, logp=o.logp, entropy=o.entropy, lse=o.lse, top_ids=o.ids, top_logp=o.alt, scale=scale)
+        d = torch.empty_like(z)
+        moe.moe_token_logprobs_grad(x, o.lse, d, targets=targets, dlogp=o.logp, entropy=o.entropy, dentropy=o.logp, scale=scale)
+        outs.append(o.all() + [d / scale])
+    assert all(torch.equal(a, b) for a, b in zip(*outs))
+
+
 # ---------------------------------------------------------------------------
 # gradient
 

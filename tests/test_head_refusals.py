@@ -56,7 +56,8 @@ COMMON = [
     (dict(rotary_dim=7), "rotary_dim"), (dict(rotary_dim=18), "rotary_dim"), (dict(rotary_dim=-2), "rotary_dim"),
     (dict(eps=-1.0), "eps"), (dict(eps=float("nan")), "eps"), (dict(rotary_dim=0), "without rotary_dim"),
     (dict(n_axes=0), "n_axes"), (dict(n_axes=9), "n_axes"), (dict(inv_freq=None), "inv_freq"), (dict(inv_freq=5 * P + 2), "inv_freq"),
-    (dict(positions=None), "positions"), (dict(positions=6 * P + 2), "positions"), (dict(pos_stride=4), "positions"),
+    (dict(positions=None), "positions"), (dict(positions=6 * P + 2), "positions"), (dict(n_axes=2, pos_stride=-1), "positions"),
+    (dict(n_axes=2, pos_stride=(1 << 36) + 1), "positions"),
     (dict(q_weight=3 * P + 2), "weights"), (dict(k_weight=4 * P + 1), "weights"), (dict(x_type=moe.MOE_Q8_32), "type of q"),
     (dict(q=None), "q "), (dict(q=P + 1), "q "), (dict(q_stride=15), "q "), (dict(q_head_stride=15), "q "), (dict(q_stride=63), "overlap"),
     (dict(k=None), "k "), (dict(k_stride=31), "overlap"), (dict(k_head_stride=8), "overlap"), (dict(flags=16), "flags"),
@@ -105,7 +106,8 @@ def test_workspaces_of_larger_batches_serve_smaller_ones():
     (dict(n_tokens=-1), "out of range"), (dict(n_tokens=(1 << 24) + 1), "out of range"), (dict(n_vocab=0), "out of range"),
     (dict(n_vocab=(1 << 22) + 1), "out of range"), (dict(top_n=-1), "out of range"), (dict(top_n=33), "out of range"),
     (dict(n_vocab=2, z_stride=2), "out of range"), (dict(z_type=3), "type"), (dict(scale=0.0), "scale"), (dict(scale=-1.0), "scale"),
-    (dict(scale=float("inf")), "scale"), (dict(scale=float("nan")), "scale"), (dict(logits=None), "logits null"),
+    (dict(scale=float("inf")), "scale"), (dict(scale=float("nan")), "scale"), (dict(scale=2.0 ** 65), "scale"), (dict(scale=2.0 ** -65), "scale"),
+    (dict(logits=None), "logits null"),
     (dict(logits=P + 1), "unaligned"), (dict(z_stride=4999), "stride"), (dict(targets=None), "together"), (dict(logp=None), "together"),
     (dict(top_ids=None), "top_n"), (dict(top_logp=None), "top_n"), (dict(top_n=0), "top_n"), (dict(entropy=4 * P + 2), "unaligned"),
     (dict(lse=5 * P + 1), "unaligned"), (dict(workspace=None), "workspace"), (dict(workspace=8 * P + 64), "workspace"),
