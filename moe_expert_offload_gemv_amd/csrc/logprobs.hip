@@ -19,10 +19,14 @@
 // values: a token's rank counts equal ones of lower id, so ties go to the lower id whatever
 // the order in which the values were found.
 //
-// Measured (as nodes of a graph): 4096 x 65537 bf16, 537 MB, 124 us = 4.3 TB/s, its gradient, 1074 MB, 212 = 5.1 TB/s, the
-// rate of a copy; 4096 x 32000 fp32 91 = 5.8 TB/s; 301 x 131072 bf16 with 8 alternatives 26 (floor 15: finding
-// them takes 5, the finishing launch 5); 1 x 65537 fp32 with 20, 13.7: two launches of a few dependent
-// trips to memory and LDS each, 3.6 and 2.4 without alternatives.
+// Measured (as nodes of a graph): 4096 x 65537 bf16, 537 MB, 124 us = 4.3 TB/s, with its gradient, 1074 MB more, 313 = 5.1
+// TB/s; 4096 x 32000 fp32 90 = 5.8 TB/s; 301 x 131072 bf16 with 8 alternatives 26.5 (floor 15: finding them takes 5, the
+// finishing launch 5); 4096 x 8000 bf16 18, with 20 alternatives 40 (to find them is four times the work of the
+// sums there: a bound, a second look and ranks for 8000 values); 1 x 65537 fp32 with 20, 12.6: two launches of a few dependent
+// trips to memory and LDS each, 5.4 without alternatives.
+// Measured and not kept: the search by one wave of the work-group (1 x 65537 with 20: 18); an atomic for all hits of
+// a thread at once (4096 x 8000: 55 against 45, the compiler's scan over the lanes); loads past the caches (4096 x 32000
+// fp32 97 against 91).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -157,13 +161,25 @@ __device__ __forceinline__ void rank_candidates(const Candidate* s_c, int count,
   }
 }
 
-// A key that at least n of the wave's lanes reach: the largest such one but for its last 12 bits
+// A key that at least n of the wave's lanes reach: the largest such one but for its last 16 bits
 __device__ __forceinline__ uint32_t nth_of_lanes(uint32_t key, int n) {
   uint32_t bound = 0;
 #pragma unroll 1
-  for (uint32_t bit = 1u << 31; bit >= 1u << 12; bit >>= 1)
+  for (uint32_t bit = 1u << 31; bit >= 1u << 16; bit >>= 1)
     if (__popcll(__ballot(key >= (bound | bit))) >= n) bound |= bit;
   return bound;
+}
+
+__device__ __forceinline__ float wave_max(float v) {
+  using namespace route_dev;
+  v = fmaxf(v, __uint_as_float(dpp32<kDppQuadXor1>(__float_as_uint(v))));
+  v = fmaxf(v, __uint_as_float(dpp32<kDppQuadXor2>(__float_as_uint(v))));
+  v = fmaxf(v, __uint_as_float(dpp32<kDppRowHalfMirror>(__float_as_uint(v))));
+  v = fmaxf(v, __uint_as_float(dpp32<kDppRowMirror>(__float_as_uint(v))));
+  const int u = __float_as_int(v);
+  const float a = __int_as_float(__builtin_amdgcn_readlane(u, 0)), b = __int_as_float(__builtin_amdgcn_readlane(u, 16));
+  const float c = __int_as_float(__builtin_amdgcn_readlane(u, 32)), d = __int_as_float(__builtin_amdgcn_readlane(u, 48));
+  return fmaxf(fmaxf(a, b), fmaxf(c, d));
 }
 
 // The same over the candidates, PER of them in a lane: every wave finds it for itself
@@ -409,15 +425,11 @@ __global__ __launch_bounds__(THREADS, TOP ? 4 : ZT == MOE_F32 ? 6 : 8) void logp
       note(it);
     }
     // over the lanes, then the waves in their order
-    float m = t.m;
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor(m, o, 64));
+    float m = wave_max(t.m);
     refer(t, m, c);
     t.s = route_dev::wave_sum(t.s);
     t.u = route_dev::wave_sum(t.u);
-    float wave_most = most;
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) wave_most = fmaxf(wave_most, __shfl_xor(wave_most, o, 64));
+    float wave_most = wave_max(most);
     if constexpr (W > 1) {
       __syncthreads();  // the item before has been read
       if ((tid & 63) == 0) s_sum[tid >> 6] = t, s_most[tid >> 6] = wave_most;
@@ -474,9 +486,7 @@ __global__ __launch_bounds__(kFinish) void logprob_finish_kernel(LogprobArgs a) 
   const float* p = a.sums + 4 * (row * a.slices + std::min(lane, a.slices - 1));
   const bool in = lane < a.slices;
   Sums t{p[0], in ? p[1] : 0.f, in ? p[2] : 0.f};
-  float most = p[3], m = t.m;
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor(m, o, 64)), most = fmaxf(most, __shfl_xor(most, o, 64));
+  const float most = wave_max(p[3]), m = wave_max(t.m);
   refer(t, m, c);
   t.s = route_dev::wave_sum(t.s);
   t.u = route_dev::wave_sum(t.u);
