@@ -451,3 +451,23 @@ def test_binding_refusals():
         moe.moe_qk_norm_rope_grad(q, k, gq, gk, dq, dk, dq_weight=dw, workspace=ws[:256], **ok)
     with pytest.raises(moe.MoeError, match="overlap"):
         moe.moe_qk_norm_rope_grad(q, k, gq, gk, dq, dk, dq_weight=dw, dk_weight=dw, workspace=ws, **ok)
+
+
+def test_gradient_of_work_groups_that_take_several_turns():
+    """One head of 512 per token: a work-group's angles are those of 16 tokens, and there are more sixteens than work-groups."""
+    T, D = 40003, 512
+    g = torch.Generator(device="cuda")
+    g.manual_seed(51)
+    x = torch.randn((T, 1, D), generator=g, device="cuda").bfloat16()
+    gr = torch.randn((T, 1, D), generator=g, device="cuda").bfloat16()
+    w = 1 + 0.1 * torch.randn(D, generator=g, device="cuda")
+    rope = Rope(T, D, D, g=rng_of(51))
+    y, dx, dw = torch.empty_like(x), torch.empty_like(x), torch.empty(D, device="cuda")
+    moe.moe_qk_norm_rope(x, None, y, None, q_weight=w, eps=EPS, **rope.kw)
+    moe.moe_qk_norm_rope_grad(x, None, gr, None, dx, None, q_weight=w, dq_weight=dw, eps=EPS, **rope.kw)
+    v, _ = normed(x.double(), w.double())
+    ref = turned(v, rope.angle, D, False)
+    assert ((y.double() - ref).abs() <= (partner(v, D, False) * (NORM + TURN) + u(torch.bfloat16) * ref.abs()) * 1.01 + 1e-40).all()
+    want, wantw, mag, wmag = grad_ref(x.double(), w.double(), gr.double(), rope.angle, D, False)
+    assert ((dx.double() - want).abs() <= (mag * (2 * NORM + TURN + 30 * E) + u(torch.bfloat16) * want.abs()) * 1.01 + 1e-40).all()
+    assert ((dw.double() - wantw).abs() <= wmag * (NORM + TURN + (T / 1024 + 256 + 64) * E)).all()

@@ -350,6 +350,28 @@ def test_gradient_against_differences():
         assert abs(diff - (d.double() * v.double()).sum()) <= size * (h * h + 100 * E / h)
 
 
+def test_more_rows_than_work_groups():
+    T, V = (1 << 22) + 3, 3  # the sums' grid ends at 2^20, the gradient's at 2^22
+    g = torch.Generator(device="cuda")
+    g.manual_seed(52)
+    z = torch.randn((T, V), generator=g, device="cuda")
+    targets = torch.randint(0, V, (T,), generator=g, device="cuda", dtype=torch.int32)
+    logp, H, lse = torch.zeros(T, device="cuda"), torch.zeros(T, device="cuda"), torch.zeros((T, 2), device="cuda")
+    ids, alt = torch.full((T, 2), 9, dtype=torch.int32, device="cuda"), torch.zeros((T, 2), device="cuda")
+    moe.moe_token_logprobs(z, targets=targets, logp=logp, entropy=H, lse=lse, top_ids=ids, top_logp=alt)
+    lp = torch.log_softmax(z.double(), dim=1)
+    # three values: their powers' roundings (5 E of a result below 8 each) and those of the sums and logarithms
+    tol = 60 * E
+    assert (logp - lp.gather(1, targets.long()[:, None]).squeeze(1)).abs().max() <= tol
+    assert (H + (lp.exp() * lp).sum(dim=1)).abs().max() <= tol
+    assert torch.equal(ids.long(), torch.sort(z, dim=1, descending=True, stable=True).indices[:, :2])
+    assert (alt - lp.gather(1, ids.long())).abs().max() <= tol
+    d = torch.full_like(z, 7.0)
+    moe.moe_token_logprobs_grad(z, lse, d, targets=targets, dlogp=torch.ones(T, device="cuda"))
+    want = torch.zeros_like(lp).scatter_(1, targets.long()[:, None], 1.0) - lp.exp()
+    assert (d - want).abs().max() <= tol
+
+
 def test_of_no_tokens():
     z = torch.zeros((0, 500), device="cuda")
     e = torch.zeros(0, device="cuda")
