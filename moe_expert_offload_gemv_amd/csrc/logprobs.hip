@@ -10,7 +10,7 @@
 // Bound by traffic, one read of the logits: a thread keeps a running maximum and both sums
 // over 16 values at a time, the next 16 on their way, in powers of two; 12 issue slots a value of which the
 // power takes four, so that 16-bit logits are nearly as long in the vector unit as on their way. Rows are cut
-// into slices while all of them fit on the chip at once.
+// into slices, if they are long, while all of them fit on the chip at once.
 //
 // The top_n largest come out of the same read. A thread also notes the largest of its values in LDS.
 // The top_n-th largest of the threads' maxima is a bound that top_n values reach at least (taken in
@@ -51,6 +51,10 @@ constexpr int kSliceStep = 2048;   // slices are whole multiples
 constexpr int kMaxSlices = 64;
 constexpr int kSliceTarget = 1024; // rows times slices at most: four work-groups a CU, all of them at once
 constexpr int kWaveRow = 2048;     // rows up to this long have one wave
+// Rows up to this long are never cut: one launch of one work-group a row against two launches, us without and with 8
+// alternatives of bf16: 1 x 8000 3.9 and 7.4 against 5.2 and 10.1, 1 x 32000 5.7 and 9.8 against 5.4 and 10.1, 300 x 8000
+// 4.8 and 9.4 against 6.8 and 13.8; beyond it the cut wins: 1 x 65537 8.1 and 12.2 against 5.4 and 10.3
+constexpr int kWholeRow = 32768;
 
 // maximum, sum of 2^((x - max) c) and of the same times (x - max) c
 struct Sums {
@@ -613,7 +617,7 @@ __global__ __launch_bounds__(THREADS) void logprob_grad_kernel(LogprobGradArgs a
 }
 
 int slices_of(int64_t T, int64_t V) {
-  if (V <= kWaveRow || T < 1) return 1;
+  if (V <= kWholeRow || T < 1) return 1;
   const int64_t want = std::max<int64_t>(1, std::min<int64_t>(kSliceTarget / T, kMaxSlices));
   const int64_t slice = ((V + want - 1) / want + kSliceStep - 1) / kSliceStep * kSliceStep;
   return (int)((V + slice - 1) / slice);
@@ -658,7 +662,7 @@ hipError_t launch_grad_types(const LogprobGradArgs& a, hipStream_t s) {
 
 // Never less for more rows: up to kSliceTarget slices in all
 int64_t logprob_workspace_bytes(int64_t T, int64_t V, int top_n) {
-  if (V <= kWaveRow || T < 1) return 0;
+  if (V <= kWholeRow || T < 1) return 0;
   const int64_t items = std::min<int64_t>(T * kMaxSlices, kSliceTarget);
   return items * (16 + 8 * (int64_t)top_n);
 }

@@ -99,7 +99,8 @@ def logits_of(g, T, V, banned=0.0, size=3.0):
 
 SHAPES = [(1, 1, 1), (1, 5, 5), (3, 7, 2), (2, 64, 32), (5, 100, 0), (4, 511, 20), (3, 2048, 32), (2, 2049, 1), (1, 2055, 8),
           (9, 4097, 32), (1, 65537, 20), (33, 8200, 5), (2, 131072, 32), (300, 333, 7), (2100, 3000, 3), (2050, 20, 20),
-          (1, 600001, 32), (300, 10000, 0)]
+          (1, 600001, 32), (300, 10000, 0), (2, 32768, 3), (1, 32769, 3), (9, 40000, 32), (33, 33000, 5), (300, 40000, 0),
+          (520, 40000, 4)]
 
 
 @pytest.mark.parametrize("T,V,n", SHAPES)
@@ -380,7 +381,7 @@ def test_of_no_tokens():
                                 dlogp=e)
 
 
-@pytest.mark.parametrize("T,V", [(2, 20000), (5, 700), (2100, 2500)])
+@pytest.mark.parametrize("T,V", [(2, 20000), (2, 40000), (5, 700), (2100, 2500)])
 def test_captured_two_at_once_and_on_another_stream(T, V):
     g = rng_of(47, T)
     zs = [torch.from_numpy(logits_of(g, T, V)).bfloat16().cuda() for _ in range(2)]
@@ -433,7 +434,7 @@ def test_captured_two_at_once_and_on_another_stream(T, V):
 
 
 def test_binding_refusals():
-    z = torch.zeros((3, 5000), device="cuda")
+    z = torch.zeros((3, 50000), device="cuda")
     y, f = torch.zeros(3, dtype=torch.int32, device="cuda"), torch.zeros(3, device="cuda")
     lse = torch.zeros((3, 2), device="cuda")
     for bad in (dict(targets=y.long(), logp=f), dict(targets=y[:2], logp=f), dict(entropy=f.half()), dict(lse=f),

@@ -22,10 +22,10 @@ OUTS = dict(out_type=BF16, q_out=7 * P, q_out_stride=64, q_out_head_stride=16, k
 GRADS = dict(g_type=BF16, gq=7 * P, gq_stride=64, gq_head_stride=16, gk=8 * P, gk_stride=32, gk_head_stride=16, d_type=BF16, dq=9 * P,
              dq_stride=64, dq_head_stride=16, dk=10 * P, dk_stride=32, dk_head_stride=16, dq_weight=11 * P, dk_weight=12 * P,
              workspace=13 * P, workspace_bytes=1 << 30, flags=0)
-LOGP = dict(device=0, stream=None, n_tokens=2, n_vocab=5000, z_type=BF16, logits=P, z_stride=5000, targets=2 * P, scale=1.0, logp=3 * P,
+LOGP = dict(device=0, stream=None, n_tokens=2, n_vocab=50000, z_type=BF16, logits=P, z_stride=50000, targets=2 * P, scale=1.0, logp=3 * P,
             entropy=4 * P, lse=5 * P, top_n=3, top_ids=6 * P, top_logp=7 * P, workspace=8 * P, workspace_bytes=1 << 30)
-LGRAD = dict(device=0, stream=None, n_tokens=2, n_vocab=5000, z_type=BF16, logits=P, z_stride=5000, targets=2 * P, scale=1.0, lse=3 * P,
-             entropy=4 * P, dlogp=5 * P, dentropy=6 * P, d_type=F32, dlogits=7 * P, d_stride=5000, flags=0)
+LGRAD = dict(device=0, stream=None, n_tokens=2, n_vocab=50000, z_type=BF16, logits=P, z_stride=50000, targets=2 * P, scale=1.0, lse=3 * P,
+             entropy=4 * P, dlogp=5 * P, dentropy=6 * P, d_type=F32, dlogits=7 * P, d_stride=50000, flags=0)
 
 
 @pytest.mark.parametrize("change,what", [
@@ -108,7 +108,7 @@ def test_workspaces_of_larger_batches_serve_smaller_ones():
     (dict(n_vocab=2, z_stride=2), "out of range"), (dict(z_type=3), "type"), (dict(scale=0.0), "scale"), (dict(scale=-1.0), "scale"),
     (dict(scale=float("inf")), "scale"), (dict(scale=float("nan")), "scale"), (dict(scale=2.0 ** 65), "scale"), (dict(scale=2.0 ** -65), "scale"),
     (dict(logits=None), "logits null"),
-    (dict(logits=P + 1), "unaligned"), (dict(z_stride=4999), "stride"), (dict(targets=None), "together"), (dict(logp=None), "together"),
+    (dict(logits=P + 1), "unaligned"), (dict(z_stride=49999), "stride"), (dict(targets=None), "together"), (dict(logp=None), "together"),
     (dict(top_ids=None), "top_n"), (dict(top_logp=None), "top_n"), (dict(top_n=0), "top_n"), (dict(entropy=4 * P + 2), "unaligned"),
     (dict(lse=5 * P + 1), "unaligned"), (dict(workspace=None), "workspace"), (dict(workspace=8 * P + 64), "workspace"),
     (dict(workspace_bytes=100), "workspace"),
@@ -120,8 +120,8 @@ def test_token_logprobs_refuses(change, what):
 
 @pytest.mark.parametrize("change,what", [
     (dict(n_tokens=-1), "out of range"), (dict(n_vocab=0), "out of range"), (dict(z_type=3), "type"), (dict(d_type=4), "type"),
-    (dict(scale=0.0), "scale"), (dict(flags=2), "flags"), (dict(logits=None), "logits null"), (dict(z_stride=4999), "stride"),
-    (dict(dlogits=None), "dlogits null"), (dict(d_stride=4999), "stride"), (dict(lse=None), "lse"), (dict(dlogp=None, dentropy=None), "neither"),
+    (dict(scale=0.0), "scale"), (dict(flags=2), "flags"), (dict(logits=None), "logits null"), (dict(z_stride=49999), "stride"),
+    (dict(dlogits=None), "dlogits null"), (dict(d_stride=49999), "stride"), (dict(lse=None), "lse"), (dict(dlogp=None, dentropy=None), "neither"),
     (dict(targets=None), "needs targets"), (dict(entropy=None), "entropy"), (dict(dlogp=5 * P + 2), "unaligned"), (dict(dlogits=P), "in place"),
     (dict(dlogits=P, d_type=BF16, flags=moe.MOE_ACCUMULATE), "in place"),
 ])
