@@ -55,6 +55,9 @@ constexpr int kWaveRow = 2048;     // rows up to this long have one wave
 // alternatives of bf16: 1 x 8000 3.9 and 7.4 against 5.2 and 10.1, 1 x 32000 5.7 and 9.8 against 5.4 and 10.1, 300 x 8000
 // 4.8 and 9.4 against 6.8 and 13.8; beyond it the cut wins: 1 x 65537 8.1 and 12.2 against 5.4 and 10.3
 constexpr int kWholeRow = 32768;
+// With a row a CU and more, rows of up to twice that: 256 x 40000 8.6 and 12.1 against 10.4 and 16.5, 301 x 65536 12.8 and 17.9
+// against 13.5 and 21.0; fewer rows lose, 100 x 65537 10.0 against 9.0
+constexpr int kManyRows = 256;
 
 // maximum, sum of 2^((x - max) c) and of the same times (x - max) c
 struct Sums {
@@ -617,7 +620,7 @@ __global__ __launch_bounds__(THREADS) void logprob_grad_kernel(LogprobGradArgs a
 }
 
 int slices_of(int64_t T, int64_t V) {
-  if (V <= kWholeRow || T < 1) return 1;
+  if (V <= (T >= kManyRows ? 2 * kWholeRow : kWholeRow) || T < 1) return 1;
   const int64_t want = std::max<int64_t>(1, std::min<int64_t>(kSliceTarget / T, kMaxSlices));
   const int64_t slice = ((V + want - 1) / want + kSliceStep - 1) / kSliceStep * kSliceStep;
   return (int)((V + slice - 1) / slice);

@@ -100,7 +100,7 @@ def logits_of(g, T, V, banned=0.0, size=3.0):
 SHAPES = [(1, 1, 1), (1, 5, 5), (3, 7, 2), (2, 64, 32), (5, 100, 0), (4, 511, 20), (3, 2048, 32), (2, 2049, 1), (1, 2055, 8),
           (9, 4097, 32), (1, 65537, 20), (33, 8200, 5), (2, 131072, 32), (300, 333, 7), (2100, 3000, 3), (2050, 20, 20),
           (1, 600001, 32), (300, 10000, 0), (2, 32768, 3), (1, 32769, 3), (9, 40000, 32), (33, 33000, 5), (300, 40000, 0),
-          (520, 40000, 4)]
+          (520, 40000, 4), (257, 65537, 4), (256, 65536, 2)]
 
 
 @pytest.mark.parametrize("T,V,n", SHAPES)
