@@ -343,6 +343,10 @@ hipError_t launch_heads_grad(HeadsArgs a, uint8_t* ws, hipStream_t s);
 
 // logprobs.hip
 constexpr int kMaxTop = 32;
+struct LogprobSlice {    // of a part of a row: sums of powers referred to m, largest logit
+  double s, u;
+  float m, most;
+};
 struct LogprobArgs {
   const void* logits;
   const int32_t* targets;  // nullptr: none
@@ -356,7 +360,8 @@ struct LogprobArgs {
   // of the launch: slices of a row, values of a slice, log2 of the iterations of a noted maximum
   int32_t slices, note_log;
   int64_t slice;
-  float *sums, *slice_values;  // [T][slices][4], [T][slices][top_n]
+  LogprobSlice* sums;    // [T][slices]
+  float* slice_values;   // [T][slices][top_n]
   int32_t* slice_ids;
 };
 int64_t logprob_workspace_bytes(int64_t T, int64_t V, int top_n);

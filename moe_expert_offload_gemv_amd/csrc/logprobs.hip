@@ -59,16 +59,45 @@ constexpr int kWholeRow = 32768;
 // against 13.5 and 21.0; fewer rows lose, 100 x 65537 10.0 against 9.0
 constexpr int kManyRows = 256;
 
-// maximum, sum of 2^((x - max) c) and of the same times (x - max) c
+// Maximum, sum of 2^((x - max) c) and of the same times (x - max) c. The sums of a row are held in 64 bits: beside a
+// confident word, which is 1, the others are far below 2^-24 each, and their mass is what its log probability says. In 32
+// bits the thread that holds that word would drop its share of them, an error that grows with the row. Runs of 16 values
+// are summed in 32 bits first, so that 64 bits cost some ten instructions for 16 values; such a run is off by
+// a few roundings of itself at most.
 struct Sums {
-  float m, s, u;
+  float m;
+  double s, u;
 };
-// the sums of `a` referred to the maximum m >= a.m
-__device__ __forceinline__ void refer(Sums& a, float m, float c) {
-  const float d = fmaxf((a.m - m) * c, kFloor), f = __builtin_amdgcn_exp2f(d);
-  a.u = f * fmaf(a.s, d, a.u);
-  a.s *= f;
+// the sums of `a` referred to the maximum m >= a.m, and others of that maximum added
+__device__ __forceinline__ void refer(Sums& a, float m, float c, float s = 0.f, float u = 0.f) {
+  const float d = fmaxf((a.m - m) * c, kFloor);
+  const double f = __builtin_amdgcn_exp2f(d);
+  a.u = fma(f, fma(a.s, (double)d, a.u), (double)u);
+  a.s = fma(f, a.s, (double)s);
   a.m = m;
+}
+template <int CTRL>
+__device__ __forceinline__ double dpp64(double v) {
+  const uint64_t b = (uint64_t)__double_as_longlong(v);
+  const uint32_t lo = route_dev::dpp32<CTRL>((uint32_t)b), hi = route_dev::dpp32<CTRL>((uint32_t)(b >> 32));
+  return __longlong_as_double((long long)((uint64_t)hi << 32 | lo));
+}
+__device__ __forceinline__ double lane_value(double v, int lane) {
+  const uint64_t b = (uint64_t)__double_as_longlong(v);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)b, lane), hi = (uint32_t)__builtin_amdgcn_readlane((int)(b >> 32), lane);
+  return __longlong_as_double((long long)((uint64_t)hi << 32 | lo));
+}
+// Both sums of the lanes, in every lane: even lanes go on with one of them and odd ones with the other
+__device__ __forceinline__ void wave_sums(Sums& t) {
+  using namespace route_dev;
+  constexpr int kRowRor4 = 0x124, kRowRor8 = 0x128;  // rotations within 16 lanes
+  const bool odd = threadIdx.x & 1;
+  double v = (odd ? t.u : t.s) + dpp64<kDppQuadXor1>(odd ? t.s : t.u);
+  v += dpp64<kDppQuadXor2>(v);
+  v += dpp64<kRowRor4>(v);
+  v += dpp64<kRowRor8>(v);
+  t.s = (lane_value(v, 0) + lane_value(v, 16)) + (lane_value(v, 32) + lane_value(v, 48));
+  t.u = (lane_value(v, 1) + lane_value(v, 17)) + (lane_value(v, 33) + lane_value(v, 49));
 }
 
 __device__ __forceinline__ uint32_t key_of(float v) { return route_dev::order_bits(v); }
@@ -105,7 +134,9 @@ __device__ __forceinline__ RowResult row_result(const Sums& t, float most, float
   r.bad = !(t.s == t.s) || z == __builtin_inff();
   r.none = !r.bad && (most == kMinusInf || z == kMinusInf);
   r.m = t.m;
-  r.log_sum = logf(t.s);
+  // the logarithm of both halves of the sum: 1 and a little must not become 1
+  const float hi = (float)t.s;
+  r.log_sum = fmaf((float)(t.s - hi), __builtin_amdgcn_rcpf(hi), logf(hi));
   return r;
 }
 constexpr uint32_t kNan = 0x7FC00000u;
@@ -114,7 +145,7 @@ constexpr uint32_t kNan = 0x7FC00000u;
 // rounding of lse would scale them all. lse is handed on in two floats.
 template <int ZT>
 __device__ __forceinline__ void put_row(const LogprobArgs& a, int64_t row, const Sums& t, const RowResult& r) {
-  const double log_sum = log((double)t.s), scale = a.scale, lse = t.m * scale + log_sum;
+  const double log_sum = log(t.s), scale = a.scale, lse = t.m * scale + log_sum;
   const float nan = __uint_as_float(kNan);
   if (a.logp) {
     const int64_t y = a.targets[row];
@@ -126,7 +157,7 @@ __device__ __forceinline__ void put_row(const LogprobArgs& a, int64_t row, const
     a.logp[row] = v;
   }
   if (a.entropy) {
-    const float h = (float)(log_sum - (double)t.u / t.s * 0.69314718055994530942);
+    const float h = (float)(log_sum - t.u / t.s * 0.69314718055994530942);
     a.entropy[row] = r.bad ? nan : r.none ? 0.f : fmaxf(h, 0.f);
   }
   if (a.lse) {
@@ -177,10 +208,14 @@ __device__ __forceinline__ uint32_t nth_of_lanes(uint32_t key, int n) {
   return bound;
 }
 
-__device__ __forceinline__ float wave_max(float v) {
+__device__ __forceinline__ float quad_max(float v) {
   using namespace route_dev;
   v = fmaxf(v, __uint_as_float(dpp32<kDppQuadXor1>(__float_as_uint(v))));
-  v = fmaxf(v, __uint_as_float(dpp32<kDppQuadXor2>(__float_as_uint(v))));
+  return fmaxf(v, __uint_as_float(dpp32<kDppQuadXor2>(__float_as_uint(v))));
+}
+__device__ __forceinline__ float wave_max(float v) {
+  using namespace route_dev;
+  v = quad_max(v);
   v = fmaxf(v, __uint_as_float(dpp32<kDppRowHalfMirror>(__float_as_uint(v))));
   v = fmaxf(v, __uint_as_float(dpp32<kDppRowMirror>(__float_as_uint(v))));
   const int u = __float_as_int(v);
@@ -373,7 +408,7 @@ __global__ __launch_bounds__(THREADS, TOP ? 4 : ZT == MOE_F32 ? 6 : 8) void logp
     const char* z = static_cast<const char*>(a.logits) + row * a.z_stride * value_size<ZT>();
     const int begin = slice * (int)a.slice, end = min(begin + (int)a.slice, (int)a.V);
     const int iters = (end - begin + kIter - 1) / kIter;
-    Sums t{kLowest, 0.f, 0.f};
+    Sums t{kLowest, 0.0, 0.0};
     float most = kMinusInf, noted = kMinusInf;
     Raw8<ZT> raw[kU];
     auto fetch = [&](int at) __attribute__((always_inline)) {
@@ -391,17 +426,21 @@ __global__ __launch_bounds__(THREADS, TOP ? 4 : ZT == MOE_F32 ? 6 : 8) void logp
       }
       most = fmaxf(most, m);
       noted = fmaxf(noted, m);
-      refer(t, fmaxf(t.m, m), c);
+      m = fmaxf(t.m, m);
+      float s = 0.f, u = 0.f;
 #pragma unroll
       for (int r = 0; r < kU; ++r) {
         if (r >= runs) break;
+        float e[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          const float d = (v[r][j] - t.m) * c, e = __builtin_amdgcn_exp2f(d);
-          t.s += e;
-          t.u = fmaf(e, fmaxf(d, kFloor), t.u);
+          const float d = (v[r][j] - m) * c;
+          e[j] = __builtin_amdgcn_exp2f(d);
+          u = fmaf(e[j], fmaxf(d, kFloor), u);
         }
+        s += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
       }
+      refer(t, m, c, s, u);
     };
     auto note = [&](int it) __attribute__((always_inline)) {
       if constexpr (TOP)
@@ -432,32 +471,25 @@ __global__ __launch_bounds__(THREADS, TOP ? 4 : ZT == MOE_F32 ? 6 : 8) void logp
       note(it);
     }
     // over the lanes, then the waves in their order
-    float m = wave_max(t.m);
-    refer(t, m, c);
-    t.s = route_dev::wave_sum(t.s);
-    t.u = route_dev::wave_sum(t.u);
+    refer(t, wave_max(t.m), c);
+    wave_sums(t);
     float wave_most = wave_max(most);
     if constexpr (W > 1) {
       __syncthreads();  // the item before has been read
       if ((tid & 63) == 0) s_sum[tid >> 6] = t, s_most[tid >> 6] = wave_most;
       __syncthreads();
-#pragma unroll
-      for (int w = 0; w < W; ++w) m = fmaxf(m, s_sum[w].m), wave_most = fmaxf(wave_most, s_most[w]);
-      Sums all{m, 0.f, 0.f};
-#pragma unroll
-      for (int w = 0; w < W; ++w) {
-        Sums o = s_sum[w];
-        refer(o, m, c);
-        all.s += o.s, all.u += o.u;
-      }
-      t = all;
+      static_assert(W == 4, "a lane of each quad per wave");
+      t = s_sum[tid & 3], wave_most = s_most[tid & 3];
+      refer(t, quad_max(t.m), c);
+      wave_most = quad_max(wave_most);
+      t.s += dpp64<route_dev::kDppQuadXor1>(t.s), t.u += dpp64<route_dev::kDppQuadXor1>(t.u);
+      t.s += dpp64<route_dev::kDppQuadXor2>(t.s), t.u += dpp64<route_dev::kDppQuadXor2>(t.u);
     }
     const RowResult r = row_result(t, wave_most, a.scale);
     if (a.slices == 1) {
       if (tid == 0) put_row<ZT>(a, row, t, r);
     } else if (tid == 0) {
-      float* p = a.sums + 4 * item;
-      p[0] = t.m, p[1] = t.s, p[2] = t.u, p[3] = wave_most;
+      a.sums[item] = LogprobSlice{t.s, t.u, t.m, wave_most};
     }
     if constexpr (TOP) {
       int* ids = a.slices == 1 ? a.top_ids + row * a.top_n : a.slice_ids + item * a.top_n;
@@ -490,13 +522,12 @@ __global__ __launch_bounds__(kFinish) void logprob_finish_kernel(LogprobArgs a) 
   const float c = a.scale * kLog2e;
   // every wave forms the row's sums: a lane per slice
   static_assert(kMaxSlices == 64, "a lane per slice");
-  const float* p = a.sums + 4 * (row * a.slices + std::min(lane, a.slices - 1));
+  const LogprobSlice p = a.sums[row * a.slices + std::min(lane, a.slices - 1)];
   const bool in = lane < a.slices;
-  Sums t{p[0], in ? p[1] : 0.f, in ? p[2] : 0.f};
-  const float most = wave_max(p[3]), m = wave_max(t.m);
+  Sums t{p.m, in ? p.s : 0.0, in ? p.u : 0.0};
+  const float most = wave_max(p.most), m = wave_max(t.m);
   refer(t, m, c);
-  t.s = route_dev::wave_sum(t.s);
-  t.u = route_dev::wave_sum(t.u);
+  wave_sums(t);
   const RowResult r = row_result(t, most, a.scale);
   if (tid == 0) put_row<ZT>(a, row, t, r);
   if (!a.top_n) return;
@@ -641,8 +672,8 @@ hipError_t launch_types(LogprobArgs a, hipStream_t s) {
   }
   if (a.slices > 1) {
     const int64_t items = a.T * a.slices;
-    a.sums = reinterpret_cast<float*>(a.ws);
-    a.slice_values = a.sums + 4 * items;
+    a.sums = reinterpret_cast<LogprobSlice*>(a.ws);
+    a.slice_values = reinterpret_cast<float*>(a.sums + items);
     a.slice_ids = reinterpret_cast<int*>(a.slice_values + items * a.top_n);
   }
   // rows beyond the grid are taken in turn by the same work-groups
@@ -667,7 +698,7 @@ hipError_t launch_grad_types(const LogprobGradArgs& a, hipStream_t s) {
 int64_t logprob_workspace_bytes(int64_t T, int64_t V, int top_n) {
   if (V <= kWholeRow || T < 1) return 0;
   const int64_t items = std::min<int64_t>(T * kMaxSlices, kSliceTarget);
-  return items * (16 + 8 * (int64_t)top_n);
+  return items * ((int64_t)sizeof(LogprobSlice) + 8 * (int64_t)top_n);
 }
 
 hipError_t launch_logprobs(const LogprobArgs& a, hipStream_t s) {

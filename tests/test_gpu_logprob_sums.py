@@ -1,0 +1,64 @@
+"""Sums behind the log probabilities on the GPU: rows of one confident word, whose log probability is the
+mass of all the others together.
+
+Tolerances count roundings: E = 2^-24 of a result per fp32 operation. They do not grow with the row.
+"""
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import moe_expert_offload_gemv_amd as moe  # noqa: E402
+from tests.test_gpu_dense_ops import TYPES, E, rng_of  # noqa: E402
+from tests.test_gpu_logprobs import Out  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+
+# Every word but one is 16, 17 or 18 below it (exact in every type). Of a word's power, relative to it: the argument, at most 18
+# nats in all however it is reached over rising maxima, with a rounding of its product with log2 e and 0.3 for that
+# constant, 1.3 * 18; the power 2; its sum with the 15 beside it 8; rising maxima, two of a thread, then lanes, waves, slices,
+# each with a power of 2 and a product, 5 * 3.
+WORD = 1.3 * 18 + 2 + 8 + 15
+# Beside the confident word, which is 1: the 15 words added to it in fp32, 8 roundings of 1 and a bit.
+PEAK = 8.1
+
+
+# uncut rows by one wave and by four; cut; many rows, uncut; long and uncut (from 513 rows on nothing is)
+@pytest.mark.parametrize("T,V", [(3, 2000), (3, 32768), (2, 65537), (260, 65536), (1, 1 << 22), (520, 1 << 20)])
+@pytest.mark.parametrize("where", ["first", "middle", "last"])
+@pytest.mark.parametrize("zt", ["f32", "bf16"])
+def test_one_confident_word(T, V, where, zt):
+    g = rng_of(61, T, V)
+    at = {"first": 0, "middle": V // 2 + 1, "last": V - 1}[where]
+    rest = torch.from_numpy(g.integers(-18, -15, V)).to(TYPES[zt]).cuda()
+    rest[at] = 0
+    z = torch.empty((T, V), dtype=TYPES[zt], device="cuda")
+    z[:] = rest
+    targets = torch.full((T,), at, dtype=torch.int32, device="cuda")
+    targets[1:] = (at + 5) % V
+    n = 2
+    o = Out(T, V, n, z)
+    kw = dict(targets=targets, logp=o.logp, entropy=o.entropy, lse=o.lse, workspace=o.ws)
+    moe.moe_token_logprobs(z, **kw, **({"top_ids": o.ids, "top_logp": o.alt} if T < 100 else {}))
+    x = rest.double().cpu().numpy()
+    p = np.exp(x)
+    others = p.sum() - 1.0  # beside 1: 53 bits are plenty for what is asked below
+    log_s = np.log1p(others)
+    s = PEAK * E + others * WORD * E
+    assert abs(float(o.logp[0]) + log_s) <= s + 1.01 * E * log_s
+    assert abs(o.lse.double().sum(dim=1).cpu().numpy() - log_s).max() <= s
+    H = float(log_s - (p * x).sum() / p.sum())
+    assert abs(o.entropy.double().cpu().numpy() - H).max() <= s + (WORD + 12) * E * H
+    if T > 1:
+        far = float(x[(at + 5) % V]) - log_s
+        assert abs(o.logp[1:].double().cpu().numpy() - far).max() <= s + 1.01 * E * abs(far)
+    if T < 100:
+        assert (o.ids[:, 0] == at).all() and abs(o.alt[:, 0].double().cpu().numpy() + log_s).max() <= s + 3 * E * log_s
+    if T * V > 1 << 26:
+        return
+    # 1 - p of the confident word, and a gradient that sums to nothing: each p has its own power's roundings besides
+    d = torch.empty((T, V), dtype=torch.float32, device="cuda")
+    moe.moe_token_logprobs_grad(z, o.lse, d, targets=torch.full_like(targets, at), dlogp=torch.ones(T, device="cuda"))
+    d = d.double().cpu().numpy()
+    assert abs(d[:, at] - others / (1 + others)).max() <= s + 4 * E
+    assert abs(d.sum(axis=1)).max() <= s + 4 * E + others * (3.3 * 18 + 4) * E
