@@ -568,7 +568,8 @@ MOE_API int moe_q4_linear(int32_t device, void* stream, int32_t n_tokens, int32_
  * pair_axis[i] (uint8 [rotary_dim / 2] on the device, NULL: 0 for all; a pair whose
  * axis is n_axes or more is not turned). positions int32 [n_axes][n_tokens], rows
  * pos_stride apart (0: one row for all), any sign; inv_freq fp32 [rotary_dim / 2]. The angle is formed
- * in 64 bits, so it is exact for every position. rotary_dim is even, 0..head_dim;
+ * and reduced in 64 bits, off by at most 2^-51 of itself (2^-20 at position 2^31 and a frequency of 1); its
+ * cosine and sine are off by 1.4 * 2^-24 besides. rotary_dim is even, 0..head_dim;
  * 0: the norm alone, with inv_freq and positions NULL. MOE_NO_NORM: the rotation
  * alone, with both weights NULL.
  * A tensor of heads [n_tokens][heads][head_dim] has its values contiguous, tokens

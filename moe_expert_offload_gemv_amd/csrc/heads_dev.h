@@ -144,17 +144,16 @@ __device__ __forceinline__ float lanes_sum(float v, int G) {
 // n / d for n < 2^20 and d's magic = ceil(2^31 / d) where n * d < 2^31
 __device__ __forceinline__ int quotient(int n, uint32_t magic) { return (int)(((uint64_t)(uint32_t)n * magic) >> 31); }
 
-// cos and sin of position * inv_freq. The angle is formed in 64 bits, in turns, and
-// reduced to an eighth of a turn either side of a quarter's multiple; there the Taylor
-// series of both are exact to 2^-26 with the terms taken. fp32 would lose the angle of
+// cos and sin of position * inv_freq, each within 1.4 * 2^-24 and the angle's own error, 2^-51 of it. The angle is
+// formed in turns and reduced to an eighth of a turn either side of a quarter's multiple, both in 64 bits; the rest, below
+// 0.8, is rounded once, and there the Taylor series of both are exact to 2^-28 with the terms taken. fp32 would lose the angle of
 // far positions (2^18 * 1.0: off by 2^-6), and tables would have to be read for every token.
 __device__ __forceinline__ float2 turn_of(int position, float inv_freq) {
   constexpr double kTurn = 0.15915494309189533577;  // 1 / (2 pi)
   double t = (double)position * ((double)inv_freq * kTurn);
   t -= rint(t);
-  const float f = (float)t;  // -0.5 .. 0.5
-  const float quarter = rintf(4.0f * f);
-  const float x = 6.283185307f * fmaf(-0.25f, quarter, f), y = x * x;
+  const double quarter = rint(4.0 * t);  // -2 .. 2
+  const float x = (float)(6.28318530717958647693 * fma(-0.25, quarter, t)), y = x * x;
   float s = fmaf(y, 1.0f / 362880.0f, -1.0f / 5040.0f);
   s = fmaf(y, s, 1.0f / 120.0f);
   s = fmaf(y, s, -1.0f / 6.0f);
