@@ -46,7 +46,6 @@ __global__ __launch_bounds__(kThreads) void heads_kernel(HeadsArgs a) {
   const HeadsPart p = is_k ? a.k : a.q;
   const int G = a.lanes, l = threadIdx.x & (G - 1), mine = threadIdx.x >> a.lanes_log;
   const int at_once = kThreads >> a.lanes_log, S = a.D / 2;
-  const bool some_still = a.R < a.D || a.axis;
   const float inv_D = 1.0f / (float)a.D;
   Place place[NG];
   float wa[NG][RUN], wb[NG][RUN];
@@ -130,7 +129,7 @@ __global__ __launch_bounds__(kThreads) void heads_kernel(HeadsArgs a) {
         if (a.R) {
           float2 angles[RUN];
           load_turns<RUN>(s_turn + token * S + RUN * (l + G * g), angles);
-          turn<false, RUN>(va[g], vb[g], angles, some_still);
+          turn<false, RUN>(va[g], vb[g], angles);
         }
         store_slots<PAIRS, RUN>(a.out_type, row, place[g], va[g], vb[g]);
       }

@@ -169,20 +169,16 @@ __device__ __forceinline__ float2 turn_of(int position, float inv_freq) {
   return r;
 }
 
-// The slots (a, b) turned by their (cos, sin), by minus the angle with BACK. some_still: there are slots that do not
-// turn, whose sine is 0; without a sine neither value sees the other, so that they are not spoilt
-// by a neighbour that is not finite.
+// The slots (a, b) turned by their (cos, sin), by minus the angle with BACK. Without a sine (position 0, or a slot that
+// does not turn) neither value sees the other, so that it is not spoilt by a neighbour that is not finite.
 template <bool BACK, int RUN>
-__device__ __forceinline__ void turn(float (&a)[RUN], float (&b)[RUN], const float2 (&cs)[RUN], bool some_still) {
-  float pa[RUN], pb[RUN];
+__device__ __forceinline__ void turn(float (&a)[RUN], float (&b)[RUN], const float2 (&cs)[RUN]) {
 #pragma unroll
-  for (int j = 0; j < RUN; ++j) pa[j] = (BACK ? b[j] : -b[j]) * cs[j].y, pb[j] = (BACK ? -a[j] : a[j]) * cs[j].y;
-  if (some_still) {
-#pragma unroll
-    for (int j = 0; j < RUN; ++j) pa[j] = cs[j].y != 0.f ? pa[j] : 0.f, pb[j] = cs[j].y != 0.f ? pb[j] : 0.f;
+  for (int j = 0; j < RUN; ++j) {
+    const bool turns = cs[j].y != 0.f;
+    const float pa = turns ? (BACK ? b[j] : -b[j]) * cs[j].y : 0.f, pb = turns ? (BACK ? -a[j] : a[j]) * cs[j].y : 0.f;
+    a[j] = fmaf(a[j], cs[j].x, pa), b[j] = fmaf(b[j], cs[j].x, pb);
   }
-#pragma unroll
-  for (int j = 0; j < RUN; ++j) a[j] = fmaf(a[j], cs[j].x, pa[j]), b[j] = fmaf(b[j], cs[j].x, pb[j]);
 }
 
 // the angles of a group of slots, in the widest reads that its place allows

@@ -46,7 +46,6 @@ __global__ __launch_bounds__(kThreads) void heads_grad_kernel(HeadsArgs a) {
   const HeadsPart p = is_k ? a.k : a.q;
   const int G = a.lanes, l = threadIdx.x & (G - 1), mine = threadIdx.x >> a.lanes_log;
   const int at_once = kThreads >> a.lanes_log, S = a.D / 2;
-  const bool some_still = a.R < a.D || a.axis;
   const float inv_D = 1.0f / (float)a.D;
   const int64_t block = (int)blockIdx.x - (is_k ? a.q.blocks : 0);
   Place place[NG];
@@ -109,7 +108,7 @@ __global__ __launch_bounds__(kThreads) void heads_grad_kernel(HeadsArgs a) {
         if (USUAL || a.R) {
           float2 angles[RUN];
           load_turns<RUN>(s_turn + now.token * S + (USUAL || place[g].in ? RUN * (l + G * g) : 0), angles);
-          turn<true, RUN>(ga[g], gb[g], angles, some_still);
+          turn<true, RUN>(ga[g], gb[g], angles);
         }
       }
       if (USUAL || a.norm) {
