@@ -166,8 +166,11 @@ __device__ __forceinline__ void put_row(const LogprobArgs& a, int64_t row, const
     a.lse[2 * row + 1] = r.bad || r.none ? 0.f : (float)(lse - hi);
   }
 }
-// log probability of a row's value above -inf; not by way of (x - max) c, which passes fp32's range first
-__device__ __forceinline__ float row_logp(const RowResult& r, float x, float scale) { return fmaf(x - r.m, scale, -r.log_sum); }
+// log probability of a row's value above -inf. By way of halves: the difference of two logits may pass fp32's range
+// where scale times it does not.
+__device__ __forceinline__ float row_logp(const RowResult& r, float x, float scale) {
+  return fmaf(0.5f * x - 0.5f * r.m, 2.0f * scale, -r.log_sum);
+}
 
 // Ranks `count` candidates (value, id) and hands each with its rank to f; every thread of the
 // work-group comes here. The order of the candidates has no part in the ranks. Four lanes share a

@@ -62,3 +62,23 @@ def test_one_confident_word(T, V, where, zt):
     d = d.double().cpu().numpy()
     assert abs(d[:, at] - others / (1 + others)).max() <= s + 4 * E
     assert abs(d.sum(axis=1)).max() <= s + 4 * E + others * (3.3 * 18 + 4) * E
+
+
+@pytest.mark.parametrize("V", [5, 3000, 65537])
+@pytest.mark.parametrize("scale", [0.5, 2.0 ** -64])
+def test_alternatives_far_below_the_best(V, scale):
+    """The difference of two fp32 logits may pass fp32's range where scale times it does not."""
+    z = torch.full((2, V), -3e38, device="cuda")
+    z[:, 1], z[1, 2] = 3e38, 2.9e38
+    n = 4
+    targets = torch.full((2,), 3, dtype=torch.int32, device="cuda")
+    o = Out(2, V, n, z)
+    moe.moe_token_logprobs(z, targets=targets, logp=o.logp, entropy=o.entropy, lse=o.lse, top_ids=o.ids, top_logp=o.alt, scale=scale,
+                           workspace=o.ws)
+    lp = scale * (z.double() - 3e38)
+    lp = lp - torch.logsumexp(lp, dim=1, keepdim=True)
+    assert (o.ids == torch.tensor([[1, 0, 2, 3], [1, 2, 0, 3]], device="cuda")).all()
+    want = lp.gather(1, o.ids.long())
+    # the float nearest 3e38 is within E of it, the difference and the product are rounded
+    assert ((o.alt.double() - want).abs() <= 4 * E * want.abs() + 1e-6).all()
+    assert ((o.logp.double() - lp[:, 3]).abs() <= 3 * E * lp[:, 3].abs() + 1e-6).all()
