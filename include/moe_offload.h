@@ -634,7 +634,8 @@ MOE_API int64_t moe_qk_norm_rope_grad_workspace_bytes(int32_t n_tokens, int32_t 
  * [n_tokens], lse: each NULL if not asked for. top_n is 0..min(n_vocab, 32); top_ids
  * int32 and top_logp fp32 [n_tokens][top_n] are NULL with 0. n_vocab is 1..2^22.
  * workspace: moe_token_logprobs_workspace_bytes bytes of device memory, 256-byte
- * aligned, as moe_q4_matmul's. */
+ * aligned, as moe_q4_matmul's; it serves up to n_tokens rows. Where rows are many the
+ * call itself uses none and takes NULL: one that needs it says so. */
 MOE_API int moe_token_logprobs(int32_t device, void* stream, int32_t n_tokens, int32_t n_vocab, int32_t z_type,
                                const void* logits, int64_t z_stride, const int32_t* targets, float scale, float* logp,
                                float* entropy, float* lse, int32_t top_n, int32_t* top_ids, float* top_logp,

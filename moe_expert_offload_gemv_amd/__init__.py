@@ -736,8 +736,15 @@ def moe_token_logprobs(logits, targets=None, logp=None, entropy=None, lse=None, 
         tp = _flat("top_logp", top_logp, dev, (T, n), "torch.float32")
         if n == 0:
             ip = tp = None
-    workspace, kp, kn = _workspace(workspace, dev, stream, lambda: moe_token_logprobs_workspace(logits, n))
-    rc = L.moe_token_logprobs(dev, _stream_of(stream, dev), T, V, zt, zp, zs, yp, scale, lp, ep, sp, n, ip, tp, kp, kn)
+    s = _stream_of(stream, dev)
+    kp, kn = None, 0
+    if workspace is not None:
+        workspace, kp, kn = _workspace(workspace, dev, stream, None)
+    rc = L.moe_token_logprobs(dev, s, T, V, zt, zp, zs, yp, scale, lp, ep, sp, n, ip, tp, kp, kn)
+    if rc and workspace is None:  # refused, perhaps for the want of one: calls of many rows use none
+        workspace, kp, kn = _workspace(None, dev, stream, lambda: moe_token_logprobs_workspace(logits, n))
+        if kp is not None:
+            rc = L.moe_token_logprobs(dev, s, T, V, zt, zp, zs, yp, scale, lp, ep, sp, n, ip, tp, kp, kn)
     if rc:
         _fail(rc)
 

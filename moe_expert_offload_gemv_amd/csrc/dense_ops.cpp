@@ -341,8 +341,9 @@ extern "C" int moe_token_logprobs(int32_t device, void* stream, int32_t n_tokens
                                   float* entropy, float* lse, int32_t top_n, int32_t* top_ids, float* top_logp,
                                   void* workspace, int64_t workspace_bytes) {
   const char* me = "moe_token_logprobs";
-  const int64_t need = moe_token_logprobs_workspace_bytes(n_tokens, n_vocab, top_n);
-  REFUSE(need < 0, "%s: n_tokens %d, n_vocab %d or top_n %d out of range", me, n_tokens, n_vocab, top_n);
+  REFUSE(moe_token_logprobs_workspace_bytes(n_tokens, n_vocab, top_n) < 0,
+         "%s: n_tokens %d, n_vocab %d or top_n %d out of range", me, n_tokens, n_vocab, top_n);
+  const int64_t need = moe::logprob_workspace_used(n_tokens, n_vocab, top_n);
   REFUSE(!value_type(z_type), "%s: bad type of the logits", me);
   REFUSE(!(scale >= 0x1p-64f && scale <= 0x1p64f), "%s: scale %g out of range", me, scale);
   if (n_tokens > 0) {

@@ -364,7 +364,8 @@ struct LogprobArgs {
   float* slice_values;   // [T][slices][top_n]
   int32_t* slice_ids;
 };
-int64_t logprob_workspace_bytes(int64_t T, int64_t V, int top_n);
+int64_t logprob_workspace_bytes(int64_t T, int64_t V, int top_n);  // of a workspace for up to T rows
+int64_t logprob_workspace_used(int64_t T, int64_t V, int top_n);   // by a call of T rows
 hipError_t launch_logprobs(const LogprobArgs& a, hipStream_t s);
 struct LogprobGradArgs {
   const void* logits;

@@ -660,6 +660,8 @@ int slices_of(int64_t T, int64_t V) {
   return (int)((V + slice - 1) / slice);
 }
 
+int64_t slice_bytes(int top_n) { return (int64_t)sizeof(LogprobSlice) + 8 * (int64_t)top_n; }
+
 template <int ZT, int THREADS>
 hipError_t launch_rows(const LogprobArgs& a, dim3 grid, hipStream_t s) {
   return a.top_n ? launch(logprob_rows_kernel<ZT, THREADS, true>, grid, dim3(THREADS), Launch{s}, a)
@@ -697,11 +699,14 @@ hipError_t launch_grad_types(const LogprobGradArgs& a, hipStream_t s) {
 
 }  // namespace
 
-// Never less for more rows: up to kSliceTarget slices in all
+// Never less for more rows, though many rows are not cut: up to kSliceTarget slices in all
 int64_t logprob_workspace_bytes(int64_t T, int64_t V, int top_n) {
   if (V <= kWholeRow || T < 1) return 0;
-  const int64_t items = std::min<int64_t>(T * kMaxSlices, kSliceTarget);
-  return items * ((int64_t)sizeof(LogprobSlice) + 8 * (int64_t)top_n);
+  return std::min<int64_t>(T * kMaxSlices, kSliceTarget) * slice_bytes(top_n);
+}
+int64_t logprob_workspace_used(int64_t T, int64_t V, int top_n) {
+  const int slices = slices_of(T, V);
+  return slices > 1 ? T * slices * slice_bytes(top_n) : 0;
 }
 
 hipError_t launch_logprobs(const LogprobArgs& a, hipStream_t s) {

@@ -82,3 +82,22 @@ def test_alternatives_far_below_the_best(V, scale):
     # the float nearest 3e38 is within E of it, the difference and the product are rounded
     assert ((o.alt.double() - want).abs() <= 4 * E * want.abs() + 1e-6).all()
     assert ((o.logp.double() - lp[:, 3]).abs() <= 3 * E * lp[:, 3].abs() + 1e-6).all()
+
+
+def test_a_row_that_is_not_cut_needs_no_workspace():
+    """The workspace of fewer rows serves more of them, and more that are not cut use none: nothing to allocate on a stream of
+    the caller's own."""
+    side = torch.cuda.Stream()
+    for T, V in ((300, 40000), (600, 70000)):
+        assert moe.moe_token_logprobs_workspace_bytes(T, V, 3) > 0
+        z = torch.randn((T, V), device="cuda")
+        want, got = torch.empty(T, device="cuda"), torch.empty(T, device="cuda")
+        moe.moe_token_logprobs(z, entropy=want, workspace=moe.moe_token_logprobs_workspace(z))
+        side.wait_stream(torch.cuda.current_stream())
+        moe.moe_token_logprobs(z, entropy=got, stream=side)
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)
+        moe.moe_token_logprobs(z, entropy=got.zero_())
+        assert torch.equal(got, want)
+    with pytest.raises(ValueError, match="workspace"):
+        moe.moe_token_logprobs(z[:5], entropy=got[:5].clone(), stream=side)
