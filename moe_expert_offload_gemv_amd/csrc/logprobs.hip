@@ -51,13 +51,27 @@ constexpr int kSliceStep = 2048;   // slices are whole multiples
 constexpr int kMaxSlices = 64;
 constexpr int kSliceTarget = 1024; // rows times slices at most: four work-groups a CU, all of them at once
 constexpr int kWaveRow = 2048;     // rows up to this long have one wave
-// Rows up to this long are never cut: one launch of one work-group a row against two launches, us without and with 8
-// alternatives of bf16: 1 x 8000 3.9 and 7.4 against 5.2 and 10.1, 1 x 32000 5.7 and 9.8 against 5.4 and 10.1, 300 x 8000
-// 4.8 and 9.4 against 6.8 and 13.8; beyond it the cut wins: 1 x 65537 8.1 and 12.2 against 5.4 and 10.3
-constexpr int kWholeRow = 32768;
-// With a row a CU and more, rows of up to twice that: 256 x 40000 8.6 and 12.1 against 10.4 and 16.5, 301 x 65536 12.8 and 17.9
-// against 13.5 and 21.0; fewer rows lose, 100 x 65537 10.0 against 9.0
-constexpr int kManyRows = 256;
+// Rows up to this long are not cut: a work-group a row in one launch, against a work-group a slice, a second launch to join
+// them and, with alternatives, a second search. Few rows leave CUs idle, so the more rows there are the longer they may be.
+// With alternatives the limit could lie higher and without them lower; it is one, so that what else is said of a row has
+// the same bits with and without them. us cut and uncut, without alternatives bf16, fp32, with 8 bf16, fp32:
+//     1 row    24000   5.7  5.5   5.6  5.4  10.5  9.5  10.4  9.4
+//              40000   5.7  6.6   5.4  6.5  10.3 10.7  10.2 10.3
+//    32 rows   32000   6.4  6.4   6.4  6.4  11.6 10.9  11.6 10.6
+//              65537   6.7  8.8   7.0  8.8  12.6 13.5  12.6 13.0
+//    64        40000   6.9  7.0   7.8  8.0  13.1 11.4  13.8 11.6
+//              80000   8.7 10.8  10.5 13.3  15.1 15.5  16.5 15.8
+//   128        65537  10.6 10.6  12.6 11.9  17.2 14.9  19.1 15.1
+//             131072  12.4 15.4  16.4 18.8  18.9 19.8  22.5 20.9
+//   200        80000  12.4 12.9  16.4 14.6  19.3 16.6  23.1 17.8
+//             262144  28.2 41.9  48.0 59.4  35.0 45.7  54.1 61.1
+//   301       131072  19.4 21.8  37.5 32.9  27.4 27.6  43.5 36.3
+//             262144  40.1 52.0  72.1 73.3  47.3 55.1  79.6 69.5
+// From one and a half rows a CU on they are not cut at any length:
+//   400       262144  51.7 54.6  98.7 78.9  59.4 61.4   107 84.1
+//   512       262144  60.1 54.9   109 98.9  69.8 59.7   115  106
+constexpr int kWholeRow = 32768, kWholeRowMore = 300;  // and more for each row
+constexpr int kMostCut = 384;                          // rows of which no length is cut
 
 // Maximum, sum of 2^((x - max) c) and of the same times (x - max) c. The sums of a row are held in 64 bits: beside a
 // confident word, which is 1, the others are far below 2^-24 each, and their mass is what its log probability says. In 32
@@ -654,7 +668,7 @@ __global__ __launch_bounds__(THREADS) void logprob_grad_kernel(LogprobGradArgs a
 }
 
 int slices_of(int64_t T, int64_t V) {
-  if (V <= (T >= kManyRows ? 2 * kWholeRow : kWholeRow) || T < 1) return 1;
+  if (T < 1 || T >= kMostCut || V <= kWholeRow + kWholeRowMore * T) return 1;
   const int64_t want = std::max<int64_t>(1, std::min<int64_t>(kSliceTarget / T, kMaxSlices));
   const int64_t slice = ((V + want - 1) / want + kSliceStep - 1) / kSliceStep * kSliceStep;
   return (int)((V + slice - 1) / slice);
@@ -701,7 +715,7 @@ hipError_t launch_grad_types(const LogprobGradArgs& a, hipStream_t s) {
 
 // Never less for more rows, though many rows are not cut: up to kSliceTarget slices in all
 int64_t logprob_workspace_bytes(int64_t T, int64_t V, int top_n) {
-  if (V <= kWholeRow || T < 1) return 0;
+  if (T < 1 || V <= kWholeRow + kWholeRowMore) return 0;
   return std::min<int64_t>(T * kMaxSlices, kSliceTarget) * slice_bytes(top_n);
 }
 int64_t logprob_workspace_used(int64_t T, int64_t V, int top_n) {

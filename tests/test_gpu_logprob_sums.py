@@ -10,7 +10,7 @@ torch = pytest.importorskip("torch")
 
 import moe_expert_offload_gemv_amd as moe  # noqa: E402
 from tests.test_gpu_dense_ops import TYPES, E, rng_of  # noqa: E402
-from tests.test_gpu_logprobs import Out  # noqa: E402
+from tests.test_gpu_logprobs import INF, Out, check  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 
@@ -23,7 +23,7 @@ WORD = 1.3 * 18 + 2 + 8 + 15
 PEAK = 8.1
 
 
-# uncut rows by one wave and by four; cut; many rows, uncut; long and uncut (from 513 rows on nothing is)
+# uncut rows by one wave and by four; cut; many rows, uncut; long, cut and uncut (from 384 rows on nothing is)
 @pytest.mark.parametrize("T,V", [(3, 2000), (3, 32768), (2, 65537), (260, 65536), (1, 1 << 22), (520, 1 << 20)])
 @pytest.mark.parametrize("where", ["first", "middle", "last"])
 @pytest.mark.parametrize("zt", ["f32", "bf16"])
@@ -101,3 +101,31 @@ def test_a_row_that_is_not_cut_needs_no_workspace():
         assert torch.equal(got, want)
     with pytest.raises(ValueError, match="workspace"):
         moe.moe_token_logprobs(z[:5], entropy=got[:5].clone(), stream=side)
+
+
+@pytest.mark.parametrize("T,n,V", [(1, 0, 33068), (2, 32, 33368), (60, 9, 50768), (255, 0, 109268), (256, 2, 109568), (383, 0, 147668),
+                                   (384, 1, 147968)])
+def test_rows_about_as_long_as_are_not_cut(T, n, V):
+    """One logit more is another form of the same row, to its roundings; so is a workspace of more rows and alternatives."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(T + V)
+    ws = torch.full((moe.moe_token_logprobs_workspace_bytes(400, V + 1, 32),), 255, dtype=torch.uint8, device="cuda")
+    assert len(ws) >= moe.moe_token_logprobs_workspace_bytes(T, V + 1, n)
+    whole = (3 * torch.randn((T, V + 1), generator=g, device="cuda")).bfloat16()
+    whole[:, V] = -INF  # the word more
+    targets = torch.randint(0, V, (T,), generator=g, device="cuda", dtype=torch.int32)
+    outs = []
+    for z in (whole[:, :V], whole):
+        o = Out(T, z.shape[1], n, z)
+        moe.moe_token_logprobs(z, targets=targets, logp=o.logp, entropy=o.entropy, lse=o.lse, workspace=ws,
+                               **({"top_ids": o.ids, "top_logp": o.alt} if n else {}))
+        check(z[:8], targets[:8], 1.0, n, _first(o, 8))
+        outs.append(o)
+    assert torch.equal(outs[0].ids, outs[1].ids)
+    assert (outs[0].lse.double().sum(dim=1) - outs[1].lse.double().sum(dim=1)).abs().max() <= 2 * (1.3 * 18 + 2 + 8 + 3 * 24) * E
+
+
+def _first(o, rows):
+    f = Out.__new__(Out)
+    f.logp, f.entropy, f.lse, f.ids, f.alt = (t[:rows] for t in o.all())
+    return f
