@@ -241,48 +241,61 @@ __device__ __forceinline__ float wave_max(float v) {
   return fmaxf(fmaxf(a, b), fmaxf(c, d));
 }
 
-// The same over the candidates, PER of them in a lane: every wave finds it for itself
-template <int PER>
-__device__ __forceinline__ uint32_t nth_of_candidates(const Candidate* s_c, int count, int n) {
-  uint32_t key[PER], bound = 0;
-  const int lane = threadIdx.x & 63;
-#pragma unroll
-  for (int i = 0; i < PER; ++i) key[i] = lane + 64 * i < count ? s_c[lane + 64 * i].key : 0u;
-#pragma unroll 1
-  for (uint32_t bit = 1u << 31; bit >= 1u << 12; bit >>= 1) {
-    int many = 0;
-#pragma unroll
-    for (int i = 0; i < PER; ++i) many += __popcll(__ballot(key[i] >= (bound | bit)));
-    if (many >= n) bound |= bit;
-  }
-  return bound;
-}
 // The top_n best of `count` candidates, ranked. Counting takes their number squared: more than a few are
-// first cut to those that reach the top_n-th key (64 x 131072 with 32 alternatives, slices of 8192: 21.5 us
+// first cut to a few that have the best among them (64 x 131072 with 32 alternatives, slices of 8192: 21.5 us
 // and 15.4).
 constexpr int kFew = 64;
 struct Few {
   Candidate c[kFew];
   int n;
 };
-template <int THREADS, typename F>
+// The least candidate of such a few, by key, then by the higher id: bits of the key until those that reach it are few,
+// and where equal keys are too many for that, bits of the id. PER candidates lie in a lane; every wave finds it for itself.
+template <int PER>
+__device__ __forceinline__ Candidate least_of_few(const Candidate* s_c, int count, int top_n) {
+  const int lane = threadIdx.x & 63;
+  uint32_t key[PER];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) key[i] = lane + 64 * i < count ? s_c[lane + 64 * i].key : 0u;
+  Candidate least{0u, 0x7FFFFFFF};
+  int reached = count;
+#pragma unroll 1
+  for (uint32_t bit = 1u << 31; bit && reached > kFew; bit >>= 1) {
+    int many = 0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) many += __popcll(__ballot(key[i] >= (least.key | bit)));
+    if (many >= top_n) least.key |= bit, reached = many;
+  }
+  if (reached <= kFew) return least;
+  int id[PER], missing = top_n;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    missing -= __popcll(__ballot(key[i] > least.key));
+    id[i] = key[i] == least.key ? s_c[lane + 64 * i].id : 0x7FFFFFFF;
+  }
+  least.id = (1 << 22) - 1;  // no id is above
+#pragma unroll 1
+  for (int bit = 1 << 21; bit; bit >>= 1) {
+    int many = 0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) many += __popcll(__ballot(id[i] <= least.id - bit));
+    if (many >= missing) least.id -= bit;
+  }
+  return least;
+}
+template <int THREADS, int MOST, typename F>
 __device__ __forceinline__ void rank_top(const Candidate* s_c, int count, int top_n, Few& s_few, F f) {
   if (count > kFew) {
-    const uint32_t bound = count <= 256 ? nth_of_candidates<4>(s_c, count, top_n) : 0u;
+    const Candidate least = count <= 256 ? least_of_few<4>(s_c, count, top_n) : least_of_few<MOST / 64>(s_c, count, top_n);
     if (threadIdx.x == 0) s_few.n = 0;
     __syncthreads();
 #pragma unroll 1
     for (int i = threadIdx.x; i < count; i += THREADS) {
       const Candidate me = s_c[i];
-      if (me.key < bound) continue;
-      const int at = atomicAdd(&s_few.n, 1);
-      if (at < kFew) s_few.c[at] = me;
+      if (me.key > least.key || (me.key == least.key && me.id <= least.id)) s_few.c[atomicAdd(&s_few.n, 1)] = me;
     }
     __syncthreads();
-    if (s_few.n <= kFew) {
-      rank_candidates<THREADS>(s_few.c, s_few.n, f);
-      return;
-    }
+    s_c = s_few.c, count = s_few.n;
   }
   rank_candidates<THREADS>(s_c, count, f);
 }
@@ -514,7 +527,7 @@ __global__ __launch_bounds__(THREADS, TOP ? 4 : ZT == MOE_F32 ? 6 : 8) void logp
       // the same for the whole work-group
       const bool none = r.bad || (a.slices == 1 && r.none);
       const int count = none ? 0 : find_top<ZT, THREADS>(s_top, z, begin, end, most, a.top_n, iters, a.note_log);
-      rank_top<THREADS>(s_top.c, count, a.top_n, s_top.few, [&](const Candidate& me, int rank) {
+      rank_top<THREADS, Top<THREADS>::kCand>(s_top.c, count, a.top_n, s_top.few, [&](const Candidate& me, int rank) {
         if (rank >= a.top_n) return;
         const float x = route_dev::order_logit(me.key);
         ids[rank] = me.id;
@@ -576,7 +589,7 @@ __global__ __launch_bounds__(kFinish) void logprob_finish_kernel(LogprobArgs a) 
   }
   __syncthreads();
   const int count = s_n;
-  rank_top<kFinish>(s_c, count, a.top_n, s_few, [&](const Candidate& me, int rank) {
+  rank_top<kFinish, kCand>(s_c, count, a.top_n, s_few, [&](const Candidate& me, int rank) {
     if (rank >= a.top_n) return;
     a.top_ids[row * a.top_n + rank] = me.id;
     a.top_logp[row * a.top_n + rank] = row_logp(r, route_dev::order_logit(me.key), a.scale);

@@ -129,3 +129,22 @@ def _first(o, rows):
     f = Out.__new__(Out)
     f.logp, f.entropy, f.lse, f.ids, f.alt = (t[:rows] for t in o.all())
     return f
+
+
+@pytest.mark.parametrize("T,V,step", [(1, 131072, 2048), (4, 70000, 2048), (3, 20000, 20000)])
+def test_many_candidates_close_together(T, V, step):
+    """More than 256 values within the 16 bits of a bound, distinct, in every other slice (or anywhere in a row that is not cut)."""
+    g = rng_of(62, T, V)
+    n = 32
+    z = torch.from_numpy(g.standard_normal((T, V)) - 5).float().cuda()
+    for t in range(T):
+        for at in range(0, V - step + 1, 2 * step):
+            many = 32 if step < V else 700
+            z[t, at + torch.from_numpy(g.permutation(step)[:many]).cuda()] = torch.from_numpy(10 + 0.06 * g.random(many)).float().cuda()
+    o = Out(T, V, n, z)
+    moe.moe_token_logprobs(z, top_ids=o.ids, top_logp=o.alt, workspace=o.ws)
+    ids = torch.sort(z, dim=1, descending=True, stable=True).indices[:, :n]
+    assert torch.equal(o.ids.long(), ids)
+    lp = torch.log_softmax(z.double(), dim=1).gather(1, ids)
+    # the best lie within 0.06 of each other: their own differences are nearly exact, the sum's roundings as in any row
+    assert ((o.alt.double() - lp).abs() <= 100 * E).all()
