@@ -374,12 +374,8 @@ __device__ int find_top(Top<THREADS>& s, const char* row, int begin, int end, fl
       above = true;
       continue;
     }
-    // still: the top_n-th largest of those that found room is a higher bound
-    rank_candidates<THREADS>(s.c, Top<THREADS>::kCand, [&](const Candidate& me, int rank) {
-      if (rank == top_n - 1) s.bound[0] = me.key;
-    });
-    __syncthreads();
-    t = s.bound[0];
+    // still: a key that top_n of those that found room reach, but few, is a higher bound
+    t = least_of_few<Top<THREADS>::kCand / 64>(s.c, Top<THREADS>::kCand, top_n).key;
     above = false;
   }
   if (!above) return count;
