@@ -625,8 +625,9 @@ MOE_API int64_t moe_qk_norm_rope_grad_workspace_bytes(int32_t n_tokens, int32_t 
  *   top_ids[t], top_logp[t] = the top_n largest logits above -inf, in descending
  *                order, ties to the lower id, and their log p; where there are
  *                fewer, ids -1 and log p -inf
- * all in one read of the logits. lse is fp32 [n_tokens][2], a value and what its
- * rounding left out, for the gradient. Logits of -inf (words that a grammar leaves
+ * all in one read of the logits, powers in fp32 and their sums in 64 bits, so that a
+ * word of p near 1 has the mass of the others for its log p. lse is fp32 [n_tokens][2], a
+ * value and what its rounding left out, for the gradient. Logits of -inf (words that a grammar leaves
  * out) have p = 0; a row of nothing else has lse and logp -inf, entropy 0 and no
  * top ids, and so has a row whose z are all below fp32's range. A row with a NaN or
  * +inf (z past fp32's range) has NaN for all of them, and ids -1.

@@ -12,7 +12,7 @@
 //
 // Measured (as nodes of a graph): 4096 x 36 heads of 128 bf16, 75 MB, 14.6-15 us = 5.1 TB/s, a copy's rate
 // (2 rows a group and no loads ahead 16.7, 4 rows at once 18.4); 12287 x 16 heads of 80 fp16, three axes, 63 MB,
-// 17.4 = 3.6 TB/s (10 of 16 lanes have values, and 2.3e5 instructions a SIMD are 15 of it); one token,
+// 17.3 = 3.6 TB/s (10 of 16 lanes have values, and 2.3e5 instructions a SIMD are 15 of it); one token,
 // 18 heads of 128 fp32, 3.2: a launch, two trips to memory and the angles between.
 #include <hip/hip_runtime.h>
 #include <stdint.h>

@@ -9,8 +9,9 @@
 // its share of the rows and keeps its sum of dweight in registers, then in the workspace;
 // heads_dweight_kernel adds the work-groups' shares in a fixed order.
 //
-// Measured: 4096 x 36 heads of 128 bf16, 113 MB, 29.6 us = 3.8 TB/s, and 3.9 for the shares; 4096 x 32 of 128 fp32, 201 MB,
-// 46 together = 4.4 TB/s: two streams read and one written.
+// Measured: 4096 x 36 heads of 128 bf16, 113 MB, 28.8 us = 3.9 TB/s, and 3.9 for the shares; 4096 x 32 of 128 fp32, 201 MB,
+// 46 together, 42 = 4.8 TB/s without the shares. The streams are the same; a lane of 16-bit heads has 32 bytes on their way,
+// one of fp32 64, and 16 waves a CU are too few for the former.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 

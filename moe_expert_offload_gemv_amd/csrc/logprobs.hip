@@ -8,22 +8,24 @@
 //   logprob_grad_kernel    logits once more: dlogits
 //
 // Bound by traffic, one read of the logits: a thread keeps a running maximum and both sums
-// over 16 values at a time, the next 16 on their way, in powers of two; 12 issue slots a value of which the
+// over 16 values at a time, the next 16 on their way, in powers of two; 11 issue slots a value of which the
 // power takes four, so that 16-bit logits are nearly as long in the vector unit as on their way. Rows are cut
-// into slices, if they are long, while all of them fit on the chip at once.
+// into slices, if they are long and few, while all of them fit on the chip at once.
 //
 // The top_n largest come out of the same read. A thread also notes the largest of its values in LDS.
 // The top_n-th largest of the threads' maxima is a bound that top_n values reach at least (taken in
 // each wave, and the best wave's); the few runs whose largest reaches it are read again, from
-// cache, and what reaches it in them, about two or three times top_n values, is ranked by counting. Equal
+// cache, and what reaches it in them, about two or three times top_n values, is ranked by counting; more, where values
+// lie close together or far from zero, are cut to a few by their bits first. Equal
 // values: a token's rank counts equal ones of lower id, so ties go to the lower id whatever
 // the order in which the values were found.
 //
-// Measured (as nodes of a graph): 4096 x 65537 bf16, 537 MB, 124 us = 4.3 TB/s, with its gradient, 1074 MB more, 313 = 5.1
-// TB/s; 4096 x 32000 fp32 90 = 5.8 TB/s; 301 x 131072 bf16 with 8 alternatives 26.5 (floor 15: finding them takes 5, the
-// finishing launch 5); 4096 x 8000 bf16 18, with 20 alternatives 40 (to find them is four times the work of the
-// sums there: a bound, a second look and ranks for 8000 values); 1 x 65537 fp32 with 20, 12.6: two launches of a few dependent
-// trips to memory and LDS each, 5.4 without alternatives.
+// Measured (as nodes of a graph): 4096 x 65537 bf16, 537 MB, 122 us = 4.4 TB/s, with its gradient, 1074 MB more, 311 = 5.2
+// TB/s; 4096 x 32000 fp32 93 = 5.6 TB/s; 301 x 131072 bf16 with 8 alternatives 27.7 (floor 15: finding them takes 5, the
+// finishing launch 5); 4096 x 8000 bf16 18.6, with 20 alternatives 39.7 (to find them is four times the work of the
+// sums there: a bound, a second look and ranks for 8000 values); 1 x 65537 fp32 with 20, 12.5: two launches of a few dependent
+// trips to memory and LDS each, 5.5 without alternatives; around 1000 instead of 0, 2000 x 8000 fp32 with 20 takes 67 and
+// 32 x 32000 62, for the bound's 16 bits then tell little apart.
 // Measured and not kept: the search by one wave of the work-group (1 x 65537 with 20: 18); an atomic for all hits of
 // a thread at once (4096 x 8000: 55 against 45, the compiler's scan over the lanes); loads past the caches (4096 x 32000
 // fp32 97 against 91).
